@@ -9,26 +9,24 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
-#include <string>
 
 #include "gdn.h"
+#include "gdn_check.h"
 #include "gdn_internal.h"
 
-namespace {
+namespace gdn {
 
-thread_local std::string g_last_error;
+static thread_local char g_last_error[512] = "";
+
+void clear_error() { g_last_error[0] = '\0'; }
 
 gdn_status fail(gdn_status st, const char* fmt, ...) {
-    char buf[512];
     va_list ap;
     va_start(ap, fmt);
-    vsnprintf(buf, sizeof(buf), fmt, ap);
+    vsnprintf(g_last_error, sizeof(g_last_error), fmt, ap);
     va_end(ap);
-    g_last_error = buf;
     return st;
 }
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 gdn_status check_shape(const gdn_shape* s) {
     if (!s) return fail(GDN_ERR_INVALID_ARGUMENT, "shape is NULL");
@@ -49,12 +47,6 @@ gdn_status check_shape(const gdn_shape* s) {
     return GDN_OK;
 }
 
-struct Ptr {
-    const char* name;
-    const void* p;
-    size_t align;
-};
-
 gdn_status check_ptrs(std::initializer_list<Ptr> ps) {
     for (const Ptr& x : ps) {
         if (!x.p) return fail(GDN_ERR_INVALID_ARGUMENT, "%s is NULL", x.name);
@@ -68,6 +60,16 @@ gdn_status hip_status(hipError_t e, const char* what) {
     if (e == hipSuccess) return GDN_OK;
     return fail(GDN_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
+
+}  // namespace gdn
+
+namespace {
+
+using gdn::aligned;
+using gdn::check_ptrs;
+using gdn::check_shape;
+using gdn::fail;
+using gdn::hip_status;
 
 gdn_status check_decode(const gdn_shape* shape, int32_t num_rows, const void* q, const void* k,
                         const void* v, const float* g, const float* beta, void* o,
@@ -223,7 +225,7 @@ gdn_status gdn_recurrent_decode(const gdn_shape* shape, int32_t num_rows, const 
                                 const void* v, const float* g, const float* beta, void* o,
                                 float* state_pool, int32_t num_slots, const int32_t* slot_in,
                                 const int32_t* slot_out, hipStream_t stream) {
-    g_last_error.clear();
+    gdn::clear_error();
     gdn_status st = check_decode(shape, num_rows, q, k, v, g, beta, o, state_pool, num_slots, slot_in,
                                  slot_out);
     if (st != GDN_OK || num_rows == 0) return st;
@@ -241,7 +243,7 @@ gdn_status gdn_chunk_prefill(const gdn_shape* shape, int32_t num_seqs, int64_t t
                              const int32_t* export_offsets, const int32_t* export_slots,
                              int64_t num_export_states, void* workspace, size_t workspace_bytes,
                              hipStream_t stream) {
-    g_last_error.clear();
+    gdn::clear_error();
     gdn_status st = check_prefill(shape, num_seqs, total_tokens, cu_seqlens, q, k, v, g, beta, o,
                                   state_pool, num_slots, init_slot, final_slot, start_pos, export_grid,
                                   export_states, export_offsets, export_slots, num_export_states,
@@ -264,7 +266,7 @@ gdn_status gdn_mixed_step(const gdn_shape* shape, int32_t num_decode_rows, const
                           int32_t export_grid, float* export_states, const int32_t* export_offsets,
                           const int32_t* export_slots, int64_t num_export_states, void* workspace,
                           size_t workspace_bytes, hipStream_t stream) {
-    g_last_error.clear();
+    gdn::clear_error();
     gdn_status st = check_decode(shape, num_decode_rows, q, k, v, g, beta, o, state_pool, num_slots,
                                  slot_in, slot_out);
     if (st != GDN_OK) return st;
@@ -303,7 +305,7 @@ gdn_status gdn_recurrent_verify(const gdn_shape* shape, int32_t num_rows, int32_
                                 const void* q, const void* k, const void* v, const float* g, const float* beta,
                                 void* o, float* state_pool, int32_t num_slots, const int32_t* slot_in,
                                 const int32_t* token_slots, hipStream_t stream) {
-    g_last_error.clear();
+    gdn::clear_error();
     if (tokens_per_row < 1)
         return fail(GDN_ERR_INVALID_ARGUMENT, "tokens_per_row %d is less than 1", tokens_per_row);
     if ((int64_t)num_rows * tokens_per_row > 0x7fffffffLL)
@@ -317,6 +319,6 @@ gdn_status gdn_recurrent_verify(const gdn_shape* shape, int32_t num_rows, int32_
     return hip_status(gdn::launch_decode(a, stream), "verify launch");
 }
 
-const char* gdn_last_error(void) { return g_last_error.c_str(); }
+const char* gdn_last_error(void) { return gdn::g_last_error; }
 
 }  // extern "C"
