@@ -3,8 +3,12 @@
 //     gated:     y = rms(x) w act(z)  or  rms(x act(z)) w,   rms(v) = v / sqrt(mean(v^2) + eps)
 //     residual:  r' = r + s act(gate) (rms(x) w_post),  y = rms(r') w_pre
 //
-// Memory-bound.  One workgroup per row (or per group of a row); a row's squares are
-// summed per thread, then over the wave and the four waves in a fixed order.
+// Memory-bound: every operand crosses HBM once.  The values of a norm stay in registers
+// between its sum and its output; TPG threads share one norm, R vectors of V elements each,
+// as many vectors as its dim needs: 16 lanes for short norms (four to a wave), one wave,
+// then one workgroup of four or sixteen waves.  A sum is taken per thread in order, then
+// over the lanes and the waves in a fixed tree, so a row's bits depend on its dim and
+// alignment alone.
 #include <hip/hip_runtime.h>
 
 #include "gdn_layer_device.h"
@@ -15,84 +19,276 @@ namespace {
 
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ float gate_of(float z, int activation) {
-    return activation == 1 ? dev::silu(z) : activation == 2 ? dev::sigmoid(z) : z;
+template <typename T, int V>
+__device__ __forceinline__ void load_some(const T* p, float (&v)[V]) {
+    if constexpr (V == 1) v[0] = (float)*p;
+    else if constexpr (V * sizeof(T) == 16) dev::load_vec(p, v);
+    else dev::load_floats(p, v);
 }
 
-__device__ __forceinline__ float block_sum(float x, float* sums) {
+template <typename T, int V>
+__device__ __forceinline__ void store_some(T* p, const float (&v)[V]) {
+    if constexpr (V == 1) {
+        *p = (T)v[0];
+    } else if constexpr (V * sizeof(T) == 16) {
+        dev::store_vec(p, v);
+    } else {
 #pragma unroll
-    for (int d = 32; d > 0; d >>= 1) x += __shfl_xor(x, d);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = x;
-    __syncthreads();
-    return (sums[0] + sums[1]) + (sums[2] + sums[3]);
+        for (int i = 0; i < V; i += 4) {
+            const float q[4] = {v[i], v[i + 1], v[i + 2], v[i + 3]};
+            dev::store_vec(p + i, q);
+        }
+    }
+}
+
+// V elements of T as values, v[] = q[] once the loads may be rounded to T in between
+template <typename T, int V>
+__device__ __forceinline__ void round_to(float (&v)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = (float)(T)v[i];
+}
+
+template <int V>
+__device__ __forceinline__ void gate(float (&z)[V], int activation) {
+    if (activation == 1)
+#pragma unroll
+        for (int i = 0; i < V; ++i) z[i] = dev::silu(z[i]);
+    else if (activation == 2)
+#pragma unroll
+        for (int i = 0; i < V; ++i) z[i] = dev::sigmoid(z[i]);
+}
+
+// Sum over the TPG threads of a norm.
+template <int TPG>
+__device__ __forceinline__ float norm_sum(float x, float* sums) {
+    if constexpr (TPG <= 64) {
+        return dev::group_sum(x, TPG);
+    } else {
+        x = dev::group_sum(x, 64);
+        __syncthreads();
+        if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = x;
+        __syncthreads();
+        float t[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < TPG / 64; ++w) t[w & 3] += sums[w];
+        return (t[0] + t[1]) + (t[2] + t[3]);
+    }
+}
+
+// U norms per thread, all of their loads issued first.
+template <typename T, int V, int TPG, int R, int U>
+__global__ __launch_bounds__(TPG > kThreads ? TPG : kThreads) void gated_norm_kernel(GatedNormArgs a) {
+    constexpr int PER = TPG > kThreads ? 1 : kThreads / TPG;
+    __shared__ float sums[TPG > 64 ? TPG / 64 : 1];
+    const unsigned total = (unsigned)(a.num_rows * a.groups);
+    const int lane = threadIdx.x % TPG;
+    const float inv_dim = 1.f / (float)a.dim;
+    float x[U][R][V], z[U][R][V];
+    unsigned idx[U], g[U];
+    int64_t row[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        idx[u] = (blockIdx.x * U + u) * PER + threadIdx.x / TPG;
+        row[u] = idx[u] / (unsigned)a.groups;
+        g[u] = idx[u] - (unsigned)row[u] * (unsigned)a.groups;
+        const T* px = static_cast<const T*>(a.x) + row[u] * a.x_stride + (size_t)g[u] * a.dim;
+        const T* pz = static_cast<const T*>(a.z) + row[u] * a.z_stride + (size_t)g[u] * a.dim;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int e = (lane + r * TPG) * V;
+            if (idx[u] < total && e < a.dim) {
+                load_some(px + e, x[u][r]);
+                if (a.z) load_some(pz + e, z[u][r]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) x[u][r][i] = z[u][r][i] = 0.f;
+            }
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (a.z) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                gate(z[u][r], a.activation);
+                if (a.gate_first)
+#pragma unroll
+                    for (int i = 0; i < V; ++i) x[u][r][i] *= z[u][r][i];
+            }
+        }
+        float s = 0.f;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int i = 0; i < V; ++i) s = fmaf(x[u][r][i], x[u][r][i], s);
+        const float n = dev::inv_sqrt(fmaf(norm_sum<TPG>(s, sums), inv_dim, a.eps));
+        const float* pw = a.weight + (a.weight_per_group ? (size_t)g[u] * a.dim : 0);
+        T* py = static_cast<T*>(a.y) + ((size_t)row[u] * a.groups + g[u]) * a.dim;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int e = (lane + r * TPG) * V;
+            if (idx[u] < total && e < a.dim) {
+                float w[V];
+                load_some(pw + e, w);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    w[i] *= x[u][r][i] * n;
+                    if (a.z && !a.gate_first) w[i] *= z[u][r][i];
+                }
+                store_some(py + e, w);
+            }
+        }
+    }
+}
+
+template <typename T, typename RT, int V, int TPG, int R>
+__global__ __launch_bounds__(TPG > kThreads ? TPG : kThreads) void residual_norm_kernel(ResidualNormArgs a) {
+    constexpr int PER = TPG > kThreads ? 1 : kThreads / TPG;
+    __shared__ float sums[TPG > 64 ? TPG / 64 : 1];
+    const int64_t row = (int64_t)blockIdx.x * PER + threadIdx.x / TPG;
+    const int lane = threadIdx.x % TPG;
+    const bool live = row < a.num_rows;
+    const float inv_dim = 1.f / (float)a.dim;
+    const T* px = static_cast<const T*>(a.x) + row * a.x_stride;
+    const T* pz = static_cast<const T*>(a.gate) + row * a.gate_stride;
+    const RT* pr = static_cast<const RT*>(a.residual) + (size_t)row * a.dim;
+    RT* po = static_cast<RT*>(a.residual_out) + (size_t)row * a.dim;
+    float x[R][V], q[R][V], z[R][V];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int e = (lane + r * TPG) * V;
+        if (live && e < a.dim) {
+            load_some(px + e, x[r]);
+            load_some(pr + e, q[r]);
+            if (a.gate) load_some(pz + e, z[r]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) x[r][i] = q[r][i] = z[r][i] = 0.f;
+        }
+    }
+    if (a.post_weight) {
+        float s = 0.f;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int i = 0; i < V; ++i) s = fmaf(x[r][i], x[r][i], s);
+        const float n = dev::inv_sqrt(fmaf(norm_sum<TPG>(s, sums), inv_dim, a.eps));
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int e = (lane + r * TPG) * V;
+            if (e < a.dim) {
+                float w[V];
+                load_some(a.post_weight + e, w);
+#pragma unroll
+                for (int i = 0; i < V; ++i) x[r][i] *= n * w[i];
+            }
+        }
+    }
+    float s = 0.f;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int e = (lane + r * TPG) * V;
+        if (a.gate) {
+            gate(z[r], a.activation);
+#pragma unroll
+            for (int i = 0; i < V; ++i) x[r][i] *= z[r][i];
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) q[r][i] = fmaf(a.residual_scale, x[r][i], q[r][i]);
+        round_to<RT>(q[r]);
+        if (live && e < a.dim) {
+            store_some(po + e, q[r]);
+#pragma unroll
+            for (int i = 0; i < V; ++i) s = fmaf(q[r][i], q[r][i], s);
+        }
+    }
+    if (!a.y) return;
+    const float n = dev::inv_sqrt(fmaf(norm_sum<TPG>(s, sums), inv_dim, a.eps));
+    T* py = static_cast<T*>(a.y) + (size_t)row * a.dim;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int e = (lane + r * TPG) * V;
+        if (live && e < a.dim) {
+            float w[V];
+            load_some(a.pre_weight + e, w);
+#pragma unroll
+            for (int i = 0; i < V; ++i) w[i] *= q[r][i] * n;
+            store_some(py + e, w);
+        }
+    }
+}
+
+template <typename T, int V, int TPG, int R>
+void gated(const GatedNormArgs& a, hipStream_t stream) {
+    constexpr int PER = TPG > kThreads ? 1 : kThreads / TPG, THREADS = TPG > kThreads ? TPG : kThreads;
+    const int64_t n = (a.num_rows * a.groups + PER - 1) / PER;
+    hipLaunchKernelGGL((gated_norm_kernel<T, V, TPG, R, 1>), dim3((unsigned)n), dim3(THREADS), 0, stream, a);
+}
+
+// Threads and vectors by the number of vectors in a norm: the smallest that holds it.
+template <typename T, int V>
+void gated_by_dim(const GatedNormArgs& a, hipStream_t stream) {
+    const int n = (a.dim + V - 1) / V;
+    if (n <= 16) gated<T, V, 16, 1>(a, stream);
+    else if (n <= 64) gated<T, V, 64, 1>(a, stream);
+    else if (n <= 256) gated<T, V, 64, 4>(a, stream);
+    else if (n <= 1024) gated<T, V, 256, 4>(a, stream);
+    else gated<T, V, 1024, V == 1 ? 16 : 4>(a, stream);
+}
+
+template <typename T, typename RT, int V, int TPG, int R>
+void residual(const ResidualNormArgs& a, hipStream_t stream) {
+    constexpr int PER = TPG > kThreads ? 1 : kThreads / TPG, THREADS = TPG > kThreads ? TPG : kThreads;
+    const int64_t n = (a.num_rows + PER - 1) / PER;
+    hipLaunchKernelGGL((residual_norm_kernel<T, RT, V, TPG, R>), dim3((unsigned)n), dim3(THREADS), 0, stream, a);
+}
+
+template <typename T, typename RT, int V>
+void residual_by_dim(const ResidualNormArgs& a, hipStream_t stream) {
+    const int n = (a.dim + V - 1) / V;
+    if (n <= 64) residual<T, RT, V, 64, 1>(a, stream);
+    else if (n <= 256) residual<T, RT, V, 256, 1>(a, stream);
+    else if (n <= 512) residual<T, RT, V, 256, 2>(a, stream);
+    else if (n <= 1024) residual<T, RT, V, 256, 4>(a, stream);
+    else residual<T, RT, V, 1024, V == 1 ? 16 : 4>(a, stream);
+}
+
+// Whether rows of `dim` elements at this address and row stride can be read in 16-byte vectors.
+bool wide(const void* p, int64_t stride, int64_t rows, int dim, size_t size) {
+    const size_t v = 16 / size;
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && dim % v == 0 && (rows == 1 || stride % v == 0);
+}
+
+template <typename T, typename RT>
+void residual_typed(const ResidualNormArgs& a, hipStream_t stream) {
+    const bool ok = wide(a.x, a.x_stride, a.num_rows, a.dim, sizeof(T)) && wide(a.residual, a.dim, 1, a.dim, sizeof(T)) &&
+                    wide(a.residual_out, a.dim, 1, a.dim, sizeof(T)) && (!a.y || wide(a.y, a.dim, 1, a.dim, sizeof(T))) &&
+                    (!a.gate || wide(a.gate, a.gate_stride, a.num_rows, a.dim, sizeof(T))) &&
+                    reinterpret_cast<uintptr_t>(a.post_weight) % 16 == 0 && reinterpret_cast<uintptr_t>(a.pre_weight) % 16 == 0;
+    if (ok) residual_by_dim<T, RT, dev::kVec<T>>(a, stream);
+    else residual_by_dim<T, RT, 1>(a, stream);
 }
 
 template <typename T>
-__global__ __launch_bounds__(kThreads) void gated_norm_kernel(GatedNormArgs a) {
-    __shared__ float sums[kThreads / 64];
-    const int64_t row = blockIdx.x / a.groups;
-    const int g = (int)(blockIdx.x - row * a.groups);
-    const T* x = static_cast<const T*>(a.x) + row * a.x_stride + (size_t)g * a.dim;
-    const T* z = a.z ? static_cast<const T*>(a.z) + row * a.z_stride + (size_t)g * a.dim : nullptr;
-    const float* w = a.weight + (a.weight_per_group ? (size_t)g * a.dim : 0);
-    T* y = static_cast<T*>(a.y) + ((size_t)row * a.groups + g) * a.dim;
-    float s = 0.f;
-    for (int i = threadIdx.x; i < a.dim; i += kThreads) {
-        float v = (float)x[i];
-        if (a.gate_first && z) v *= gate_of((float)z[i], a.activation);
-        s = fmaf(v, v, s);
-    }
-    const float r = 1.f / sqrtf(block_sum(s, sums) / a.dim + a.eps);
-    for (int i = threadIdx.x; i < a.dim; i += kThreads) {
-        const float gate = z ? gate_of((float)z[i], a.activation) : 1.f;
-        y[i] = (T)((float)x[i] * gate * r * w[i]);
-    }
-}
-
-template <typename T, typename R>
-__global__ __launch_bounds__(kThreads) void residual_norm_kernel(ResidualNormArgs a) {
-    __shared__ float sums[kThreads / 64];
-    const int64_t row = blockIdx.x;
-    const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
-    const T* z = a.gate ? static_cast<const T*>(a.gate) + row * a.gate_stride : nullptr;
-    const R* res = static_cast<const R*>(a.residual) + (size_t)row * a.dim;
-    R* out = static_cast<R*>(a.residual_out) + (size_t)row * a.dim;
-    float post = 1.f;
-    if (a.post_weight) {
-        float s = 0.f;
-        for (int i = threadIdx.x; i < a.dim; i += kThreads) s = fmaf((float)x[i], (float)x[i], s);
-        post = 1.f / sqrtf(block_sum(s, sums) / a.dim + a.eps);
-    }
-    float s = 0.f;
-    for (int i = threadIdx.x; i < a.dim; i += kThreads) {
-        float v = (float)x[i] * post;
-        if (a.post_weight) v *= a.post_weight[i];
-        if (z) v *= gate_of((float)z[i], a.activation);
-        const R o = (R)fmaf(a.residual_scale, v, (float)res[i]);
-        out[i] = o;
-        s = fmaf((float)o, (float)o, s);
-    }
-    if (!a.y) return;
-    const float pre = 1.f / sqrtf(block_sum(s, sums) / a.dim + a.eps);
-    T* y = static_cast<T*>(a.y) + (size_t)row * a.dim;
-    for (int i = threadIdx.x; i < a.dim; i += kThreads) y[i] = (T)((float)out[i] * pre * a.pre_weight[i]);
+void gated_typed(const GatedNormArgs& a, hipStream_t stream) {
+    const bool ok = wide(a.x, a.x_stride, a.num_rows, a.dim, sizeof(T)) && wide(a.y, a.dim, 1, a.dim, sizeof(T)) &&
+                    (!a.z || wide(a.z, a.z_stride, a.num_rows, a.dim, sizeof(T))) && reinterpret_cast<uintptr_t>(a.weight) % 16 == 0;
+    if (ok) gated_by_dim<T, dev::kVec<T>>(a, stream);
+    else gated_by_dim<T, 1>(a, stream);
 }
 
 }  // namespace
 
 hipError_t launch_gated_norm(const GatedNormArgs& a, hipStream_t stream) {
-    const dim3 grid((unsigned)(a.num_rows * a.groups));
-    if (a.dtype == 1) hipLaunchKernelGGL((gated_norm_kernel<__bf16>), grid, dim3(kThreads), 0, stream, a);
-    else hipLaunchKernelGGL((gated_norm_kernel<float>), grid, dim3(kThreads), 0, stream, a);
+    if (a.dtype == 1) gated_typed<__bf16>(a, stream);
+    else gated_typed<float>(a, stream);
     return hipGetLastError();
 }
 
 hipError_t launch_residual_norm(const ResidualNormArgs& a, hipStream_t stream) {
-    const dim3 grid((unsigned)a.num_rows);
-    if (a.dtype == 0) hipLaunchKernelGGL((residual_norm_kernel<float, float>), grid, dim3(kThreads), 0, stream, a);
-    else if (a.residual_dtype == 0) hipLaunchKernelGGL((residual_norm_kernel<__bf16, float>), grid, dim3(kThreads), 0, stream, a);
-    else hipLaunchKernelGGL((residual_norm_kernel<__bf16, __bf16>), grid, dim3(kThreads), 0, stream, a);
+    if (a.dtype == 0) residual_typed<float, float>(a, stream);
+    else if (a.residual_dtype == 0) residual_typed<__bf16, float>(a, stream);
+    else residual_typed<__bf16, __bf16>(a, stream);
     return hipGetLastError();
 }
 
