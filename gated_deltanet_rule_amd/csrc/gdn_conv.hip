@@ -2,14 +2,19 @@
 //
 //     a_t = bias + sum_{j < W} w_j x_{t - W + 1 + j},  u = silu(a),  y = u / sqrt(sum_head u^2 + eps)
 //
-// Memory-bound: every input is read and every output written once, two flops per tap in
-// between.  A thread owns one 16-byte vector of channels of one token; a head's sum of
-// squares is a butterfly over the lanes that hold it.  The states (the last W - 1 inputs)
-// are written by a second launch, so that a sequence resumed in place reads its old state
-// before it is replaced.
+// Memory-bound: every input is read and every output written once.  A lane owns one
+// 16-byte vector of channels, a wave 64 of them, and walks a tile of tokens with the last
+// W - 1 inputs and the weights in registers, so only the W - 1 rows before a tile are read
+// twice.  The inputs of the next kGroup tokens are in flight while kGroup are computed.  A
+// head's sum of squares goes over the lanes that hold it.
+//
+// A sequence's old state is read, and its final state written, by the tile that holds its
+// first token: that tile also takes the first W - 1 tokens where they reach beyond it, so
+// no other one reads the old state and a resume in place needs no second launch.
 #include <hip/hip_runtime.h>
 
 #include "gdn_device.h"
+#include "gdn_internal.h"
 #include "gdn_layer_device.h"
 #include "gdn_layer_internal.h"
 
@@ -17,57 +22,86 @@ namespace gdn {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+constexpr int kGroup = 4;
+constexpr int kTile = 32;     // most tokens of a tile
 
-// The run and its first channel of channel block cb: runs are cut into blocks of
-// kThreads vectors, each run's own, so that heads start at lane multiples.
+// Runs are cut into pieces of 64 vectors, each run's own, so that heads start at multiples
+// of their lanes.
 template <typename T>
-__device__ __forceinline__ bool channel_of(const ConvArgs& a, int cb, int& seg, int& ch, int& c) {
-    constexpr int W = kThreads * dev::kVec<T>;
-    int base = 0;
-    for (seg = 0; seg < 3; ++seg) {
-        const int n = (a.channels[seg] + W - 1) / W;
-        if (cb < n) break;
-        cb -= n;
-        base += a.channels[seg];
-    }
-    if (seg == 3) return false;
-    ch = cb * W + threadIdx.x * dev::kVec<T>;   // channel within the run
-    c = base + ch;                              // channel of x
-    return ch < a.channels[seg];
-}
-
-template <typename T>
-int channel_blocks(const ConvArgs& a) {
-    constexpr int W = kThreads * dev::kVec<T>;
+int pieces(const ConvArgs& a) {
+    constexpr int W = 64 * dev::kVec<T>;
     int n = 0;
     for (int i = 0; i < 3; ++i) n += (a.channels[i] + W - 1) / W;
     return n;
 }
 
-__device__ __forceinline__ int slot_or_none(const int32_t* slots, int i, int num_slots) {
+// Where a lane's channels are: the run, the channel within it, the channel of x.
+struct Channels {
+    int seg, ch, c;
+};
+
+template <typename T>
+__device__ __forceinline__ bool channels_of(const ConvArgs& a, int piece, Channels& w) {
+    constexpr int W = 64 * dev::kVec<T>;
+    int base = 0;
+    for (w.seg = 0; w.seg < 3; ++w.seg) {
+        const int n = (a.channels[w.seg] + W - 1) / W;
+        if (piece < n) break;
+        piece -= n;
+        base += a.channels[w.seg];
+    }
+    if (w.seg == 3) return false;
+    w.ch = piece * W + (threadIdx.x & 63) * dev::kVec<T>;
+    w.c = base + w.ch;
+    return w.ch < a.channels[w.seg];
+}
+
+__device__ __forceinline__ int slot_or_none(const int32_t* slots, int64_t i, int num_slots) {
     const int s = slots[i];
     return s >= 0 && s < num_slots ? s : -1;
 }
 
-// Activation and head norm of one vector.  The lanes of a head are consecutive and
-// either all active or all not.
-template <int V>
-__device__ __forceinline__ void finish(const ConvArgs& a, int seg, float (&u)[V]) {
-    if (a.silu)
-#pragma unroll
-        for (int i = 0; i < V; ++i) u[i] = dev::silu(u[i]);
-    if (a.l2_dim[seg] > 0) {
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) s = fmaf(u[i], u[i], s);
-        for (int d = a.l2_dim[seg] / V / 2; d > 0; d >>= 1) s += __shfl_xor(s, d);
-        const float r = 1.f / sqrtf(s + a.l2_eps);
-#pragma unroll
-        for (int i = 0; i < V; ++i) u[i] *= r;
-    }
-}
+// Weights and bias of a lane's channels, and the outputs from W inputs, oldest first.
+template <typename T, int W>
+struct Taps {
+    static constexpr int V = dev::kVec<T>;
+    float w[V * W], b[V];
 
-// Input at local position pos of a sequence (its state below 0), as fp32.
+    __device__ __forceinline__ void load(const ConvArgs& a, int c) {
+        dev::load_floats(a.weight + (size_t)c * W, w);
+        if (a.bias) {
+            dev::load_floats(a.bias + c, b);
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e) b[e] = 0.f;
+        }
+    }
+
+    // The lanes of a head are consecutive and either all active or all not.
+    __device__ __forceinline__ void apply(const ConvArgs& a, int l2_dim, const float (*in)[V], float (&u)[V]) const {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            u[e] = b[e];
+#pragma unroll
+            for (int j = 0; j < W; ++j) u[e] = fmaf(w[e * W + j], in[j][e], u[e]);
+        }
+        if (a.silu)
+#pragma unroll
+            for (int e = 0; e < V; ++e) u[e] = dev::silu(u[e]);
+        if (l2_dim > 0) {
+            float s = 0.f;
+#pragma unroll
+            for (int e = 0; e < V; ++e) s = fmaf(u[e], u[e], s);
+            const float r = dev::inv_sqrt(dev::group_sum(s, l2_dim / V) + a.l2_eps);
+#pragma unroll
+            for (int e = 0; e < V; ++e) u[e] *= r;
+        }
+    }
+};
+
+// Input at local position pos of a sequence, the state's rows below 0 (zeros without one).
+// At W = 4 a wave reads three of them where it enters a sequence.
 template <typename T, int W, int V>
 __device__ __forceinline__ void input_at(const ConvArgs& a, int64_t lo, int64_t pos, int slot, int c, float (&v)[V]) {
     if (pos >= 0) {
@@ -80,126 +114,143 @@ __device__ __forceinline__ void input_at(const ConvArgs& a, int64_t lo, int64_t 
     }
 }
 
+// The state before local position pos: the W - 1 inputs that end there.
 template <typename T, int W>
-__global__ __launch_bounds__(kThreads) void conv_kernel(ConvArgs a) {
+__device__ __forceinline__ void copy_state(const ConvArgs& a, T* dst, int64_t lo, int64_t pos, int slot, int c) {
+    float rows[W - 1][dev::kVec<T>];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) input_at<T, W>(a, lo, pos - (W - 1) + j, slot, c, rows[j]);
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) dev::store_vec(dst + (size_t)j * a.C + c, rows[j]);
+}
+
+// Where export idx goes, or NULL.
+template <typename T, int W>
+__device__ __forceinline__ T* export_to(const ConvArgs& a, int64_t idx) {
+    if (idx < 0 || idx >= a.export_capacity) return nullptr;
+    if (!a.export_slots) return static_cast<T*>(a.export_states) + (size_t)idx * (W - 1) * a.C;
+    const int s = slot_or_none(a.export_slots, idx, a.num_slots);
+    return s >= 0 ? static_cast<T*>(a.pool) + (size_t)s * (W - 1) * a.C : nullptr;
+}
+
+template <typename T, int W>
+__global__ __launch_bounds__(kThreads) void conv_prefill_kernel(ConvArgs a, int tile) {
     constexpr int V = dev::kVec<T>;
-    int seg, ch, c;
-    const bool live = channel_of<T>(a, blockIdx.y, seg, ch, c);
-    if (!live) return;
-    const int64_t t = blockIdx.x;
-    // the token's sequence: the last one that starts at or before it
-    int i, lo, len;
-    if (a.cu_seqlens) {
-        int l = 0, h = a.num_seqs - 1;
-        while (l < h) {
-            const int mid = (l + h + 1) >> 1;
-            if (a.cu_seqlens[mid] <= t) l = mid;
-            else h = mid - 1;
+    Channels w;
+    if (!channels_of<T>(a, blockIdx.y * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w)) return;
+    const int64_t t0 = (int64_t)blockIdx.x * tile, t1 = t0 + tile < a.total_tokens ? t0 + tile : a.total_tokens;
+    const bool last = blockIdx.x + 1 == gridDim.x;
+    Taps<T, W> taps;
+    if (a.total_tokens > 0) taps.load(a, w.c);
+    const int l2_dim = a.l2_dim[w.seg];
+    // the first sequence that starts at t0 or later
+    int i = 0;
+    {
+        int h = a.num_seqs;
+        while (i < h) {
+            const int mid = (i + h) >> 1;
+            if (a.cu_seqlens[mid] >= t0) h = mid;
+            else i = mid + 1;
         }
-        i = l;
-        dev::seq_range(a.cu_seqlens, i, a.total_tokens, lo, len);
-        if (t < lo || t >= lo + len) return;
-    } else {
-        i = lo = (int)t;
-        len = 1;
+        i = __builtin_amdgcn_readfirstlane(i);
     }
-    const int slot = slot_or_none(a.init_slot, i, a.num_slots);
-    T* y = static_cast<T*>(a.y[seg]) + (size_t)t * a.channels[seg] + ch;
-    float u[V];
-    if (!a.cu_seqlens && slot < 0) {            // padding row
+    // the sequence that is under way at t0, then those that start in this tile
+    for (i = i > 0 ? i - 1 : 0; i < a.num_seqs; ++i) {
+        int lo, len;
+        dev::seq_range(a.cu_seqlens, i, a.total_tokens, lo, len);
+        lo = __builtin_amdgcn_readfirstlane(lo);
+        len = __builtin_amdgcn_readfirstlane(len);
+        if (lo >= t1 && !last) break;
+        const bool owned = lo >= t0;
+        const int64_t hi = (int64_t)lo + len;
+        // local positions of this tile: an owned sequence's first W - 1 tokens are all its tile's
+        int64_t from = owned ? 0 : t0 - lo, to = (hi < t1 ? hi : t1) - lo;
+        if (!owned && from < W - 1) from = W - 1;
+        if (owned && to < W - 1) to = len < W - 1 ? len : W - 1;
+        const int slot = owned ? slot_or_none(a.init_slot, i, a.num_slots) : -1;
+        if (from < to) {
+            float in[W - 1 + kGroup][V], next[kGroup][V];
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) input_at<T, W>(a, lo, from - (W - 1) + j, slot, w.c, in[j]);
+            const T* x = static_cast<const T*>(a.x) + (size_t)lo * a.x_stride + w.c;
+            T* y = static_cast<T*>(a.y[w.seg]) + (size_t)lo * a.channels[w.seg] + w.ch;
+            auto fetch = [&](int64_t p) {
+#pragma unroll
+                for (int k = 0; k < kGroup; ++k)
+                    if (p + k < to) dev::load_vec(x + (size_t)(p + k) * a.x_stride, next[k]);
+            };
+            fetch(from);
+            for (int64_t p = from; p < to; p += kGroup) {
+#pragma unroll
+                for (int k = 0; k < kGroup; ++k)
+#pragma unroll
+                    for (int e = 0; e < V; ++e) in[W - 1 + k][e] = next[k][e];
+                fetch(p + kGroup);
+#pragma unroll
+                for (int k = 0; k < kGroup; ++k)
+                    if (p + k < to) {
+                        float u[V];
+                        taps.apply(a, l2_dim, in + k, u);
+                        dev::store_vec(y + (size_t)(p + k) * a.channels[w.seg], u);
+                    }
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+                    for (int e = 0; e < V; ++e) in[j][e] = in[kGroup + j][e];
+            }
+        }
+        if (a.export_grid > 0) {
+            // the states after this tile's tokens, local positions (from, to]
+            const int64_t s = a.start_pos ? a.start_pos[i] : 0, g = a.export_grid;
+            for (int64_t p = ((s + from) / g + 1) * g; p <= s + to; p += g) {
+                T* dst = export_to<T, W>(a, a.export_offsets[i] + p / g - s / g - 1);
+                if (dst) copy_state<T, W>(a, dst, lo, p - s, slot, w.c);
+            }
+        }
+        const int fin = owned ? slot_or_none(a.final_slot, i, a.num_slots) : -1;
+        if (fin >= 0) copy_state<T, W>(a, static_cast<T*>(a.pool) + (size_t)fin * (W - 1) * a.C, lo, len, slot, w.c);
+    }
+}
+
+// One token of each row: the same sums over the row's state and its token.
+template <typename T, int W>
+__global__ __launch_bounds__(kThreads) void conv_decode_kernel(ConvArgs a) {
+    constexpr int V = dev::kVec<T>;
+    Channels w;
+    if (!channels_of<T>(a, blockIdx.y * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w)) return;
+    const int b = blockIdx.x;
+    const int slot = slot_or_none(a.init_slot, b, a.num_slots), fin = slot_or_none(a.final_slot, b, a.num_slots);
+    T* y = static_cast<T*>(a.y[w.seg]) + (size_t)b * a.channels[w.seg] + w.ch;
+    float in[W][V], u[V];
+    if (slot < 0) {                              // padding row
 #pragma unroll
         for (int e = 0; e < V; ++e) u[e] = 0.f;
         dev::store_vec(y, u);
         return;
     }
+    Taps<T, W> taps;
+    taps.load(a, w.c);
 #pragma unroll
-    for (int e = 0; e < V; ++e) u[e] = a.bias ? a.bias[c + e] : 0.f;
-#pragma unroll
-    for (int j = 0; j < W; ++j) {
-        float v[V];
-        input_at<T, W>(a, lo, t - lo - (W - 1) + j, slot, c, v);
-#pragma unroll
-        for (int e = 0; e < V; ++e) u[e] = fmaf(a.weight[(size_t)(c + e) * W + j], v[e], u[e]);
-    }
-    finish(a, seg, u);
+    for (int j = 0; j < W; ++j) input_at<T, W>(a, b, j - (W - 1), slot, w.c, in[j]);
+    taps.apply(a, a.l2_dim[w.seg], in, u);
     dev::store_vec(y, u);
-}
-
-template <typename T, int W>
-__global__ __launch_bounds__(kThreads) void conv_state_kernel(ConvArgs a) {
-    constexpr int V = dev::kVec<T>;
-    int seg, ch, c;
-    if (!channel_of<T>(a, blockIdx.y, seg, ch, c)) return;
-    const int64_t unit = blockIdx.x;
-    float rows[W - 1][V];
-    auto put = [&](T* dst) {
+    if (fin < 0) return;
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) dev::store_vec(dst + (size_t)j * a.C + c, rows[j]);
-    };
-    // where export idx goes, or NULL
-    auto export_to = [&](int64_t idx) -> T* {
-        if (idx < 0 || idx >= a.export_capacity) return nullptr;
-        if (!a.export_slots) return static_cast<T*>(a.export_states) + (size_t)idx * (W - 1) * a.C;
-        const int s = a.export_slots[idx];
-        return s >= 0 && s < a.num_slots ? static_cast<T*>(a.pool) + (size_t)s * (W - 1) * a.C : nullptr;
-    };
-    if (unit < a.num_seqs) {
-        const int i = (int)unit;
-        int lo = i, len = 1;
-        if (a.cu_seqlens) dev::seq_range(a.cu_seqlens, i, a.total_tokens, lo, len);
-        const int slot = slot_or_none(a.init_slot, i, a.num_slots);
-        if (!a.cu_seqlens && slot < 0) return;
-        if (a.export_grid > 0) {
-            // an export within the first W - 1 tokens holds rows of the old state: it is
-            // made here, before the final state may replace them
-            const int64_t s = a.start_pos ? a.start_pos[i] : 0;
-            const int64_t p = (s / a.export_grid + 1) * a.export_grid - s;
-            if (p < W - 1 && p <= len) {
-                T* dst = export_to(a.export_offsets[i]);
-                if (dst) {
-#pragma unroll
-                    for (int j = 0; j < W - 1; ++j) input_at<T, W>(a, lo, p - (W - 1) + j, slot, c, rows[j]);
-                    put(dst);
-                }
-            }
-        }
-        const int fin = slot_or_none(a.final_slot, i, a.num_slots);
-        if (fin < 0) return;
-#pragma unroll
-        for (int j = 0; j < W - 1; ++j) input_at<T, W>(a, lo, (int64_t)len - (W - 1) + j, slot, c, rows[j]);
-        put(static_cast<T*>(a.pool) + (size_t)fin * (W - 1) * a.C);
-        return;
-    }
-    const int64_t idx = unit - a.num_seqs;
-    if (idx >= a.export_offsets[a.num_seqs]) return;
-    int l = 0, h = a.num_seqs - 1;
-    while (l < h) {
-        const int mid = (l + h + 1) >> 1;
-        if (a.export_offsets[mid] <= idx) l = mid;
-        else h = mid - 1;
-    }
-    int lo, len;
-    dev::seq_range(a.cu_seqlens, l, a.total_tokens, lo, len);
-    const int64_t s = a.start_pos ? a.start_pos[l] : 0;
-    const int64_t p = (s / a.export_grid + 1 + idx - a.export_offsets[l]) * a.export_grid - s;
-    if (p < W - 1 || p > len) return;
-    T* dst = export_to(idx);
-    if (!dst) return;
-#pragma unroll
-    for (int j = 0; j < W - 1; ++j) input_at<T, W>(a, lo, p - (W - 1) + j, -1, c, rows[j]);
-    put(dst);
+    for (int j = 0; j < W - 1; ++j) dev::store_vec(static_cast<T*>(a.pool) + ((size_t)fin * (W - 1) + j) * a.C + w.c, in[j + 1]);
 }
 
 template <typename T, int W>
 hipError_t launch_typed(const ConvArgs& a, hipStream_t stream) {
-    const unsigned cb = (unsigned)channel_blocks<T>(a);
-    if (a.total_tokens > 0) {
-        hipLaunchKernelGGL((conv_kernel<T, W>), dim3((unsigned)a.total_tokens, cb), dim3(kThreads), 0, stream, a);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
+    const unsigned p = (unsigned)pieces<T>(a), py = (p + kWaves - 1) / kWaves;
+    if (!a.cu_seqlens) {
+        hipLaunchKernelGGL((conv_decode_kernel<T, W>), dim3((unsigned)a.total_tokens, py), dim3(kThreads), 0, stream, a);
+        return hipGetLastError();
     }
-    hipLaunchKernelGGL((conv_state_kernel<T, W>), dim3((unsigned)(a.num_seqs + a.export_capacity), cb), dim3(kThreads), 0,
-                       stream, a);
+    // Shorter tiles while the waves do not fill the card eight to a compute unit.
+    int tile = kTile;
+    while (tile > kGroup && (a.total_tokens + tile - 1) / tile * p < 8 * (int64_t)device_cus()) tile /= 2;
+    const int64_t tiles = (a.total_tokens + tile - 1) / tile;
+    hipLaunchKernelGGL((conv_prefill_kernel<T, W>), dim3((unsigned)(tiles < 1 ? 1 : tiles), py), dim3(kThreads), 0, stream, a, tile);
     return hipGetLastError();
 }
 
@@ -212,10 +263,8 @@ hipError_t launch_width(const ConvArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-hipError_t launch_conv_prefill(const ConvArgs& a, hipStream_t stream) {
+hipError_t launch_conv(const ConvArgs& a, hipStream_t stream) {
     return a.dtype == 1 ? launch_width<__bf16>(a, stream) : launch_width<float>(a, stream);
 }
-
-hipError_t launch_conv_decode(const ConvArgs& a, hipStream_t stream) { return launch_conv_prefill(a, stream); }
 
 }  // namespace gdn

@@ -269,7 +269,7 @@ gdn_status gdn_causal_conv_prefill(const gdn_conv_shape* shape, int32_t num_seqs
     a.export_states = export_grid > 0 && !export_slots ? export_states : nullptr;
     a.export_offsets = export_grid > 0 ? export_offsets : nullptr;
     a.export_capacity = export_grid > 0 && (a.export_states || a.export_slots) ? num_export_states : 0;
-    return hip_status(gdn::launch_conv_prefill(a, stream), "convolution launch");
+    return hip_status(gdn::launch_conv(a, stream), "convolution launch");
 }
 
 gdn_status gdn_causal_conv_decode(const gdn_conv_shape* shape, int32_t num_rows, const void* x, int64_t x_stride,
@@ -292,7 +292,7 @@ gdn_status gdn_causal_conv_decode(const gdn_conv_shape* shape, int32_t num_rows,
     a.total_tokens = num_rows;
     a.init_slot = slot_in;
     a.final_slot = slot_out;
-    return hip_status(gdn::launch_conv_decode(a, stream), "convolution decode launch");
+    return hip_status(gdn::launch_conv(a, stream), "convolution decode launch");
 }
 
 size_t gdn_ssm_chunk_prefill_workspace_size(const gdn_shape* shape, int32_t num_seqs, int64_t total_tokens) {

@@ -50,8 +50,7 @@ struct ConvArgs {
     const int32_t* export_slots;
     int64_t export_capacity;
 };
-hipError_t launch_conv_prefill(const ConvArgs& a, hipStream_t stream);
-hipError_t launch_conv_decode(const ConvArgs& a, hipStream_t stream);
+hipError_t launch_conv(const ConvArgs& a, hipStream_t stream);
 
 // One scan call; decode as for the convolution.
 struct SsmArgs {
