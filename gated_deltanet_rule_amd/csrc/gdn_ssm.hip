@@ -1,26 +1,795 @@
-// gdn_ssm.hip -- selective state space scan for gfx950, token by token.
+// gdn_ssm.hip -- selective state space scan for gfx950: chunked prefill on the matrix
+// cores, and one token of each of many cached rows.
 //
 //     d = softplus(dt + bias),  S <- e^(d A) S + d b x^T,  y = scale S^T c + D x
 //
-// A workgroup of 256 threads holds 64 columns of one head's state (d_k x 64 fp32) in
-// registers: 16 threads of one float4 cover a row's columns, the 16 row groups hold
-// every sixteenth row.  Each token decays the state, adds the outer product and sums
-// S^T c over the row groups through LDS in a fixed order.  A decode row is one token; a
-// packed sequence is walked from its first token to its last.
+// Prefill.  Within a chunk of up to 64 tokens (rows i, j) with start state S (d_k x d_v)
+//     G    = inclusive cumsum of d A inside the chunk
+//     W_ij = (c_i . b_j) e^(G_i - G_j) d_j  for j <= i, else 0
+//     Y    = scale (diag(e^G) C S + W X) + D X
+//     S   <- e^(G_last) S + B^T diag(e^(G_last - G) d) X
+// Only S goes from chunk to chunk.  Two workgroup shapes run the same arithmetic per
+// element, so a sequence's bits do not depend on which one its call takes:
+//   whole heads   one workgroup per (sequence, head), each of its four waves a quarter of
+//                 the columns with its part of S in accumulators; W is formed once and
+//                 shared in LDS.  For calls with enough chains to fill the card.
+//   strips        one workgroup per (sequence, head, 16 columns): four waves form Y, each a
+//                 quarter of the chunk's tokens, while four others advance S, each a
+//                 quarter of its rows; the state passes between them in LDS, by chunk
+//                 parity, so one barrier per chunk is enough.  For calls with few chains,
+//                 bound by the length of the longest one.
+// Operands.  16x16 tiles; lane l holds column l % 16 and rows 4 (l / 16) .. + 3 of a result
+// (that is the "tile half" below), and the same elements are what an operand needs along k,
+// so W and S turn from results into operands in place: products are formed as
+// W^T = B C^T, Y^T = S^T C^T + X^T W^T, and a lane ends up with four neighbouring columns of
+// Y.  B^T and X come out of LDS by transposing reads.
+// Precision.  bf16: the decayed d x is split into three bf16 parts (8 bits each, exact), so
+// the state keeps fp32 accuracy; W and the S that multiplies C are rounded once to bf16 (each
+// adds 2^-9 relative to its own product, on a y that is rounded to bf16 itself).  fp32: fp32
+// matrix products, nothing rounded below fp32.  G is summed in 64 bits and kept as a pair, as
+// its differences are what counts.
+// A non-finite x must not reach earlier tokens through the zeros of W: a chunk that holds one
+// takes it out of the product and sets its column to NaN from its token on.
+//
+// Decode.  A workgroup of 256 threads holds 64 columns of one head's state in registers;
+// bound by the states' traffic.
 #include <hip/hip_runtime.h>
 
 #include "gdn_device.h"
+#include "gdn_internal.h"
 #include "gdn_layer_device.h"
 #include "gdn_layer_internal.h"
 
 namespace gdn {
 namespace {
 
+using dev::kC;
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+typedef __attribute__((address_space(3))) volatile u32x2 lds_vu32x2;
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+
+// ---------------------------------------------------------------- operands
+
+// A chunk's rows of a token-major tensor as a raw buffer of `bytes`: loads past it give
+// zeros and stores past it are dropped, which is how rows beyond a chunk's end enter.
+__device__ __forceinline__ rsrc_t rows_rsrc(const void* base, int bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, bytes, 0x00020000);
+}
+__device__ __forceinline__ u32x4 load16(rsrc_t r, int off) {
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
+
+// What a lane holds of one 16-wide k tile (Half: four elements), and products over a pair
+// of tiles.
+template <typename T>
+struct Ops;
+
+template <>
+struct Ops<__bf16> {
+    typedef bf16x4 Half;
+    static constexpr int kTerms = 3;
+    static constexpr int kPad = 16;      // LDS rows: an odd multiple of 8 dwords, with the swizzle below conflict free
+
+    static __device__ __forceinline__ f32x4 mma(Half a0, Half a1, Half b0, Half b1, f32x4 c) {
+        const bf16x8 a = __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7);
+        const bf16x8 b = __builtin_shufflevector(b0, b1, 0, 1, 2, 3, 4, 5, 6, 7);
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ Half round(f32x4 v) { return __builtin_convertvector(v, bf16x4); }
+    static __device__ __forceinline__ f32x4 widen(Half h) {
+        const u32x2 w = __builtin_bit_cast(u32x2, h);
+        return f32x4{__builtin_bit_cast(float, w[0] << 16), __builtin_bit_cast(float, w[0] & 0xffff0000u),
+                     __builtin_bit_cast(float, w[1] << 16), __builtin_bit_cast(float, w[1] & 0xffff0000u)};
+    }
+    static __device__ __forceinline__ Half load_half(rsrc_t r, int off) {
+        return __builtin_bit_cast(Half, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
+    }
+    static __device__ __forceinline__ void store_half(Half h, rsrc_t r, int off) {
+        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, h), r, off, 0, 0);
+    }
+    // v = t[2] + t[1] + t[0] exactly: the leading 8 bits of what is left, three times
+    static __device__ __forceinline__ void split(f32x4 v, Half (&t)[kTerms]) {
+#pragma unroll
+        for (int k = kTerms - 1; k >= 0; --k) {
+            u32x4 w = __builtin_bit_cast(u32x4, v);
+            t[k] = __builtin_bit_cast(Half, u32x2{__builtin_amdgcn_perm(w[1], w[0], 0x07060302u), __builtin_amdgcn_perm(w[3], w[2], 0x07060302u)});
+            if (k > 0) {
+                w = w & 0xffff0000u;
+                v = v - __builtin_bit_cast(f32x4, w);
+            }
+        }
+    }
+    // Column swizzle of an LDS row: its 16-byte groups in pairs, swapped in every other eight rows.
+    static __device__ __forceinline__ int column(int row, int c) { return c ^ (row & 8); }
+    // Four elements of a row, as one 8-byte read: two of them paired into one instruction
+    // cost four times as much on this card, and a volatile read is never paired.
+    static __device__ __forceinline__ Half row_half(const __bf16* m, int pitch, int row, int c) {
+        const u32x2 w = *(lds_vu32x2*)(m + row * pitch + column(row, c));
+        return __builtin_bit_cast(Half, w);
+    }
+    // Rows r0 + 4 (l / 16) + e of column c0 + l % 16 (a transposing read: lane l points at
+    // row r0 + l / 4, columns c0 + 4 (l % 4)).
+    static __device__ __forceinline__ Half col_half(const __bf16* m, int pitch, int r0, int c0, int lane) {
+        const int row = r0 + (lane >> 2);
+        return __builtin_bit_cast(Half, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(m + row * pitch + column(row, c0 + 4 * (lane & 3)))));
+    }
+    static __device__ __forceinline__ unsigned exponents(u32x4 w) {
+        unsigned m = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = max(m, max(w[i] & 0x7f800000u, (w[i] << 16) & 0x7f800000u));
+        return m;
+    }
+};
+
+template <>
+struct Ops<float> {
+    typedef f32x4 Half;
+    static constexpr int kTerms = 1;
+    static constexpr int kPad = 4;
+
+    static __device__ __forceinline__ f32x4 mma(Half a0, Half a1, Half b0, Half b1, f32x4 c) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a0[e], b0[e], c, 0, 0, 0);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a1[e], b1[e], c, 0, 0, 0);
+        return c;
+    }
+    static __device__ __forceinline__ Half round(f32x4 v) { return v; }
+    static __device__ __forceinline__ f32x4 widen(Half h) { return h; }
+    static __device__ __forceinline__ Half load_half(rsrc_t r, int off) { return __builtin_bit_cast(Half, load16(r, off)); }
+    static __device__ __forceinline__ void store_half(Half h, rsrc_t r, int off) {
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, h), r, off, 0, 0);
+    }
+    static __device__ __forceinline__ void split(f32x4 v, Half (&t)[kTerms]) { t[0] = v; }
+    static __device__ __forceinline__ int column(int, int c) { return c; }
+    static __device__ __forceinline__ Half row_half(const float* m, int pitch, int row, int c) {
+        return *reinterpret_cast<const f32x4*>(m + row * pitch + c);
+    }
+    static __device__ __forceinline__ Half col_half(const float* m, int pitch, int r0, int c0, int lane) {
+        const float* p = m + (r0 + 4 * (lane >> 4)) * pitch + c0 + (lane & 15);
+        return f32x4{p[0], p[pitch], p[2 * pitch], p[3 * pitch]};
+    }
+    static __device__ __forceinline__ unsigned exponents(u32x4 w) {
+        unsigned m = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = max(m, w[i] & 0x7f800000u);
+        return m;
+    }
+};
+
+// ---------------------------------------------------------------- steps and decays of a chunk
+
+struct Gates {
+    float hi[kC], lo[kC];   // G log2 e = hi + lo
+    float d[kC];            // step
+    float w[kC];            // e^(G_last - G) d
+    float eg[kC];           // e^G; rows past the chunk's end repeat the last one
+};
+
+// Inclusive sum over a wave in 64 bits, as dev::wave_inclusive_sum.
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ double dpp_term64(double x) {
+    const u32x2 w = __builtin_bit_cast(u32x2, x);
+    return __builtin_bit_cast(double, u32x2{(unsigned)__builtin_amdgcn_update_dpp(0, (int)w[0], CTRL, ROW_MASK, 0xf, true),
+                                            (unsigned)__builtin_amdgcn_update_dpp(0, (int)w[1], CTRL, ROW_MASK, 0xf, true)});
+}
+__device__ __forceinline__ double wave_sum64(double x) {
+    x += dpp_term64<0x111, 0xf>(x);
+    x += dpp_term64<0x112, 0xf>(x);
+    x += dpp_term64<0x114, 0xf>(x);
+    x += dpp_term64<0x118, 0xf>(x);
+    x += dpp_term64<0x142, 0xa>(x);
+    x += dpp_term64<0x143, 0xc>(x);
+    return x;
+}
+
+// One wave, lane l for the chunk's token l of n.
+__device__ __forceinline__ void make_gates(Gates& g, float dt, float bias, float A, int softplus, int n, int lane) {
+    const float raw = dt + bias;
+    float d = softplus ? dev::softplus(raw) : raw;
+    if (lane >= n) d = 0.f;
+    const double G = wave_sum64((double)d * (double)A * 1.4426950408889634074);
+    const u32x2 w = __builtin_bit_cast(u32x2, G);
+    const double last = __builtin_bit_cast(double, u32x2{(unsigned)__builtin_amdgcn_readlane((int)w[0], kC - 1),
+                                                         (unsigned)__builtin_amdgcn_readlane((int)w[1], kC - 1)});
+    const float hi = (float)G;
+    g.hi[lane] = hi;
+    g.lo[lane] = (float)(G - (double)hi);
+    g.d[lane] = d;
+    g.w[lane] = d * __builtin_amdgcn_exp2f((float)(last - G));
+    g.eg[lane] = __builtin_amdgcn_exp2f(hi);
+}
+
+// A tile of W^T from the scores c_i . b_j: lane l holds i = 16 it + l % 16, j = 16 jt + 4 (l / 16) + e.
+template <typename T>
+__device__ __forceinline__ typename Ops<T>::Half decayed(const Gates& g, f32x4 sc, int it, int jt, int lane) {
+    const int i = 16 * it + (lane & 15), j0 = 16 * jt + 4 * (lane >> 4);
+    const f32x4 hi = *reinterpret_cast<const f32x4*>(g.hi + j0), d = *reinterpret_cast<const f32x4*>(g.d + j0);
+    const float gi = g.hi[i];
+    f32x4 diff;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) diff[e] = gi - hi[e];
+    if constexpr (sizeof(T) == 4) {      // beside bf16's rounding the low parts do not count
+        const f32x4 lo = *reinterpret_cast<const f32x4*>(g.lo + j0);
+        const float gl = g.lo[i];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) diff[e] += gl - lo[e];
+    }
+    f32x4 w;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = j0 + e <= i ? sc[e] * (__builtin_amdgcn_exp2f(diff[e]) * d[e]) : 0.f;
+    return Ops<T>::round(w);
+}
+
+// The decayed steps times x of one tile half, in parts.
+template <typename T>
+__device__ __forceinline__ void weighted(const Gates& g, typename Ops<T>::Half x, int t, int lane, typename Ops<T>::Half (&out)[Ops<T>::kTerms]) {
+    const f32x4 w = *reinterpret_cast<const f32x4*>(g.w + 16 * t + 4 * (lane >> 4));
+    f32x4 v = Ops<T>::widen(x);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] *= w[e];
+    Ops<T>::split(v, out);
+}
+
+// Takes non-finite values out of a column's tile halves (lane: rows 4 (l / 16) + e of tile t,
+// one column); returns the first row that held one, kC without.
+template <typename T>
+__device__ __forceinline__ int take_out(typename Ops<T>::Half (&x)[kC / 16], int lane) {
+    int first = kC;
+#pragma unroll
+    for (int t = kC / 16 - 1; t >= 0; --t) {
+        f32x4 v = Ops<T>::widen(x[t]);
+#pragma unroll
+        for (int e = 3; e >= 0; --e)
+            if (!(fabsf(v[e]) < __builtin_inff())) {
+                v[e] = 0.f;
+                first = 16 * t + 4 * (lane >> 4) + e;
+            }
+        x[t] = Ops<T>::round(v);
+    }
+    first = min(first, __shfl_xor(first, 16));
+    return min(first, __shfl_xor(first, 32));
+}
+
+// Sequence and position bookkeeping of a workgroup.
+struct Walk {
+    int lo, len, skew, chunks;
+    int64_t start;
+    __device__ __forceinline__ Walk(const SsmArgs& a, int i) {
+        dev::seq_range(a.cu_seqlens, i, a.total_tokens, lo, len);
+        lo = __builtin_amdgcn_readfirstlane(lo);
+        len = __builtin_amdgcn_readfirstlane(len);
+        start = a.start_pos ? __builtin_amdgcn_readfirstlane(a.start_pos[i]) : 0;
+        skew = (int)(start & (kC - 1));
+        chunks = dev::seq_chunks(len, skew);
+    }
+    // first row of chunk c and its tokens, 0 past the last chunk
+    __device__ __forceinline__ void span(int c, int64_t& row, int& n) const {
+        int b, e;
+        dev::chunk_span(c, skew, len, b, e);
+        n = c < chunks ? e - b : 0;
+        row = lo + (n > 0 ? b : 0);
+    }
+    // where the state after chunk c is exported, or NULL
+    __device__ __forceinline__ float* export_to(const SsmArgs& a, int i, int c, size_t state) const {
+        if (a.export_grid <= 0) return nullptr;
+        int b, e;
+        dev::chunk_span(c, skew, len, b, e);
+        const int64_t pos = start + e;
+        if (pos % a.export_grid != 0) return nullptr;
+        const int64_t idx = (int64_t)a.export_offsets[i] + pos / a.export_grid - start / a.export_grid - 1;
+        if (idx < 0 || idx >= a.export_capacity) return nullptr;
+        if (!a.export_slots) return a.export_states + (size_t)idx * state;
+        const int sl = a.export_slots[idx];
+        return sl >= 0 && sl < a.num_slots ? a.pool + (size_t)sl * state : nullptr;
+    }
+};
+
+// Workgroups go to the 8 XCDs round robin by index: renumber them so that each XCD gets a
+// contiguous run, and the heads of a group, which read the same b and c, share one L2.
+__device__ __forceinline__ unsigned xcd_run(unsigned wg) {
+    return (gridDim.x & 7u) == 0 ? (wg & 7u) * (gridDim.x >> 3) + (wg >> 3) : wg;
+}
+
+// Rows [row, row + n) of a [tokens, heads, width] tensor at one head, from column c0 on.
+template <typename T>
+__device__ __forceinline__ rsrc_t head_rows(const void* base, int64_t row, int n, int heads, int h, int width, int c0, int columns) {
+    const T* p = static_cast<const T*>(base) + ((size_t)row * heads + h) * width + c0;
+    return rows_rsrc(p, n > 0 ? (int)(((size_t)(n - 1) * heads * width + columns) * sizeof(T)) : 0);
+}
+
+// A 64 x N block on its way from memory to LDS through the registers of TH threads.
+template <typename T, int N, int TH>
+struct Staged {
+    static constexpr int V = 16 / sizeof(T), PER_ROW = N / V, VECS = kC * PER_ROW;
+    static constexpr int K = (VECS + TH - 1) / TH;
+    u32x4 v[K];
+
+    __device__ __forceinline__ void load(rsrc_t r, int row_bytes, int tid) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int u = tid + k * TH;
+            if (VECS % TH == 0 || u < VECS) v[k] = load16(r, (u / PER_ROW) * row_bytes + (u % PER_ROW) * 16);
+        }
+    }
+    // row-major, rows swizzled as Ops<T>::column says
+    __device__ __forceinline__ void store(T* m, int pitch, int tid) const {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int u = tid + k * TH, row = u / PER_ROW;
+            if (VECS % TH == 0 || u < VECS) *reinterpret_cast<u32x4*>(m + row * pitch + Ops<T>::column(row, (u % PER_ROW) * V)) = v[k];
+        }
+    }
+    // as operands of rows: the two (bf16) or one (fp32) halves of a lane side by side
+    __device__ __forceinline__ void store_operands(T* m, int tid) const {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int u = tid + k * TH, row = u / PER_ROW, c = (u % PER_ROW) * V;
+            if constexpr (sizeof(T) == 2) {
+                // pair block (row tile, c / 32), lane (row % 16, group), half (c / 16) % 2
+                T* p = m + ((row >> 4) * (N / 32) + (c >> 5)) * 512 + ((row & 15) + 16 * ((c & 15) >> 2)) * 8 + ((c >> 4) & 1) * 4;
+                *reinterpret_cast<u32x2*>(p) = u32x2{v[k][0], v[k][1]};
+                *reinterpret_cast<u32x2*>(p + 128) = u32x2{v[k][2], v[k][3]};
+            } else {
+                T* p = m + ((row >> 4) * (N / 16) + (c >> 4)) * 256 + ((row & 15) + 16 * ((c & 15) >> 2)) * 4;
+                *reinterpret_cast<u32x4*>(p) = v[k];
+            }
+        }
+    }
+    __device__ __forceinline__ bool any_not_finite(int tid) const {
+        unsigned m = 0;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (VECS % TH == 0 || tid + k * TH < VECS) m = max(m, Ops<T>::exponents(v[k]));
+        return m == 0x7f800000u;
+    }
+};
+
+// A lane's two halves of pair s of an operand block stored by Staged::store_operands.
+template <typename T>
+__device__ __forceinline__ void pair_of(const T* block, int s, int lane, typename Ops<T>::Half& h0, typename Ops<T>::Half& h1) {
+    typedef typename Ops<T>::Half Half;
+    if constexpr (sizeof(T) == 2) {
+        const bf16x8 v = *reinterpret_cast<const bf16x8*>(block + s * 512 + lane * 8);
+        h0 = __builtin_shufflevector(v, v, 0, 1, 2, 3);
+        h1 = __builtin_shufflevector(v, v, 4, 5, 6, 7);
+    } else {
+        h0 = *reinterpret_cast<const Half*>(block + 2 * s * 256 + lane * 4);
+        h1 = *reinterpret_cast<const Half*>(block + (2 * s + 1) * 256 + lane * 4);
+    }
+}
+
+// The scores of one tile: sum over d_k of b_j (rows of LDS) and c_i (the lane's halves).
+template <typename T, int DK, typename C>
+__device__ __forceinline__ f32x4 score_tile(const T* b, int pitch, int jt, int lane, C c_pair) {
+    typedef typename Ops<T>::Half Half;
+    f32x4 sc = {0.f, 0.f, 0.f, 0.f};
+    const int row = 16 * jt + (lane & 15), g4 = 4 * (lane >> 4);
+#pragma unroll
+    for (int s = 0; s < DK / 32; ++s) {
+        Half c0, c1;
+        c_pair(s, c0, c1);
+        sc = Ops<T>::mma(Ops<T>::row_half(b, pitch, row, 32 * s + g4), Ops<T>::row_half(b, pitch, row, 32 * s + 16 + g4), c0, c1, sc);
+    }
+    return sc;
+}
+
+// ---------------------------------------------------------------- whole heads
+
+template <typename T, int DK, int DV>
+struct HeadSmem {
+    static constexpr int BP = DK + Ops<T>::kPad, XP = DV + Ops<T>::kPad;
+    alignas(16) T b[kC * BP];
+    T x[kC * XP];
+    T c[kC * DK];            // operand order
+    T w[10 * 256];           // lower tiles of W, a lane's half each
+    Gates gate[2];           // by chunk parity
+    int bad[2];              // chunk + 1 where its x holds a non-finite value
+};
+
+template <typename T, int DK, int DV>
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void ssm_head_kernel(SsmArgs a) {
+    typedef typename Ops<T>::Half Half;
+    typedef HeadSmem<T, DK, DV> SM;
+    constexpr int CT = DV / 64, NT = DK / 16, TT = kC / 16, TERMS = Ops<T>::kTerms;
+    __shared__ SM sm;
+    const int unit = (int)xcd_run(blockIdx.x), i = unit / a.H_v, h = unit - i * a.H_v;
+    const int kh = h / (a.H_v / a.H_k);
+    const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int li = lane & 15, g4 = 4 * (lane >> 4), col0 = (DV / 4) * wv;
+    const size_t state = (size_t)a.H_v * DK * DV;
+    const Walk walk(a, i);
+    const float A = a.A[h], bias = a.dt_bias ? a.dt_bias[h] : 0.f, D = a.D ? a.D[h] : 0.f;
+    const int krow = a.H_k * DK * (int)sizeof(T), vrow = a.H_v * DV * (int)sizeof(T);
+
+    // S[nt][ct]: rows 16 nt + g4 + e, column col0 + 16 ct + li
+    f32x4 S[NT][CT];
+    auto at = [&](int nt, int ct, int e) { return (size_t)(16 * nt + g4 + e) * DV + col0 + 16 * ct + li; };
+    const int sin = a.init_slot[i];
+    const bool have = sin >= 0 && sin < a.num_slots;
+    {
+        const float* src = have ? a.pool + (size_t)sin * state + (size_t)h * DK * DV : nullptr;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) S[nt][ct][e] = have ? src[at(nt, ct, e)] : 0.f;
+        // waited for here, once: inside the loop the wait would also take in the prefetches
+        __builtin_amdgcn_s_waitcnt(0x0F70);
+    }
+    auto put = [&](float* dst) {
+        dst += (size_t)h * DK * DV;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) dst[at(nt, ct, e)] = S[nt][ct][e];
+    };
+
+    Staged<T, DK, 256> sb, sc;
+    Staged<T, DV, 256> sx;
+    float dt_next = 0.f;
+    auto fetch = [&](int c) {
+        int64_t row;
+        int n;
+        walk.span(c, row, n);
+        sb.load(head_rows<T>(a.b, row, n, a.H_k, kh, DK, 0, DK), krow, tid);
+        sc.load(head_rows<T>(a.c, row, n, a.H_k, kh, DK, 0, DK), krow, tid);
+        sx.load(head_rows<T>(a.x, row, n, a.H_v, h, DV, 0, DV), vrow, tid);
+    };
+    auto fetch_dt = [&](int c) {
+        int64_t row;
+        int n;
+        walk.span(c, row, n);
+        dt_next = lane < n ? a.dt[(size_t)(row + lane) * a.H_v + h] : 0.f;
+    };
+    auto gates = [&](int c) {
+        int64_t row;
+        int n;
+        walk.span(c, row, n);
+        make_gates(sm.gate[c & 1], dt_next, bias, A, a.dt_softplus, n, lane);
+    };
+    if (tid < 2) sm.bad[tid] = 0;
+    fetch(0);
+    if (wv == 3) {                       // the last wave makes the gates, a chunk ahead
+        fetch_dt(0);
+        gates(0);
+        fetch_dt(1);
+    }
+    __syncthreads();
+
+    for (int c = 0; c < walk.chunks; ++c) {
+        const Gates& g = sm.gate[c & 1];
+        sb.store(sm.b, SM::BP, tid);
+        sc.store_operands(sm.c, tid);
+        sx.store(sm.x, SM::XP, tid);
+        if (sx.any_not_finite(tid)) sm.bad[c & 1] = c + 1;
+        dev::lds_barrier();
+        fetch(c + 1);
+        // lower tiles of W, in turn
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            const int blk = wv + 4 * k;
+            if (blk < 10) {
+                const int it = blk >= 6 ? 3 : blk >= 3 ? 2 : blk >= 1 ? 1 : 0, jt = blk - it * (it + 1) / 2;
+                const T* cb = sm.c + it * 16 * DK;
+                const f32x4 s = score_tile<T, DK>(sm.b, SM::BP, jt, lane, [&](int p, Half& h0, Half& h1) { pair_of<T>(cb, p, lane, h0, h1); });
+                *reinterpret_cast<Half*>(sm.w + blk * 256 + lane * 4) = decayed<T>(g, s, it, jt, lane);
+            }
+        }
+        // Y^T = S^T C^T, then the rows' e^G
+        f32x4 y[TT][CT];
+#pragma unroll
+        for (int it = 0; it < TT; ++it)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) y[it][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < NT / 2; ++s) {
+            Half s0[CT], s1[CT];
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                s0[ct] = Ops<T>::round(S[2 * s][ct]);
+                s1[ct] = Ops<T>::round(S[2 * s + 1][ct]);
+            }
+#pragma unroll
+            for (int it = 0; it < TT; ++it) {
+                Half c0, c1;
+                pair_of<T>(sm.c + it * 16 * DK, s, lane, c0, c1);
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) y[it][ct] = Ops<T>::mma(s0[ct], s1[ct], c0, c1, y[it][ct]);
+            }
+        }
+#pragma unroll
+        for (int it = 0; it < TT; ++it) {
+            const float eg = g.eg[16 * it + li];
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[it][ct][e] *= eg;
+        }
+        if (wv == 3) {
+            gates(c + 1);
+            fetch_dt(c + 2);
+        }
+        dev::lds_barrier();
+        // Y^T += X^T W^T
+        Half x[CT][TT];
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+            for (int t = 0; t < TT; ++t) x[ct][t] = Ops<T>::col_half(sm.x, SM::XP, 16 * t, col0 + 16 * ct, lane);
+        // S <- e^(G_last) S + B^T (w X)
+        const float decay = g.eg[kC - 1];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) S[nt][ct][e] *= decay;
+#pragma unroll
+        for (int s = 0; s < TT / 2; ++s) {
+            Half v0[CT][TERMS], v1[CT][TERMS];
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                weighted<T>(g, x[ct][2 * s], 2 * s, lane, v0[ct]);
+                weighted<T>(g, x[ct][2 * s + 1], 2 * s + 1, lane, v1[ct]);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const Half b0 = Ops<T>::col_half(sm.b, SM::BP, 32 * s, 16 * nt, lane), b1 = Ops<T>::col_half(sm.b, SM::BP, 32 * s + 16, 16 * nt, lane);
+#pragma unroll
+                for (int k = 0; k < TERMS; ++k)
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) S[nt][ct] = Ops<T>::mma(b0, b1, v0[ct][k], v1[ct][k], S[nt][ct]);
+            }
+        }
+        int bad[CT];
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) bad[ct] = kC;
+        if (sm.bad[c & 1] == c + 1)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) bad[ct] = take_out<T>(x[ct], lane);
+#pragma unroll
+        for (int it = 0; it < TT; ++it)
+#pragma unroll
+            for (int s = 0; s <= it / 2; ++s) {
+                const Half w0 = *reinterpret_cast<const Half*>(sm.w + (it * (it + 1) / 2 + 2 * s) * 256 + lane * 4);
+                Half w1 = {};
+                if (2 * s + 1 <= it) w1 = *reinterpret_cast<const Half*>(sm.w + (it * (it + 1) / 2 + 2 * s + 1) * 256 + lane * 4);
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) y[it][ct] = Ops<T>::mma(x[ct][2 * s], x[ct][2 * s + 1], w0, w1, y[it][ct]);
+            }
+        int64_t row;
+        int n;
+        walk.span(c, row, n);
+        const rsrc_t ry = head_rows<T>(a.y, row, n, a.H_v, h, DV, 0, DV);
+#pragma unroll
+        for (int it = 0; it < TT; ++it)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                const int t = 16 * it + li, p = col0 + 16 * ct + g4;
+                const f32x4 xt = Ops<T>::widen(Ops<T>::row_half(sm.x, SM::XP, t, p));
+                f32x4 o;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[e] = fmaf(a.scale, y[it][ct][e], D * xt[e]);
+                if (sm.bad[c & 1] == c + 1)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (__shfl(bad[ct], g4 + e) <= t) o[e] = __builtin_nanf("");
+                Ops<T>::store_half(Ops<T>::round(o), ry, t * vrow + p * (int)sizeof(T));
+            }
+        float* dst = walk.export_to(a, i, c, state);
+        if (dst) put(dst);
+        dev::lds_barrier();
+    }
+    const int fin = a.final_slot[i];
+    if (fin >= 0 && fin < a.num_slots) put(a.pool + (size_t)fin * state);
+}
+
+// ---------------------------------------------------------------- strips
+
+constexpr int kStrip = 16;
+
+template <typename T, int DK>
+struct StripSmem {
+    static constexpr int BP = DK + Ops<T>::kPad, XP = kStrip + (sizeof(T) == 4 ? 4 : 0);
+    alignas(16) T b[2][kC * BP];          // by chunk parity, as all of it
+    T x[2][kC * XP];
+    T s[2][DK * kStrip];      // the state as operand, rounded to T
+    Gates gate[2];
+    int bad[2];
+};
+
+template <typename T, int DK, int DV>
+__global__ __launch_bounds__(512, 2) void ssm_strip_kernel(SsmArgs a) {
+    typedef typename Ops<T>::Half Half;
+    typedef StripSmem<T, DK> SM;
+    constexpr int NT = DK / 64, TT = kC / 16, TERMS = Ops<T>::kTerms, NS = DV / kStrip, PAIRS = DK / 32;
+    __shared__ SM sm;
+    const unsigned wg = xcd_run(blockIdx.x);
+    const int col0 = kStrip * (int)(wg % NS), unit = (int)(wg / NS), i = unit / a.H_v, h = unit - i * a.H_v;
+    const int kh = h / (a.H_v / a.H_k);
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const bool forms_y = wave < 4;
+    const int wv = wave & 3;             // its quarter of the tokens or of the state's rows
+    const int li = lane & 15, g4 = 4 * (lane >> 4);
+    const size_t state = (size_t)a.H_v * DK * DV;
+    const Walk walk(a, i);
+    const float A = a.A[h], bias = a.dt_bias ? a.dt_bias[h] : 0.f, D = a.D ? a.D[h] : 0.f;
+    const int krow = a.H_k * DK * (int)sizeof(T), vrow = a.H_v * DV * (int)sizeof(T);
+
+    f32x4 S[NT];                         // rows 16 (NT wv + nt) + g4 + e, column col0 + li
+    auto at = [&](int nt, int e) { return (size_t)(16 * (NT * wv + nt) + g4 + e) * DV + col0 + li; };
+    auto put = [&](float* dst) {
+        dst += (size_t)h * DK * DV;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) dst[at(nt, e)] = S[nt][e];
+    };
+    auto share = [&](int parity) {       // a lane's half of tile t in operand order
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int t = NT * wv + nt;
+            T* p = sizeof(T) == 2 ? sm.s[parity] + (t >> 1) * 512 + lane * 8 + (t & 1) * 4 : sm.s[parity] + t * 256 + lane * 4;
+            *reinterpret_cast<Half*>(p) = Ops<T>::round(S[nt]);
+        }
+    };
+
+    // Loads run two chunks ahead of their use, in two register sets by chunk parity.
+    Staged<T, DK, 512> sb[2];
+    Staged<T, kStrip, 512> sx[2];
+    Half cf[2][2 * PAIRS];
+    float dts[2];
+    auto fetch = [&](int c, int p) {
+        int64_t row;
+        int n;
+        walk.span(c, row, n);
+        sb[p].load(head_rows<T>(a.b, row, n, a.H_k, kh, DK, 0, DK), krow, tid);
+        sx[p].load(head_rows<T>(a.x, row, n, a.H_v, h, DV, col0, kStrip), vrow, tid);
+        if (wave == 0) dts[p] = lane < n ? a.dt[(size_t)(row + lane) * a.H_v + h] : 0.f;
+    };
+    auto fetch_c = [&](int c, int p) {
+        int64_t row;
+        int n;
+        walk.span(c, row, n);
+        const rsrc_t r = head_rows<T>(a.c, row, n, a.H_k, kh, DK, 0, DK);
+#pragma unroll
+        for (int t = 0; t < 2 * PAIRS; ++t) cf[p][t] = Ops<T>::load_half(r, (16 * wv + li) * krow + (16 * t + g4) * (int)sizeof(T));
+    };
+    auto stage = [&](int c, int p) {
+        sb[p].store(sm.b[p], SM::BP, tid);
+        sx[p].store(sm.x[p], SM::XP, tid);
+        if (sx[p].any_not_finite(tid)) sm.bad[p] = c + 1;
+        if (wave == 0) {
+            int64_t row;
+            int n;
+            walk.span(c, row, n);
+            make_gates(sm.gate[p], dts[p], bias, A, a.dt_softplus, n, lane);
+        }
+    };
+    auto body = [&](int c, int p) {
+        stage(c + 1, p ^ 1);
+        fetch(c + 3, p ^ 1);
+        const Gates& g = sm.gate[p];
+        Half x[TT];
+#pragma unroll
+        for (int t = 0; t < TT; ++t) x[t] = Ops<T>::col_half(sm.x[p], SM::XP, 16 * t, 0, lane);
+        if (forms_y) {
+            Half w[TT];
+#pragma unroll
+            for (int jt = 0; jt < TT; ++jt) {
+                w[jt] = Half{};
+                if (jt <= wv) {
+                    const f32x4 s = score_tile<T, DK>(sm.b[p], SM::BP, jt, lane, [&](int q, Half& h0, Half& h1) {
+                        h0 = cf[p][2 * q];
+                        h1 = cf[p][2 * q + 1];
+                    });
+                    w[jt] = decayed<T>(g, s, wv, jt, lane);
+                }
+            }
+            f32x4 y = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int s = 0; s < PAIRS; ++s) {
+                Half s0, s1;
+                pair_of<T>(sm.s[p], s, lane, s0, s1);
+                y = Ops<T>::mma(s0, s1, cf[p][2 * s], cf[p][2 * s + 1], y);
+            }
+            fetch_c(c + 2, p);
+            const float eg = g.eg[16 * wv + li];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] *= eg;
+            const bool poisoned = sm.bad[p] == c + 1;
+            const int bad = poisoned ? take_out<T>(x, lane) : kC;
+#pragma unroll
+            for (int s = 0; s < TT / 2; ++s)
+                if (2 * s <= wv) y = Ops<T>::mma(x[2 * s], x[2 * s + 1], w[2 * s], w[2 * s + 1], y);
+            int64_t row;
+            int n;
+            walk.span(c, row, n);
+            const rsrc_t ry = head_rows<T>(a.y, row, n, a.H_v, h, DV, col0, kStrip);
+            const int t = 16 * wv + li;
+            const f32x4 xt = Ops<T>::widen(Ops<T>::row_half(sm.x[p], SM::XP, t, g4));
+            f32x4 o;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] = fmaf(a.scale, y[e], D * xt[e]);
+            if (poisoned)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (__shfl(bad, g4 + e) <= t) o[e] = __builtin_nanf("");
+            Ops<T>::store_half(Ops<T>::round(o), ry, t * vrow + g4 * (int)sizeof(T));
+        } else {
+            const float decay = g.eg[kC - 1];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) S[nt][e] *= decay;
+#pragma unroll
+            for (int s = 0; s < TT / 2; ++s) {
+                Half v0[TERMS], v1[TERMS];
+                weighted<T>(g, x[2 * s], 2 * s, lane, v0);
+                weighted<T>(g, x[2 * s + 1], 2 * s + 1, lane, v1);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const int n0 = 16 * (NT * wv + nt);
+                    const Half b0 = Ops<T>::col_half(sm.b[p], SM::BP, 32 * s, n0, lane), b1 = Ops<T>::col_half(sm.b[p], SM::BP, 32 * s + 16, n0, lane);
+#pragma unroll
+                    for (int k = 0; k < TERMS; ++k) S[nt] = Ops<T>::mma(b0, b1, v0[k], v1[k], S[nt]);
+                }
+            }
+            share(p ^ 1);
+            float* dst = walk.export_to(a, i, c, state);
+            if (dst) put(dst);
+        }
+        dev::lds_barrier();
+    };
+
+    if (tid < 2) sm.bad[tid] = 0;
+    fetch(0, 0);
+    fetch(1, 1);
+    if (forms_y) {
+        fetch_c(0, 0);
+        fetch_c(1, 1);
+    } else {
+        const int sin = a.init_slot[i];
+        const bool have = sin >= 0 && sin < a.num_slots;
+        const float* src = have ? a.pool + (size_t)sin * state + (size_t)h * DK * DV : nullptr;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) S[nt][e] = have ? src[at(nt, e)] : 0.f;
+        share(0);
+    }
+    __syncthreads();
+    stage(0, 0);
+    fetch(2, 0);
+    dev::lds_barrier();
+    for (int c = 0; c < walk.chunks; c += 2) {
+        body(c, 0);
+        if (c + 1 < walk.chunks) body(c + 1, 1);
+    }
+    const int fin = a.final_slot[i];
+    if (!forms_y && fin >= 0 && fin < a.num_slots) put(a.pool + (size_t)fin * state);
+}
+
+// ---------------------------------------------------------------- decode
+
 constexpr int kThreads = 256;
 constexpr int kCols = 64;
 
+// 16 threads of one float4 cover a row's columns, the 16 row groups hold every sixteenth
+// row; S^T c is summed over the row groups through LDS in a fixed order.
 template <typename T, int DK, int DV>
-__global__ __launch_bounds__(kThreads) void ssm_token_kernel(SsmArgs a) {
+__global__ __launch_bounds__(kThreads) void ssm_decode_kernel(SsmArgs a) {
     constexpr int TPR = kCols / 4, RG = kThreads / TPR, R = DK / RG, NCW = DV / kCols;
     const int unit = blockIdx.x / NCW;
     const int col0 = kCols * (blockIdx.x - unit * NCW);
@@ -29,93 +798,88 @@ __global__ __launch_bounds__(kThreads) void ssm_token_kernel(SsmArgs a) {
     const int tid = threadIdx.x, c4 = tid % TPR, rg = tid / TPR;
     const size_t SE = (size_t)DK * DV;
 
-    const int sin = a.init_slot[i];
-    const bool have = sin >= 0 && sin < a.num_slots;
-    int lo = i, len = 1;
-    if (a.cu_seqlens) dev::seq_range(a.cu_seqlens, i, a.total_tokens, lo, len);
-    else if (!have) {                            // padding row
-        T* y = static_cast<T*>(a.y) + ((size_t)i * a.H_v + h) * DV;
-        if (tid < kCols) y[col0 + tid] = (T)0.f;
+    const int sin = a.init_slot[i], fin = a.final_slot[i];
+    T* y = static_cast<T*>(a.y) + ((size_t)i * a.H_v + h) * DV + col0 + 4 * c4;
+    if (sin < 0 || sin >= a.num_slots) {         // padding row
+        if (rg == 0) y[0] = y[1] = y[2] = y[3] = (T)0.f;
         return;
     }
-    float4 s[R];
+    const float* src = a.pool + ((size_t)sin * a.H_v + h) * SE + col0 + 4 * c4;
+    f32x4 s[R];
 #pragma unroll
-    for (int m = 0; m < R; ++m)
-        s[m] = have ? *reinterpret_cast<const float4*>(a.pool + ((size_t)sin * a.H_v + h) * SE + (size_t)(rg + RG * m) * DV + col0 + 4 * c4)
-                    : make_float4(0.f, 0.f, 0.f, 0.f);
-    auto put = [&](float* state) {
-#pragma unroll
-        for (int m = 0; m < R; ++m) *reinterpret_cast<float4*>(state + (size_t)(rg + RG * m) * DV + col0 + 4 * c4) = s[m];
-    };
-    const int64_t pos0 = a.start_pos ? a.start_pos[i] : 0;
-    int64_t next_export = a.export_grid > 0 ? (pos0 / a.export_grid + 1) * a.export_grid : 0, exported = 0;
-    const float A = a.A[h], bias = a.dt_bias ? a.dt_bias[h] : 0.f, D = a.D ? a.D[h] : 0.f;
-
+    for (int m = 0; m < R; ++m) s[m] = *reinterpret_cast<const f32x4*>(src + (size_t)(rg + RG * m) * DV);
     __shared__ float bc[2][DK];
-    __shared__ float4 red[RG][TPR];
-    for (int t = 0; t < len; ++t) {
-        const size_t row = (size_t)(lo + t);
-        if (tid < DK) bc[0][tid] = (float)static_cast<const T*>(a.b)[(row * a.H_k + kh) * DK + tid];
-        else if (tid < 2 * DK) bc[1][tid - DK] = (float)static_cast<const T*>(a.c)[(row * a.H_k + kh) * DK + tid - DK];
-        const T* xp = static_cast<const T*>(a.x) + (row * a.H_v + h) * DV + col0 + 4 * c4;
-        const float4 x = make_float4((float)xp[0], (float)xp[1], (float)xp[2], (float)xp[3]);
-        const float raw = a.dt[row * a.H_v + h] + bias;
-        const float d = a.dt_softplus ? dev::softplus(raw) : raw;
-        const float decay = expf(d * A);
-        __syncthreads();
-        float4 p = make_float4(0.f, 0.f, 0.f, 0.f);
+    __shared__ f32x4 red[RG][TPR];
+    if (tid < DK) bc[0][tid] = (float)static_cast<const T*>(a.b)[((size_t)i * a.H_k + kh) * DK + tid];
+    else if (tid < 2 * DK) bc[1][tid - DK] = (float)static_cast<const T*>(a.c)[((size_t)i * a.H_k + kh) * DK + tid - DK];
+    const T* xp = static_cast<const T*>(a.x) + ((size_t)i * a.H_v + h) * DV + col0 + 4 * c4;
+    const f32x4 x = {(float)xp[0], (float)xp[1], (float)xp[2], (float)xp[3]};
+    const float raw = a.dt[(size_t)i * a.H_v + h] + (a.dt_bias ? a.dt_bias[h] : 0.f), D = a.D ? a.D[h] : 0.f;
+    const float d = a.dt_softplus ? dev::softplus(raw) : raw;
+    const float decay = expf(d * a.A[h]);
+    __syncthreads();
+    f32x4 p = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int m = 0; m < R; ++m) {
-            const float db = d * bc[0][rg + RG * m], cr = bc[1][rg + RG * m];
-            s[m].x = fmaf(db, x.x, decay * s[m].x); s[m].y = fmaf(db, x.y, decay * s[m].y);
-            s[m].z = fmaf(db, x.z, decay * s[m].z); s[m].w = fmaf(db, x.w, decay * s[m].w);
-            p.x = fmaf(s[m].x, cr, p.x); p.y = fmaf(s[m].y, cr, p.y);
-            p.z = fmaf(s[m].z, cr, p.z); p.w = fmaf(s[m].w, cr, p.w);
-        }
-        red[rg][c4] = p;
-        __syncthreads();
-        if (rg == 0) {
-            float4 o = red[0][c4];
+    for (int m = 0; m < R; ++m) {
+        const float db = d * bc[0][rg + RG * m], cr = bc[1][rg + RG * m];
 #pragma unroll
-            for (int r = 1; r < RG; ++r) {
-                const float4 q = red[r][c4];
-                o.x += q.x; o.y += q.y; o.z += q.z; o.w += q.w;
-            }
-            T* y = static_cast<T*>(a.y) + (row * a.H_v + h) * DV + col0 + 4 * c4;
-            y[0] = (T)fmaf(D, x.x, a.scale * o.x); y[1] = (T)fmaf(D, x.y, a.scale * o.y);
-            y[2] = (T)fmaf(D, x.z, a.scale * o.z); y[3] = (T)fmaf(D, x.w, a.scale * o.w);
-        }
-        if (a.export_grid > 0 && pos0 + t + 1 == next_export) {
-            const int64_t idx = (int64_t)a.export_offsets[i] + exported;
-            next_export += a.export_grid;
-            ++exported;
-            if (idx >= 0 && idx < a.export_capacity) {
-                if (!a.export_slots) {
-                    put(a.export_states + ((size_t)idx * a.H_v + h) * SE);
-                } else {
-                    const int sl = a.export_slots[idx];
-                    if (sl >= 0 && sl < a.num_slots) put(a.pool + ((size_t)sl * a.H_v + h) * SE);
-                }
-            }
+        for (int e = 0; e < 4; ++e) {
+            s[m][e] = fmaf(db, x[e], decay * s[m][e]);
+            p[e] = fmaf(s[m][e], cr, p[e]);
         }
     }
-    const int fin = a.final_slot[i];
-    if (fin >= 0 && fin < a.num_slots) put(a.pool + ((size_t)fin * a.H_v + h) * SE);
+    red[rg][c4] = p;
+    if (fin >= 0 && fin < a.num_slots) {
+        float* dst = a.pool + ((size_t)fin * a.H_v + h) * SE + col0 + 4 * c4;
+#pragma unroll
+        for (int m = 0; m < R; ++m) *reinterpret_cast<f32x4*>(dst + (size_t)(rg + RG * m) * DV) = s[m];
+    }
+    dev::lds_barrier();
+    if (rg == 0) {
+        f32x4 o = red[0][c4];
+#pragma unroll
+        for (int r = 1; r < RG; ++r)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] += red[r][c4][e];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = (T)fmaf(D, x[e], a.scale * o[e]);
+    }
+}
+
+// ---------------------------------------------------------------- launches
+
+template <typename T, int DK, int DV>
+hipError_t decode_typed(const SsmArgs& a, hipStream_t stream) {
+    const unsigned blocks = (unsigned)a.num_seqs * (unsigned)a.H_v * (unsigned)(DV / kCols);
+    hipLaunchKernelGGL((ssm_decode_kernel<T, DK, DV>), dim3(blocks), dim3(kThreads), 0, stream, a);
+    return hipGetLastError();
 }
 
 template <typename T, int DK, int DV>
-hipError_t launch_typed(const SsmArgs& a, hipStream_t stream) {
-    const unsigned blocks = (unsigned)a.num_seqs * (unsigned)a.H_v * (unsigned)(DV / kCols);
-    hipLaunchKernelGGL((ssm_token_kernel<T, DK, DV>), dim3(blocks), dim3(kThreads), 0, stream, a);
+hipError_t prefill_typed(const SsmArgs& a, hipStream_t stream) {
+    const int64_t chains = (int64_t)a.num_seqs * a.H_v;
+    // Strips while they, at one workgroup each, do not outnumber the compute units by far.
+    if (chains * (DV / kStrip) <= 4 * (int64_t)device_cus())
+        hipLaunchKernelGGL((ssm_strip_kernel<T, DK, DV>), dim3((unsigned)(chains * (DV / kStrip))), dim3(512), 0, stream, a);
+    else
+        hipLaunchKernelGGL((ssm_head_kernel<T, DK, DV>), dim3((unsigned)chains), dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 
 template <typename T>
-hipError_t launch_dims(const SsmArgs& a, hipStream_t stream) {
-    if (a.d_k == 128 && a.d_v == 128) return launch_typed<T, 128, 128>(a, stream);
-    if (a.d_k == 128 && a.d_v == 64) return launch_typed<T, 128, 64>(a, stream);
-    if (a.d_k == 64 && a.d_v == 128) return launch_typed<T, 64, 128>(a, stream);
-    return launch_typed<T, 64, 64>(a, stream);
+hipError_t prefill_dims(const SsmArgs& a, hipStream_t stream) {
+    if (a.d_k == 128 && a.d_v == 128) return prefill_typed<T, 128, 128>(a, stream);
+    if (a.d_k == 128 && a.d_v == 64) return prefill_typed<T, 128, 64>(a, stream);
+    if (a.d_k == 64 && a.d_v == 128) return prefill_typed<T, 64, 128>(a, stream);
+    return prefill_typed<T, 64, 64>(a, stream);
+}
+
+template <typename T>
+hipError_t decode_dims(const SsmArgs& a, hipStream_t stream) {
+    if (a.d_k == 128 && a.d_v == 128) return decode_typed<T, 128, 128>(a, stream);
+    if (a.d_k == 128 && a.d_v == 64) return decode_typed<T, 128, 64>(a, stream);
+    if (a.d_k == 64 && a.d_v == 128) return decode_typed<T, 64, 128>(a, stream);
+    return decode_typed<T, 64, 64>(a, stream);
 }
 
 }  // namespace
@@ -123,9 +887,11 @@ hipError_t launch_dims(const SsmArgs& a, hipStream_t stream) {
 size_t ssm_workspace_bytes(int, int, int, int, int, int64_t) { return 0; }
 
 hipError_t launch_ssm_decode(const SsmArgs& a, hipStream_t stream) {
-    return a.dtype == 1 ? launch_dims<__bf16>(a, stream) : launch_dims<float>(a, stream);
+    return a.dtype == 1 ? decode_dims<__bf16>(a, stream) : decode_dims<float>(a, stream);
 }
 
-hipError_t launch_ssm_prefill(const SsmArgs& a, hipStream_t stream) { return launch_ssm_decode(a, stream); }
+hipError_t launch_ssm_prefill(const SsmArgs& a, hipStream_t stream) {
+    return a.dtype == 1 ? prefill_dims<__bf16>(a, stream) : prefill_dims<float>(a, stream);
+}
 
 }  // namespace gdn
