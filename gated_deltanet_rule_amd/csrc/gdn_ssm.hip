@@ -110,15 +110,16 @@ struct Ops<__bf16> {
     static __device__ __forceinline__ int column(int row, int c) { return c ^ (row & 8); }
     // Four elements of a row, as one 8-byte read: two of them paired into one instruction
     // cost four times as much on this card, and a volatile read is never paired.
-    static __device__ __forceinline__ Half row_half(const __bf16* m, int pitch, int row, int c) {
-        const u32x2 w = *(lds_vu32x2*)(m + row * pitch + column(row, c));
+    // t: a multiple of 16, g4: the lane's place in it (the swizzle moves only that).
+    static __device__ __forceinline__ Half row_half(const __bf16* m, int pitch, int row, int t, int g4) {
+        const u32x2 w = *(lds_vu32x2*)(m + (row * pitch + (g4 ^ (row & 8))) + t);
         return __builtin_bit_cast(Half, w);
     }
     // Rows r0 + 4 (l / 16) + e of column c0 + l % 16 (a transposing read: lane l points at
     // row r0 + l / 4, columns c0 + 4 (l % 4)).
     static __device__ __forceinline__ Half col_half(const __bf16* m, int pitch, int r0, int c0, int lane) {
-        const int row = r0 + (lane >> 2);
-        return __builtin_bit_cast(Half, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(m + row * pitch + column(row, c0 + 4 * (lane & 3)))));
+        const int row = lane >> 2, at = row * pitch + ((4 * (lane & 3)) ^ (row & 8));
+        return __builtin_bit_cast(Half, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(m + at + (r0 * pitch + c0))));
     }
     static __device__ __forceinline__ unsigned exponents(u32x4 w) {
         unsigned m = 0;
@@ -149,11 +150,11 @@ struct Ops<float> {
     }
     static __device__ __forceinline__ void split(f32x4 v, Half (&t)[kTerms]) { t[0] = v; }
     static __device__ __forceinline__ int column(int, int c) { return c; }
-    static __device__ __forceinline__ Half row_half(const float* m, int pitch, int row, int c) {
-        return *reinterpret_cast<const f32x4*>(m + row * pitch + c);
+    static __device__ __forceinline__ Half row_half(const float* m, int pitch, int row, int t, int g4) {
+        return *reinterpret_cast<const f32x4*>(m + (row * pitch + g4) + t);
     }
     static __device__ __forceinline__ Half col_half(const float* m, int pitch, int r0, int c0, int lane) {
-        const float* p = m + (r0 + 4 * (lane >> 4)) * pitch + c0 + (lane & 15);
+        const float* p = m + (4 * (lane >> 4) * pitch + (lane & 15)) + (r0 * pitch + c0);
         return f32x4{p[0], p[pitch], p[2 * pitch], p[3 * pitch]};
     }
     static __device__ __forceinline__ unsigned exponents(u32x4 w) {
@@ -376,7 +377,7 @@ __device__ __forceinline__ f32x4 score_tile(const T* b, int pitch, int jt, int l
     for (int s = 0; s < DK / 32; ++s) {
         Half c0, c1;
         c_pair(s, c0, c1);
-        sc = Ops<T>::mma(Ops<T>::row_half(b, pitch, row, 32 * s + g4), Ops<T>::row_half(b, pitch, row, 32 * s + 16 + g4), c0, c1, sc);
+        sc = Ops<T>::mma(Ops<T>::row_half(b, pitch, row, 32 * s, g4), Ops<T>::row_half(b, pitch, row, 32 * s + 16, g4), c0, c1, sc);
     }
     return sc;
 }
@@ -394,16 +395,16 @@ struct HeadSmem {
     int bad[2];              // chunk + 1 where its x holds a non-finite value
 };
 
-template <typename T, int DK, int DV>
-__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void ssm_head_kernel(SsmArgs a) {
+template <typename T, int DK, int DV, int CT>
+__global__ __launch_bounds__(4 * DV / CT, sizeof(T) == 2 ? DV / CT / 32 : 1) void ssm_head_kernel(SsmArgs a) {
     typedef typename Ops<T>::Half Half;
     typedef HeadSmem<T, DK, DV> SM;
-    constexpr int CT = DV / 64, NT = DK / 16, TT = kC / 16, TERMS = Ops<T>::kTerms;
+    constexpr int NW = DV / (16 * CT), TH = 64 * NW, NT = DK / 16, TT = kC / 16, TERMS = Ops<T>::kTerms;
     __shared__ SM sm;
     const int unit = (int)xcd_run(blockIdx.x), i = unit / a.H_v, h = unit - i * a.H_v;
     const int kh = h / (a.H_v / a.H_k);
     const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int li = lane & 15, g4 = 4 * (lane >> 4), col0 = (DV / 4) * wv;
+    const int li = lane & 15, g4 = 4 * (lane >> 4), col0 = 16 * CT * wv;
     const size_t state = (size_t)a.H_v * DK * DV;
     const Walk walk(a, i);
     const float A = a.A[h], bias = a.dt_bias ? a.dt_bias[h] : 0.f, D = a.D ? a.D[h] : 0.f;
@@ -411,7 +412,10 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void ssm_head_kernel(S
 
     // S[nt][ct]: rows 16 nt + g4 + e, column col0 + 16 ct + li
     f32x4 S[NT][CT];
-    auto at = [&](int nt, int ct, int e) { return (size_t)(16 * nt + g4 + e) * DV + col0 + 16 * ct + li; };
+    // (a uniform address for each element beside one offset per lane: the alternative keeps
+    // an address per element in registers)
+    const unsigned mine = (unsigned)(g4 * DV + col0 + li);
+    auto at = [](int nt, int ct, int e) { return (16 * nt + e) * DV + 16 * ct; };
     const int sin = a.init_slot[i];
     const bool have = sin >= 0 && sin < a.num_slots;
     {
@@ -421,7 +425,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void ssm_head_kernel(S
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) S[nt][ct][e] = have ? src[at(nt, ct, e)] : 0.f;
+                for (int e = 0; e < 4; ++e) S[nt][ct][e] = have ? (src + at(nt, ct, e))[mine] : 0.f;
         // waited for here, once: inside the loop the wait would also take in the prefetches
         __builtin_amdgcn_s_waitcnt(0x0F70);
     }
@@ -432,11 +436,11 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void ssm_head_kernel(S
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) dst[at(nt, ct, e)] = S[nt][ct][e];
+                for (int e = 0; e < 4; ++e) (dst + at(nt, ct, e))[mine] = S[nt][ct][e];
     };
 
-    Staged<T, DK, 256> sb, sc;
-    Staged<T, DV, 256> sx;
+    Staged<T, DK, TH> sb, sc;
+    Staged<T, DV, TH> sx;
     float dt_next = 0.f;
     auto fetch = [&](int c) {
         int64_t row;
@@ -460,7 +464,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void ssm_head_kernel(S
     };
     if (tid < 2) sm.bad[tid] = 0;
     fetch(0);
-    if (wv == 3) {                       // the last wave makes the gates, a chunk ahead
+    if (wv == NW - 1) {                       // the last wave makes the gates, a chunk ahead
         fetch_dt(0);
         gates(0);
         fetch_dt(1);
@@ -477,14 +481,15 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void ssm_head_kernel(S
         fetch(c + 1);
         // lower tiles of W, in turn
 #pragma unroll
-        for (int k = 0; k < 3; ++k) {
-            const int blk = wv + 4 * k;
+        for (int k = 0; k < (10 + NW - 1) / NW; ++k) {
+            const int blk = wv + NW * k;
             if (blk < 10) {
                 const int it = blk >= 6 ? 3 : blk >= 3 ? 2 : blk >= 1 ? 1 : 0, jt = blk - it * (it + 1) / 2;
                 const T* cb = sm.c + it * 16 * DK;
                 const f32x4 s = score_tile<T, DK>(sm.b, SM::BP, jt, lane, [&](int p, Half& h0, Half& h1) { pair_of<T>(cb, p, lane, h0, h1); });
                 *reinterpret_cast<Half*>(sm.w + blk * 256 + lane * 4) = decayed<T>(g, s, it, jt, lane);
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
         // Y^T = S^T C^T, then the rows' e^G
         f32x4 y[TT][CT];
@@ -507,6 +512,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void ssm_head_kernel(S
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) y[it][ct] = Ops<T>::mma(s0[ct], s1[ct], c0, c1, y[it][ct]);
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
         for (int it = 0; it < TT; ++it) {
@@ -516,7 +522,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void ssm_head_kernel(S
 #pragma unroll
                 for (int e = 0; e < 4; ++e) y[it][ct][e] *= eg;
         }
-        if (wv == 3) {
+        if (wv == NW - 1) {
             gates(c + 1);
             fetch_dt(c + 2);
         }
@@ -527,31 +533,6 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void ssm_head_kernel(S
         for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
             for (int t = 0; t < TT; ++t) x[ct][t] = Ops<T>::col_half(sm.x, SM::XP, 16 * t, col0 + 16 * ct, lane);
-        // S <- e^(G_last) S + B^T (w X)
-        const float decay = g.eg[kC - 1];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) S[nt][ct][e] *= decay;
-#pragma unroll
-        for (int s = 0; s < TT / 2; ++s) {
-            Half v0[CT][TERMS], v1[CT][TERMS];
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) {
-                weighted<T>(g, x[ct][2 * s], 2 * s, lane, v0[ct]);
-                weighted<T>(g, x[ct][2 * s + 1], 2 * s + 1, lane, v1[ct]);
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const Half b0 = Ops<T>::col_half(sm.b, SM::BP, 32 * s, 16 * nt, lane), b1 = Ops<T>::col_half(sm.b, SM::BP, 32 * s + 16, 16 * nt, lane);
-#pragma unroll
-                for (int k = 0; k < TERMS; ++k)
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) S[nt][ct] = Ops<T>::mma(b0, b1, v0[ct][k], v1[ct][k], S[nt][ct]);
-            }
-        }
         int bad[CT];
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) bad[ct] = kC;
@@ -577,7 +558,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void ssm_head_kernel(S
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
                 const int t = 16 * it + li, p = col0 + 16 * ct + g4;
-                const f32x4 xt = Ops<T>::widen(Ops<T>::row_half(sm.x, SM::XP, t, p));
+                const f32x4 xt = Ops<T>::widen(Ops<T>::row_half(sm.x, SM::XP, t, col0 + 16 * ct, g4));
                 f32x4 o;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[e] = fmaf(a.scale, y[it][ct][e], D * xt[e]);
@@ -587,6 +568,38 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void ssm_head_kernel(S
                         if (__shfl(bad[ct], g4 + e) <= t) o[e] = __builtin_nanf("");
                 Ops<T>::store_half(Ops<T>::round(o), ry, t * vrow + p * (int)sizeof(T));
             }
+        __builtin_amdgcn_sched_barrier(0);
+        // S <- e^(G_last) S + B^T (w X), x as it came
+        if (sm.bad[c & 1] == c + 1)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int t = 0; t < TT; ++t) x[ct][t] = Ops<T>::col_half(sm.x, SM::XP, 16 * t, col0 + 16 * ct, lane);
+        const float decay = g.eg[kC - 1];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) S[nt][ct][e] *= decay;
+#pragma unroll
+        for (int s = 0; s < TT / 2; ++s) {
+            Half v0[CT][TERMS], v1[CT][TERMS];
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                weighted<T>(g, x[ct][2 * s], 2 * s, lane, v0[ct]);
+                weighted<T>(g, x[ct][2 * s + 1], 2 * s + 1, lane, v1[ct]);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const Half b0 = Ops<T>::col_half(sm.b, SM::BP, 32 * s, 16 * nt, lane), b1 = Ops<T>::col_half(sm.b, SM::BP, 32 * s + 16, 16 * nt, lane);
+#pragma unroll
+                for (int k = 0; k < TERMS; ++k)
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) S[nt][ct] = Ops<T>::mma(b0, b1, v0[ct][k], v1[ct][k], S[nt][ct]);
+                if (nt % 2 == 1) __builtin_amdgcn_sched_barrier(0);
+            }
+        }
         float* dst = walk.export_to(a, i, c, state);
         if (dst) put(dst);
         dev::lds_barrier();
@@ -628,13 +641,14 @@ __global__ __launch_bounds__(512, 2) void ssm_strip_kernel(SsmArgs a) {
     const int krow = a.H_k * DK * (int)sizeof(T), vrow = a.H_v * DV * (int)sizeof(T);
 
     f32x4 S[NT];                         // rows 16 (NT wv + nt) + g4 + e, column col0 + li
-    auto at = [&](int nt, int e) { return (size_t)(16 * (NT * wv + nt) + g4 + e) * DV + col0 + li; };
+    const unsigned mine = (unsigned)((16 * NT * wv + g4) * DV + col0 + li);
+    auto at = [](int nt, int e) { return (16 * nt + e) * DV; };
     auto put = [&](float* dst) {
         dst += (size_t)h * DK * DV;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) dst[at(nt, e)] = S[nt][e];
+            for (int e = 0; e < 4; ++e) (dst + at(nt, e))[mine] = S[nt][e];
     };
     auto share = [&](int parity) {       // a lane's half of tile t in operand order
 #pragma unroll
@@ -718,7 +732,7 @@ __global__ __launch_bounds__(512, 2) void ssm_strip_kernel(SsmArgs a) {
             walk.span(c, row, n);
             const rsrc_t ry = head_rows<T>(a.y, row, n, a.H_v, h, DV, col0, kStrip);
             const int t = 16 * wv + li;
-            const f32x4 xt = Ops<T>::widen(Ops<T>::row_half(sm.x[p], SM::XP, t, g4));
+            const f32x4 xt = Ops<T>::widen(Ops<T>::row_half(sm.x[p], SM::XP, t, 0, g4));
             f32x4 o;
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[e] = fmaf(a.scale, y[e], D * xt[e]);
@@ -766,7 +780,7 @@ __global__ __launch_bounds__(512, 2) void ssm_strip_kernel(SsmArgs a) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) S[nt][e] = have ? src[at(nt, e)] : 0.f;
+            for (int e = 0; e < 4; ++e) S[nt][e] = have ? (src + at(nt, e))[mine] : 0.f;
         share(0);
     }
     __syncthreads();
@@ -857,12 +871,13 @@ hipError_t decode_typed(const SsmArgs& a, hipStream_t stream) {
 
 template <typename T, int DK, int DV>
 hipError_t prefill_typed(const SsmArgs& a, hipStream_t stream) {
+    constexpr int CT = DV / 64;
     const int64_t chains = (int64_t)a.num_seqs * a.H_v;
     // Strips while they, at one workgroup each, do not outnumber the compute units by far.
     if (chains * (DV / kStrip) <= 4 * (int64_t)device_cus())
         hipLaunchKernelGGL((ssm_strip_kernel<T, DK, DV>), dim3((unsigned)(chains * (DV / kStrip))), dim3(512), 0, stream, a);
     else
-        hipLaunchKernelGGL((ssm_head_kernel<T, DK, DV>), dim3((unsigned)chains), dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((ssm_head_kernel<T, DK, DV, CT>), dim3((unsigned)chains), dim3(4 * DV / CT), 0, stream, a);
     return hipGetLastError();
 }
 
