@@ -278,17 +278,30 @@ struct Walk {
         n = c < chunks ? e - b : 0;
         row = lo + (n > 0 ? b : 0);
     }
-    // where the state after chunk c is exported, or NULL
-    __device__ __forceinline__ float* export_to(const SsmArgs& a, int i, int c, size_t state) const {
-        if (a.export_grid <= 0) return nullptr;
+    // local position after chunk c
+    __device__ __forceinline__ int end_of(int c) const {
         int b, e;
         dev::chunk_span(c, skew, len, b, e);
-        const int64_t pos = start + e;
-        if (pos % a.export_grid != 0) return nullptr;
-        const int64_t idx = (int64_t)a.export_offsets[i] + pos / a.export_grid - start / a.export_grid - 1;
-        if (idx < 0 || idx >= a.export_capacity) return nullptr;
-        if (!a.export_slots) return a.export_states + (size_t)idx * state;
-        const int sl = a.export_slots[idx];
+        return e;
+    }
+};
+
+// The states on the export grid, in order: chunks end at every one of its positions.
+struct Exports {
+    int64_t next, idx;      // local position of the next one (past any sequence without a grid), its place in the list
+    __device__ __forceinline__ Exports(const SsmArgs& a, const Walk& walk, int i) {
+        const bool any = a.export_grid > 0 && walk.chunks > 0;
+        next = any ? (walk.start / a.export_grid + 1) * a.export_grid - walk.start : INT64_MAX;
+        idx = any ? a.export_offsets[i] : 0;
+    }
+    // called after every chunk with its end: where the state goes, or NULL
+    __device__ __forceinline__ float* take(const SsmArgs& a, int end, size_t state) {
+        if (end != next) return nullptr;
+        const int64_t at = idx++;
+        next += a.export_grid;
+        if (at < 0 || at >= a.export_capacity) return nullptr;
+        if (!a.export_slots) return a.export_states + (size_t)at * state;
+        const int sl = a.export_slots[at];
         return sl >= 0 && sl < a.num_slots ? a.pool + (size_t)sl * state : nullptr;
     }
 };
@@ -306,6 +319,12 @@ __device__ __forceinline__ rsrc_t head_rows(const void* base, int64_t row, int n
     return rows_rsrc(p, n > 0 ? (int)(((size_t)(n - 1) * heads * width + columns) * sizeof(T)) : 0);
 }
 
+// dt of row + lane, 0 from n on.
+__device__ __forceinline__ float load_step(const SsmArgs& a, int64_t row, int n, int h, int lane) {
+    const rsrc_t r = rows_rsrc(a.dt + (size_t)row * a.H_v + h, n > 0 ? ((n - 1) * a.H_v + 1) * 4 : 0);
+    return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, lane * a.H_v * 4, 0, 0));
+}
+
 // A 64 x N block on its way from memory to LDS through the registers of TH threads.
 template <typename T, int N, int TH>
 struct Staged {
@@ -317,7 +336,7 @@ struct Staged {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int u = tid + k * TH;
-            if (VECS % TH == 0 || u < VECS) v[k] = load16(r, (u / PER_ROW) * row_bytes + (u % PER_ROW) * 16);
+            v[k] = load16(r, (u / PER_ROW) * row_bytes + (u % PER_ROW) * 16);      // past the block: past the buffer's end too
         }
     }
     // row-major, rows swizzled as Ops<T>::column says
@@ -454,7 +473,7 @@ __global__ __launch_bounds__(4 * DV / CT, sizeof(T) == 2 ? DV / CT / 32 : 1) voi
         int64_t row;
         int n;
         walk.span(c, row, n);
-        dt_next = lane < n ? a.dt[(size_t)(row + lane) * a.H_v + h] : 0.f;
+        dt_next = load_step(a, row, n, h, lane);
     };
     auto gates = [&](int c) {
         int64_t row;
@@ -471,6 +490,7 @@ __global__ __launch_bounds__(4 * DV / CT, sizeof(T) == 2 ? DV / CT / 32 : 1) voi
     }
     __syncthreads();
 
+    Exports exports(a, walk, i);
     for (int c = 0; c < walk.chunks; ++c) {
         const Gates& g = sm.gate[c & 1];
         sb.store(sm.b, SM::BP, tid);
@@ -600,7 +620,7 @@ __global__ __launch_bounds__(4 * DV / CT, sizeof(T) == 2 ? DV / CT / 32 : 1) voi
                 if (nt % 2 == 1) __builtin_amdgcn_sched_barrier(0);
             }
         }
-        float* dst = walk.export_to(a, i, c, state);
+        float* dst = exports.take(a, walk.end_of(c), state);
         if (dst) put(dst);
         dev::lds_barrier();
     }
@@ -632,7 +652,6 @@ __global__ __launch_bounds__(512, 2) void ssm_strip_kernel(SsmArgs a) {
     const int col0 = kStrip * (int)(wg % NS), unit = (int)(wg / NS), i = unit / a.H_v, h = unit - i * a.H_v;
     const int kh = h / (a.H_v / a.H_k);
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const bool forms_y = wave < 4;
     const int wv = wave & 3;             // its quarter of the tokens or of the state's rows
     const int li = lane & 15, g4 = 4 * (lane >> 4);
     const size_t state = (size_t)a.H_v * DK * DV;
@@ -640,83 +659,42 @@ __global__ __launch_bounds__(512, 2) void ssm_strip_kernel(SsmArgs a) {
     const float A = a.A[h], bias = a.dt_bias ? a.dt_bias[h] : 0.f, D = a.D ? a.D[h] : 0.f;
     const int krow = a.H_k * DK * (int)sizeof(T), vrow = a.H_v * DV * (int)sizeof(T);
 
-    f32x4 S[NT];                         // rows 16 (NT wv + nt) + g4 + e, column col0 + li
-    const unsigned mine = (unsigned)((16 * NT * wv + g4) * DV + col0 + li);
-    auto at = [](int nt, int e) { return (16 * nt + e) * DV; };
-    auto put = [&](float* dst) {
-        dst += (size_t)h * DK * DV;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) (dst + at(nt, e))[mine] = S[nt][e];
-    };
-    auto share = [&](int parity) {       // a lane's half of tile t in operand order
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int t = NT * wv + nt;
-            T* p = sizeof(T) == 2 ? sm.s[parity] + (t >> 1) * 512 + lane * 8 + (t & 1) * 4 : sm.s[parity] + t * 256 + lane * 4;
-            *reinterpret_cast<Half*>(p) = Ops<T>::round(S[nt]);
-        }
-    };
-
-    // Loads run two chunks ahead of their use, in two register sets by chunk parity.
-    Staged<T, DK, 512> sb[2];
-    Staged<T, kStrip, 512> sx[2];
-    Half cf[2][2 * PAIRS];
-    float dts[2];
-    auto fetch = [&](int c, int p) {
-        int64_t row;
-        int n;
-        walk.span(c, row, n);
-        sb[p].load(head_rows<T>(a.b, row, n, a.H_k, kh, DK, 0, DK), krow, tid);
-        sx[p].load(head_rows<T>(a.x, row, n, a.H_v, h, DV, col0, kStrip), vrow, tid);
-        if (wave == 0) dts[p] = lane < n ? a.dt[(size_t)(row + lane) * a.H_v + h] : 0.f;
-    };
-    auto fetch_c = [&](int c, int p) {
-        int64_t row;
-        int n;
-        walk.span(c, row, n);
-        const rsrc_t r = head_rows<T>(a.c, row, n, a.H_k, kh, DK, 0, DK);
-#pragma unroll
-        for (int t = 0; t < 2 * PAIRS; ++t) cf[p][t] = Ops<T>::load_half(r, (16 * wv + li) * krow + (16 * t + g4) * (int)sizeof(T));
-    };
-    auto stage = [&](int c, int p) {
-        sb[p].store(sm.b[p], SM::BP, tid);
-        sx[p].store(sm.x[p], SM::XP, tid);
-        if (sx[p].any_not_finite(tid)) sm.bad[p] = c + 1;
-        if (wave == 0) {
+    // The two halves of the workgroup run loops of their own between the same barriers, so that
+    // the waits of each count its own loads and stores alone.  Loads run two chunks ahead of
+    // their use, in two register sets by chunk parity; an odd count of chunks is made even by
+    // one without tokens, which changes nothing.
+    if (tid < 2) sm.bad[tid] = 0;
+    if (wave < 4) {
+        Half cf[2][2 * PAIRS];
+        auto fetch_c = [&](int c, int p) {
             int64_t row;
             int n;
             walk.span(c, row, n);
-            make_gates(sm.gate[p], dts[p], bias, A, a.dt_softplus, n, lane);
-        }
-    };
-    auto body = [&](int c, int p) {
-        stage(c + 1, p ^ 1);
-        fetch(c + 3, p ^ 1);
-        const Gates& g = sm.gate[p];
-        Half x[TT];
+            const rsrc_t r = head_rows<T>(a.c, row, n, a.H_k, kh, DK, 0, DK);
 #pragma unroll
-        for (int t = 0; t < TT; ++t) x[t] = Ops<T>::col_half(sm.x[p], SM::XP, 16 * t, 0, lane);
-        if (forms_y) {
-            Half w[TT];
+            for (int t = 0; t < 2 * PAIRS; ++t) cf[p][t] = Ops<T>::load_half(r, (16 * wv + li) * krow + (16 * t + g4) * (int)sizeof(T));
+        };
+        auto body = [&](int c, int p) {
+            const Gates& g = sm.gate[p];
+            Half x[TT], w[TT];
 #pragma unroll
-            for (int jt = 0; jt < TT; ++jt) {
-                w[jt] = Half{};
-                if (jt <= wv) {
-                    const f32x4 s = score_tile<T, DK>(sm.b[p], SM::BP, jt, lane, [&](int q, Half& h0, Half& h1) {
-                        h0 = cf[p][2 * q];
-                        h1 = cf[p][2 * q + 1];
-                    });
-                    w[jt] = decayed<T>(g, s, wv, jt, lane);
-                }
-            }
+            for (int t = 0; t < TT; ++t) x[t] = Ops<T>::col_half(sm.x[p], SM::XP, 16 * t, 0, lane);
             f32x4 y = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int s = 0; s < PAIRS; ++s) {
                 Half s0, s1;
                 pair_of<T>(sm.s[p], s, lane, s0, s1);
                 y = Ops<T>::mma(s0, s1, cf[p][2 * s], cf[p][2 * s + 1], y);
+            }
+            // every wave forms four tiles, those past its diagonal as zeros: without branches
+            // their chains of products overlap
+#pragma unroll
+            for (int jt = 0; jt < TT; ++jt) {
+                const f32x4 s = score_tile<T, DK>(sm.b[p], SM::BP, jt, lane, [&](int q, Half& h0, Half& h1) {
+                    h0 = cf[p][2 * q];
+                    h1 = cf[p][2 * q + 1];
+                });
+                w[jt] = decayed<T>(g, s, wv, jt, lane);
             }
             fetch_c(c + 2, p);
             const float eg = g.eg[16 * wv + li];
@@ -741,39 +719,95 @@ __global__ __launch_bounds__(512, 2) void ssm_strip_kernel(SsmArgs a) {
                 for (int e = 0; e < 4; ++e)
                     if (__shfl(bad, g4 + e) <= t) o[e] = __builtin_nanf("");
             Ops<T>::store_half(Ops<T>::round(o), ry, t * vrow + g4 * (int)sizeof(T));
-        } else {
-            const float decay = g.eg[kC - 1];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) S[nt][e] *= decay;
-#pragma unroll
-            for (int s = 0; s < TT / 2; ++s) {
-                Half v0[TERMS], v1[TERMS];
-                weighted<T>(g, x[2 * s], 2 * s, lane, v0);
-                weighted<T>(g, x[2 * s + 1], 2 * s + 1, lane, v1);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const int n0 = 16 * (NT * wv + nt);
-                    const Half b0 = Ops<T>::col_half(sm.b[p], SM::BP, 32 * s, n0, lane), b1 = Ops<T>::col_half(sm.b[p], SM::BP, 32 * s + 16, n0, lane);
-#pragma unroll
-                    for (int k = 0; k < TERMS; ++k) S[nt] = Ops<T>::mma(b0, b1, v0[k], v1[k], S[nt]);
-                }
-            }
-            share(p ^ 1);
-            float* dst = walk.export_to(a, i, c, state);
-            if (dst) put(dst);
+            dev::lds_barrier();
+        };
+        fetch_c(0, 0);
+        fetch_c(1, 1);
+        __syncthreads();
+        dev::lds_barrier();
+        for (int c = 0; c < walk.chunks; c += 2) {
+            body(c, 0);
+            body(c + 1, 1);
         }
+        return;
+    }
+
+    const int htid = tid - 256;
+    Staged<T, DK, 256> sb[2];
+    Staged<T, kStrip, 256> sx[2];
+    float dts[2];
+    auto fetch = [&](int c, int p) {
+        int64_t row;
+        int n;
+        walk.span(c, row, n);
+        sb[p].load(head_rows<T>(a.b, row, n, a.H_k, kh, DK, 0, DK), krow, htid);
+        sx[p].load(head_rows<T>(a.x, row, n, a.H_v, h, DV, col0, kStrip), vrow, htid);
+        dts[p] = load_step(a, row, n, h, lane);
+    };
+    auto stage = [&](int c, int p) {
+        sb[p].store(sm.b[p], SM::BP, htid);
+        sx[p].store(sm.x[p], SM::XP, htid);
+        if (sx[p].any_not_finite(htid)) sm.bad[p] = c + 1;
+        if (wv == 3) {
+            int64_t row;
+            int n;
+            walk.span(c, row, n);
+            make_gates(sm.gate[p], dts[p], bias, A, a.dt_softplus, n, lane);
+        }
+    };
+    f32x4 S[NT];                         // rows 16 (NT wv + nt) + g4 + e, column col0 + li
+    const unsigned mine = (unsigned)((16 * NT * wv + g4) * DV + col0 + li);
+    auto at = [](int nt, int e) { return (16 * nt + e) * DV; };
+    auto put = [&](float* dst) {
+        dst += (size_t)h * DK * DV;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) (dst + at(nt, e))[mine] = S[nt][e];
+    };
+    auto share = [&](int parity) {       // a lane's half of tile t in operand order
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int t = NT * wv + nt;
+            T* p = sizeof(T) == 2 ? sm.s[parity] + (t >> 1) * 512 + lane * 8 + (t & 1) * 4 : sm.s[parity] + t * 256 + lane * 4;
+            *reinterpret_cast<Half*>(p) = Ops<T>::round(S[nt]);
+        }
+    };
+    Exports exports(a, walk, i);
+    auto body = [&](int c, int p) {
+        const Gates& g = sm.gate[p];
+        Half x[TT];
+#pragma unroll
+        for (int t = 0; t < TT; ++t) x[t] = Ops<T>::col_half(sm.x[p], SM::XP, 16 * t, 0, lane);
+        const float decay = g.eg[kC - 1];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) S[nt][e] *= decay;
+#pragma unroll
+        for (int s = 0; s < TT / 2; ++s) {
+            Half v0[TERMS], v1[TERMS];
+            weighted<T>(g, x[2 * s], 2 * s, lane, v0);
+            weighted<T>(g, x[2 * s + 1], 2 * s + 1, lane, v1);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const int n0 = 16 * (NT * wv + nt);
+                const Half b0 = Ops<T>::col_half(sm.b[p], SM::BP, 32 * s, n0, lane), b1 = Ops<T>::col_half(sm.b[p], SM::BP, 32 * s + 16, n0, lane);
+#pragma unroll
+                for (int k = 0; k < TERMS; ++k) S[nt] = Ops<T>::mma(b0, b1, v0[k], v1[k], S[nt]);
+            }
+        }
+        stage(c + 1, p ^ 1);
+        fetch(c + 3, p ^ 1);
+        share(p ^ 1);
+        float* dst = exports.take(a, walk.end_of(c), state);
+        if (dst) put(dst);
         dev::lds_barrier();
     };
 
-    if (tid < 2) sm.bad[tid] = 0;
     fetch(0, 0);
     fetch(1, 1);
-    if (forms_y) {
-        fetch_c(0, 0);
-        fetch_c(1, 1);
-    } else {
+    {
         const int sin = a.init_slot[i];
         const bool have = sin >= 0 && sin < a.num_slots;
         const float* src = have ? a.pool + (size_t)sin * state + (size_t)h * DK * DV : nullptr;
@@ -781,18 +815,18 @@ __global__ __launch_bounds__(512, 2) void ssm_strip_kernel(SsmArgs a) {
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) S[nt][e] = have ? (src + at(nt, e))[mine] : 0.f;
-        share(0);
     }
+    share(0);
     __syncthreads();
     stage(0, 0);
     fetch(2, 0);
     dev::lds_barrier();
     for (int c = 0; c < walk.chunks; c += 2) {
         body(c, 0);
-        if (c + 1 < walk.chunks) body(c + 1, 1);
+        body(c + 1, 1);
     }
     const int fin = a.final_slot[i];
-    if (!forms_y && fin >= 0 && fin < a.num_slots) put(a.pool + (size_t)fin * state);
+    if (fin >= 0 && fin < a.num_slots) put(a.pool + (size_t)fin * state);
 }
 
 // ---------------------------------------------------------------- decode
