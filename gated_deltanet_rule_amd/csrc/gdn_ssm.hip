@@ -631,19 +631,24 @@ __global__ __launch_bounds__(4 * DV / CT, sizeof(T) == 2 ? DV / CT / 32 : 1) voi
 // ---------------------------------------------------------------- strips
 
 constexpr int kStrip = 16;
+constexpr int kStripThreads = 768;
 
 template <typename T, int DK>
 struct StripSmem {
     static constexpr int BP = DK + Ops<T>::kPad, XP = kStrip + (sizeof(T) == 4 ? 4 : 0);
-    alignas(16) T b[2][kC * BP];          // by chunk parity, as all of it
+    // C comes from LDS (operand order) where it fits beside the rest, else each wave loads its own
+    static constexpr bool kStageC = sizeof(T) == 2;
+    alignas(16) T b[2][kC * BP];                    // by chunk parity, as all but the gates
+    T c[2][kStageC ? kC * DK : 8];
     T x[2][kC * XP];
-    T s[2][DK * kStrip];      // the state as operand, rounded to T
-    Gates gate[2];
+    T v[2][Ops<T>::kTerms][kC * XP];      // e^(G_last - G) d x, in parts
+    T s[2][DK * kStrip];                  // the state as operand, rounded to T
+    Gates gate[4];                        // by chunk modulo 4: made two chunks ahead
     int bad[2];
 };
 
 template <typename T, int DK, int DV>
-__global__ __launch_bounds__(512, 2) void ssm_strip_kernel(SsmArgs a) {
+__global__ __launch_bounds__(kStripThreads, 3) void ssm_strip_kernel(SsmArgs a) {
     typedef typename Ops<T>::Half Half;
     typedef StripSmem<T, DK> SM;
     constexpr int NT = DK / 64, TT = kC / 16, TERMS = Ops<T>::kTerms, NS = DV / kStrip, PAIRS = DK / 32;
@@ -652,31 +657,36 @@ __global__ __launch_bounds__(512, 2) void ssm_strip_kernel(SsmArgs a) {
     const int col0 = kStrip * (int)(wg % NS), unit = (int)(wg / NS), i = unit / a.H_v, h = unit - i * a.H_v;
     const int kh = h / (a.H_v / a.H_k);
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wv = wave & 3;             // its quarter of the tokens or of the state's rows
+    const int wv = wave & 3;             // its quarter of the tokens, of the state's rows, of the staging
     const int li = lane & 15, g4 = 4 * (lane >> 4);
     const size_t state = (size_t)a.H_v * DK * DV;
     const Walk walk(a, i);
-    const float A = a.A[h], bias = a.dt_bias ? a.dt_bias[h] : 0.f, D = a.D ? a.D[h] : 0.f;
     const int krow = a.H_k * DK * (int)sizeof(T), vrow = a.H_v * DV * (int)sizeof(T);
 
-    // The two halves of the workgroup run loops of their own between the same barriers, so that
-    // the waits of each count its own loads and stores alone.  Loads run two chunks ahead of
-    // their use, in two register sets by chunk parity; an odd count of chunks is made even by
-    // one without tokens, which changes nothing.
+    // Three groups of four waves run loops of their own between the same barriers (so that the
+    // waits of each count its own loads and stores alone): one forms Y of chunk c, one advances
+    // S over it and makes the gates of chunk c + 2, one stages chunk c + 1.  Loads run two
+    // chunks ahead of their use, in two register sets by chunk parity; an odd count of chunks
+    // is made even by one without tokens, which changes nothing.
     if (tid < 2) sm.bad[tid] = 0;
     if (wave < 4) {
+        const float D = a.D ? a.D[h] : 0.f;
         Half cf[2][2 * PAIRS];
         auto fetch_c = [&](int c, int p) {
             int64_t row;
             int n;
             walk.span(c, row, n);
             const rsrc_t r = head_rows<T>(a.c, row, n, a.H_k, kh, DK, 0, DK);
+            if constexpr (!SM::kStageC)
 #pragma unroll
-            for (int t = 0; t < 2 * PAIRS; ++t) cf[p][t] = Ops<T>::load_half(r, (16 * wv + li) * krow + (16 * t + g4) * (int)sizeof(T));
+                for (int t = 0; t < 2 * PAIRS; ++t) cf[p][t] = Ops<T>::load_half(r, (16 * wv + li) * krow + (16 * t + g4) * (int)sizeof(T));
         };
         auto body = [&](int c, int p) {
-            const Gates& g = sm.gate[p];
+            const Gates& g = sm.gate[c & 3];
             Half x[TT], w[TT];
+            if constexpr (SM::kStageC)
+#pragma unroll
+                for (int s = 0; s < PAIRS; ++s) pair_of<T>(sm.c[p] + wv * 16 * DK, s, lane, cf[p][2 * s], cf[p][2 * s + 1]);
 #pragma unroll
             for (int t = 0; t < TT; ++t) x[t] = Ops<T>::col_half(sm.x[p], SM::XP, 16 * t, 0, lane);
             f32x4 y = {0.f, 0.f, 0.f, 0.f};
@@ -732,82 +742,70 @@ __global__ __launch_bounds__(512, 2) void ssm_strip_kernel(SsmArgs a) {
         return;
     }
 
-    const int htid = tid - 256;
-    Staged<T, DK, 256> sb[2];
-    Staged<T, kStrip, 256> sx[2];
-    float dts[2];
-    auto fetch = [&](int c, int p) {
-        int64_t row;
-        int n;
-        walk.span(c, row, n);
-        sb[p].load(head_rows<T>(a.b, row, n, a.H_k, kh, DK, 0, DK), krow, htid);
-        sx[p].load(head_rows<T>(a.x, row, n, a.H_v, h, DV, col0, kStrip), vrow, htid);
-        dts[p] = load_step(a, row, n, h, lane);
-    };
-    auto stage = [&](int c, int p) {
-        sb[p].store(sm.b[p], SM::BP, htid);
-        sx[p].store(sm.x[p], SM::XP, htid);
-        if (sx[p].any_not_finite(htid)) sm.bad[p] = c + 1;
-        if (wv == 3) {
+    if (wave < 8) {
+        f32x4 S[NT];                         // rows 16 (NT wv + nt) + g4 + e, column col0 + li
+        const unsigned mine = (unsigned)((16 * NT * wv + g4) * DV + col0 + li);
+        auto at = [](int nt, int e) { return (16 * nt + e) * DV; };
+        auto put = [&](float* dst) {
+            dst += (size_t)h * DK * DV;
+    #pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+    #pragma unroll
+                for (int e = 0; e < 4; ++e) (dst + at(nt, e))[mine] = S[nt][e];
+        };
+        auto share = [&](int parity) {       // a lane's half of tile t in operand order
+    #pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const int t = NT * wv + nt;
+                T* p = sizeof(T) == 2 ? sm.s[parity] + (t >> 1) * 512 + lane * 8 + (t & 1) * 4 : sm.s[parity] + t * 256 + lane * 4;
+                *reinterpret_cast<Half*>(p) = Ops<T>::round(S[nt]);
+            }
+        };
+        // its first wave makes the gates
+        const float A = a.A[h], bias = a.dt_bias ? a.dt_bias[h] : 0.f;
+        float dts[2];
+        auto fetch_dt = [&](int c, int p) {
             int64_t row;
             int n;
             walk.span(c, row, n);
-            make_gates(sm.gate[p], dts[p], bias, A, a.dt_softplus, n, lane);
-        }
-    };
-    f32x4 S[NT];                         // rows 16 (NT wv + nt) + g4 + e, column col0 + li
-    const unsigned mine = (unsigned)((16 * NT * wv + g4) * DV + col0 + li);
-    auto at = [](int nt, int e) { return (16 * nt + e) * DV; };
-    auto put = [&](float* dst) {
-        dst += (size_t)h * DK * DV;
+            dts[p] = load_step(a, row, wv == 0 ? n : 0, h, lane);
+        };
+        auto gates = [&](int c, int p) {
+            int64_t row;
+            int n;
+            walk.span(c, row, n);
+            if (wv == 0) make_gates(sm.gate[c & 3], dts[p], bias, A, a.dt_softplus, n, lane);
+        };
+        Exports exports(a, walk, i);
+        auto body = [&](int c, int p) {
+            const float decay = sm.gate[c & 3].eg[kC - 1];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) (dst + at(nt, e))[mine] = S[nt][e];
-    };
-    auto share = [&](int parity) {       // a lane's half of tile t in operand order
+                for (int e = 0; e < 4; ++e) S[nt][e] *= decay;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int t = NT * wv + nt;
-            T* p = sizeof(T) == 2 ? sm.s[parity] + (t >> 1) * 512 + lane * 8 + (t & 1) * 4 : sm.s[parity] + t * 256 + lane * 4;
-            *reinterpret_cast<Half*>(p) = Ops<T>::round(S[nt]);
-        }
-    };
-    Exports exports(a, walk, i);
-    auto body = [&](int c, int p) {
-        const Gates& g = sm.gate[p];
-        Half x[TT];
+            for (int s = 0; s < TT / 2; ++s) {
+                Half v0[TERMS], v1[TERMS];
 #pragma unroll
-        for (int t = 0; t < TT; ++t) x[t] = Ops<T>::col_half(sm.x[p], SM::XP, 16 * t, 0, lane);
-        const float decay = g.eg[kC - 1];
+                for (int k = 0; k < TERMS; ++k) {
+                    v0[k] = Ops<T>::col_half(sm.v[p][k], SM::XP, 32 * s, 0, lane);
+                    v1[k] = Ops<T>::col_half(sm.v[p][k], SM::XP, 32 * s + 16, 0, lane);
+                }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt) {
+                    const int n0 = 16 * (NT * wv + nt);
+                    const Half b0 = Ops<T>::col_half(sm.b[p], SM::BP, 32 * s, n0, lane), b1 = Ops<T>::col_half(sm.b[p], SM::BP, 32 * s + 16, n0, lane);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) S[nt][e] *= decay;
-#pragma unroll
-        for (int s = 0; s < TT / 2; ++s) {
-            Half v0[TERMS], v1[TERMS];
-            weighted<T>(g, x[2 * s], 2 * s, lane, v0);
-            weighted<T>(g, x[2 * s + 1], 2 * s + 1, lane, v1);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const int n0 = 16 * (NT * wv + nt);
-                const Half b0 = Ops<T>::col_half(sm.b[p], SM::BP, 32 * s, n0, lane), b1 = Ops<T>::col_half(sm.b[p], SM::BP, 32 * s + 16, n0, lane);
-#pragma unroll
-                for (int k = 0; k < TERMS; ++k) S[nt] = Ops<T>::mma(b0, b1, v0[k], v1[k], S[nt]);
+                    for (int k = 0; k < TERMS; ++k) S[nt] = Ops<T>::mma(b0, b1, v0[k], v1[k], S[nt]);
+                }
             }
-        }
-        stage(c + 1, p ^ 1);
-        fetch(c + 3, p ^ 1);
-        share(p ^ 1);
-        float* dst = exports.take(a, walk.end_of(c), state);
-        if (dst) put(dst);
-        dev::lds_barrier();
-    };
-
-    fetch(0, 0);
-    fetch(1, 1);
-    {
+            share(p ^ 1);
+            gates(c + 2, p);
+            fetch_dt(c + 4, p);
+            float* dst = exports.take(a, walk.end_of(c), state);
+            if (dst) put(dst);
+            dev::lds_barrier();
+        };
         const int sin = a.init_slot[i];
         const bool have = sin >= 0 && sin < a.num_slots;
         const float* src = have ? a.pool + (size_t)sin * state + (size_t)h * DK * DV : nullptr;
@@ -815,8 +813,58 @@ __global__ __launch_bounds__(512, 2) void ssm_strip_kernel(SsmArgs a) {
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) S[nt][e] = have ? (src + at(nt, e))[mine] : 0.f;
+        share(0);
+        fetch_dt(0, 0);
+        fetch_dt(1, 1);
+        gates(0, 0);
+        fetch_dt(2, 0);
+        __syncthreads();
+        gates(1, 1);
+        fetch_dt(3, 1);
+        dev::lds_barrier();
+        for (int c = 0; c < walk.chunks; c += 2) {
+            body(c, 0);
+            body(c + 1, 1);
+        }
+        const int fin = a.final_slot[i];
+        if (fin >= 0 && fin < a.num_slots) put(a.pool + (size_t)fin * state);
+        return;
     }
-    share(0);
+
+    const int ltid = tid - 512, xr = ltid >> 2, xc = 4 * (ltid & 3);      // staging: a row and four columns of x
+    Staged<T, DK, 256> sb[2], sc[2];
+    Half sx[2];
+    auto fetch = [&](int c, int p) {
+        int64_t row;
+        int n;
+        walk.span(c, row, n);
+        sb[p].load(head_rows<T>(a.b, row, n, a.H_k, kh, DK, 0, DK), krow, ltid);
+        if constexpr (SM::kStageC) sc[p].load(head_rows<T>(a.c, row, n, a.H_k, kh, DK, 0, DK), krow, ltid);
+        sx[p] = Ops<T>::load_half(head_rows<T>(a.x, row, n, a.H_v, h, DV, col0, kStrip), xr * vrow + xc * (int)sizeof(T));
+    };
+    auto stage = [&](int c, int p) {
+        const float w = sm.gate[c & 3].w[xr];
+        const int at = xr * SM::XP + Ops<T>::column(xr, xc);
+        sb[p].store(sm.b[p], SM::BP, ltid);
+        if constexpr (SM::kStageC) sc[p].store_operands(sm.c[p], ltid);
+        *reinterpret_cast<Half*>(sm.x[p] + at) = sx[p];
+        f32x4 v = Ops<T>::widen(sx[p]);
+        if (!(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))) < __builtin_inff()) ||
+            !(v[0] == v[0] && v[1] == v[1] && v[2] == v[2] && v[3] == v[3])) sm.bad[p] = c + 1;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] *= w;
+        Half part[TERMS];
+        Ops<T>::split(v, part);
+#pragma unroll
+        for (int k = 0; k < TERMS; ++k) *reinterpret_cast<Half*>(sm.v[p][k] + at) = part[k];
+    };
+    auto body = [&](int c, int p) {
+        stage(c + 1, p ^ 1);
+        fetch(c + 3, p ^ 1);
+        dev::lds_barrier();
+    };
+    fetch(0, 0);
+    fetch(1, 1);
     __syncthreads();
     stage(0, 0);
     fetch(2, 0);
@@ -825,8 +873,6 @@ __global__ __launch_bounds__(512, 2) void ssm_strip_kernel(SsmArgs a) {
         body(c, 0);
         body(c + 1, 1);
     }
-    const int fin = a.final_slot[i];
-    if (fin >= 0 && fin < a.num_slots) put(a.pool + (size_t)fin * state);
 }
 
 // ---------------------------------------------------------------- decode
@@ -909,7 +955,7 @@ hipError_t prefill_typed(const SsmArgs& a, hipStream_t stream) {
     const int64_t chains = (int64_t)a.num_seqs * a.H_v;
     // Strips while they, at one workgroup each, do not outnumber the compute units by far.
     if (chains * (DV / kStrip) <= 4 * (int64_t)device_cus())
-        hipLaunchKernelGGL((ssm_strip_kernel<T, DK, DV>), dim3((unsigned)(chains * (DV / kStrip))), dim3(512), 0, stream, a);
+        hipLaunchKernelGGL((ssm_strip_kernel<T, DK, DV>), dim3((unsigned)(chains * (DV / kStrip))), dim3(kStripThreads), 0, stream, a);
     else
         hipLaunchKernelGGL((ssm_head_kernel<T, DK, DV, CT>), dim3((unsigned)chains), dim3(4 * DV / CT), 0, stream, a);
     return hipGetLastError();
