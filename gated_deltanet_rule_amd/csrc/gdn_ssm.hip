@@ -35,6 +35,8 @@
 // bound by the states' traffic.
 #include <hip/hip_runtime.h>
 
+#include <cstddef>
+
 #include "gdn_device.h"
 #include "gdn_internal.h"
 #include "gdn_layer_device.h"
@@ -630,6 +632,74 @@ __global__ __launch_bounds__(4 * DV / CT, sizeof(T) == 2 ? DV / CT / 32 : 1) voi
 
 // ---------------------------------------------------------------- strips
 
+// The strips of a head, and the heads of a group, need the same scores: a first launch forms W
+// and the decays of every chunk, all chunks side by side, and leaves them in the workspace.
+// Record of a chunk and head:
+template <typename T>
+struct Weights {
+    T w[10 * 256];           // lower tiles of W, a lane's half each
+    float d[kC];             // e^(G_last - G) d
+    float eg[kC];            // e^G
+};
+
+// Records of a sequence start here: far enough from those of the one before, whatever its skew.
+__device__ __forceinline__ int64_t first_record(int lo, int i) { return (lo >> 6) + 2 * (int64_t)i; }
+int64_t record_count(int num_seqs, int64_t total_tokens) { return (total_tokens >> 6) + 2 * (int64_t)num_seqs; }
+
+constexpr int kHeadBatch = 4;     // heads of one workgroup
+
+template <typename T, int DK>
+__global__ __launch_bounds__(256) void ssm_weights_kernel(SsmArgs a) {
+    constexpr int BP = DK + Ops<T>::kPad;
+    typedef typename Ops<T>::Half Half;
+    __shared__ __attribute__((aligned(16))) T smb[kC * BP], smc[kC * DK];
+    __shared__ Gates gate[kHeadBatch];
+    const int R = a.H_v / a.H_k, batches = (R + kHeadBatch - 1) / kHeadBatch;
+    const int64_t record = blockIdx.x / (unsigned)(a.H_k * batches);
+    const int part = (int)(blockIdx.x - record * (a.H_k * batches)), kh = part / batches, r0 = kHeadBatch * (part - kh * batches);
+    const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int i = 0;
+    for (int hi = a.num_seqs - 1; i < hi;) {      // the last sequence whose records start at this one or before
+        const int mid = (i + hi + 1) >> 1;
+        int lo, len;
+        dev::seq_range(a.cu_seqlens, mid, a.total_tokens, lo, len);
+        if (first_record(lo, mid) <= record) i = mid;
+        else hi = mid - 1;
+    }
+    i = __builtin_amdgcn_readfirstlane(i);
+    const Walk walk(a, i);
+    const int64_t c = record - first_record(walk.lo, i);
+    if (c < 0 || c >= walk.chunks) return;
+    int64_t row;
+    int n;
+    walk.span((int)c, row, n);
+    Staged<T, DK, 256> sb, sc;
+    const int krow = a.H_k * DK * (int)sizeof(T);
+    sb.load(head_rows<T>(a.b, row, n, a.H_k, kh, DK, 0, DK), krow, tid);
+    sc.load(head_rows<T>(a.c, row, n, a.H_k, kh, DK, 0, DK), krow, tid);
+    Weights<T>* out = static_cast<Weights<T>*>(a.workspace) + record * a.H_v + kh * R + r0;
+    if (r0 + wv < R) {
+        const int h = kh * R + r0 + wv;
+        const float dt = load_step(a, row, n, h, lane);
+        make_gates(gate[wv], dt, a.dt_bias ? a.dt_bias[h] : 0.f, a.A[h], a.dt_softplus, n, lane);
+        out[wv].d[lane] = gate[wv].w[lane];
+        out[wv].eg[lane] = gate[wv].eg[lane];
+    }
+    sb.store(smb, BP, tid);
+    sc.store_operands(smc, tid);
+    __syncthreads();
+    const int heads = R - r0 < kHeadBatch ? R - r0 : kHeadBatch;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        const int blk = wv + 4 * k;
+        if (blk >= 10) break;
+        const int it = blk >= 6 ? 3 : blk >= 3 ? 2 : blk >= 1 ? 1 : 0, jt = blk - it * (it + 1) / 2;
+        const T* cb = smc + it * 16 * DK;
+        const f32x4 s = score_tile<T, DK>(smb, BP, jt, lane, [&](int p, Half& h0, Half& h1) { pair_of<T>(cb, p, lane, h0, h1); });
+        for (int r = 0; r < heads; ++r) *reinterpret_cast<Half*>(out[r].w + blk * 256 + lane * 4) = decayed<T>(gate[r], s, it, jt, lane);
+    }
+}
+
 constexpr int kStrip = 16;
 constexpr int kStripThreads = 768;
 
@@ -638,12 +708,11 @@ struct StripSmem {
     static constexpr int BP = DK + Ops<T>::kPad, XP = kStrip + (sizeof(T) == 4 ? 4 : 0);
     // C comes from LDS (operand order) where it fits beside the rest, else each wave loads its own
     static constexpr bool kStageC = sizeof(T) == 2;
-    alignas(16) T b[2][kC * BP];                    // by chunk parity, as all but the gates
+    alignas(16) T b[2][kC * BP];                    // by chunk parity, as all of it
     T c[2][kStageC ? kC * DK : 8];
     T x[2][kC * XP];
     T v[2][Ops<T>::kTerms][kC * XP];      // e^(G_last - G) d x, in parts
     T s[2][DK * kStrip];                  // the state as operand, rounded to T
-    Gates gate[4];                        // by chunk modulo 4: made two chunks ahead
     int bad[2];
 };
 
@@ -665,25 +734,36 @@ __global__ __launch_bounds__(kStripThreads, 3) void ssm_strip_kernel(SsmArgs a) 
 
     // Three groups of four waves run loops of their own between the same barriers (so that the
     // waits of each count its own loads and stores alone): one forms Y of chunk c, one advances
-    // S over it and makes the gates of chunk c + 2, one stages chunk c + 1.  Loads run two
-    // chunks ahead of their use, in two register sets by chunk parity; an odd count of chunks
-    // is made even by one without tokens, which changes nothing.
+    // S over it, one stages chunk c + 1.  Loads run two chunks ahead of their use, in two
+    // register sets by chunk parity; an odd count of chunks is made even by one without tokens,
+    // which changes nothing.
+    const Weights<T>* rec = static_cast<const Weights<T>*>(a.workspace) + first_record(walk.lo, i) * a.H_v + h;
+    // a record's buffer, empty past the last chunk
+    auto record = [&](int c) { return rows_rsrc(rec + (size_t)(c < walk.chunks ? c : 0) * a.H_v, c < walk.chunks ? (int)sizeof(Weights<T>) : 0); };
+    auto load_float = [](rsrc_t r, int off) { return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0)); };
+    constexpr int kDOff = offsetof(Weights<T>, d), kEgOff = offsetof(Weights<T>, eg), kHalf = 4 * (int)sizeof(T);
     if (tid < 2) sm.bad[tid] = 0;
     if (wave < 4) {
         const float D = a.D ? a.D[h] : 0.f;
-        Half cf[2][2 * PAIRS];
-        auto fetch_c = [&](int c, int p) {
+        Half cf[2][2 * PAIRS], w[2][TT];
+        float egs[2];
+        auto fetch = [&](int c, int p) {
             int64_t row;
             int n;
             walk.span(c, row, n);
-            const rsrc_t r = head_rows<T>(a.c, row, n, a.H_k, kh, DK, 0, DK);
-            if constexpr (!SM::kStageC)
+            const rsrc_t r = record(c);
 #pragma unroll
-                for (int t = 0; t < 2 * PAIRS; ++t) cf[p][t] = Ops<T>::load_half(r, (16 * wv + li) * krow + (16 * t + g4) * (int)sizeof(T));
+            for (int jt = 0; jt < TT; ++jt)      // tiles past the diagonal: past the buffer, zeros
+                w[p][jt] = Ops<T>::load_half(r, jt <= wv ? ((wv * (wv + 1) / 2 + jt) * 64 + lane) * kHalf : (int)sizeof(Weights<T>));
+            egs[p] = load_float(r, kEgOff + 4 * (16 * wv + li));
+            if constexpr (!SM::kStageC) {
+                const rsrc_t rc = head_rows<T>(a.c, row, n, a.H_k, kh, DK, 0, DK);
+#pragma unroll
+                for (int t = 0; t < 2 * PAIRS; ++t) cf[p][t] = Ops<T>::load_half(rc, (16 * wv + li) * krow + (16 * t + g4) * (int)sizeof(T));
+            }
         };
         auto body = [&](int c, int p) {
-            const Gates& g = sm.gate[c & 3];
-            Half x[TT], w[TT];
+            Half x[TT];
             if constexpr (SM::kStageC)
 #pragma unroll
                 for (int s = 0; s < PAIRS; ++s) pair_of<T>(sm.c[p] + wv * 16 * DK, s, lane, cf[p][2 * s], cf[p][2 * s + 1]);
@@ -696,25 +776,14 @@ __global__ __launch_bounds__(kStripThreads, 3) void ssm_strip_kernel(SsmArgs a) 
                 pair_of<T>(sm.s[p], s, lane, s0, s1);
                 y = Ops<T>::mma(s0, s1, cf[p][2 * s], cf[p][2 * s + 1], y);
             }
-            // every wave forms four tiles, those past its diagonal as zeros: without branches
-            // their chains of products overlap
 #pragma unroll
-            for (int jt = 0; jt < TT; ++jt) {
-                const f32x4 s = score_tile<T, DK>(sm.b[p], SM::BP, jt, lane, [&](int q, Half& h0, Half& h1) {
-                    h0 = cf[p][2 * q];
-                    h1 = cf[p][2 * q + 1];
-                });
-                w[jt] = decayed<T>(g, s, wv, jt, lane);
-            }
-            fetch_c(c + 2, p);
-            const float eg = g.eg[16 * wv + li];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] *= eg;
+            for (int e = 0; e < 4; ++e) y[e] *= egs[p];
             const bool poisoned = sm.bad[p] == c + 1;
             const int bad = poisoned ? take_out<T>(x, lane) : kC;
 #pragma unroll
             for (int s = 0; s < TT / 2; ++s)
-                if (2 * s <= wv) y = Ops<T>::mma(x[2 * s], x[2 * s + 1], w[2 * s], w[2 * s + 1], y);
+                if (2 * s <= wv) y = Ops<T>::mma(x[2 * s], x[2 * s + 1], w[p][2 * s], w[p][2 * s + 1], y);
+            fetch(c + 2, p);
             int64_t row;
             int n;
             walk.span(c, row, n);
@@ -731,8 +800,8 @@ __global__ __launch_bounds__(kStripThreads, 3) void ssm_strip_kernel(SsmArgs a) 
             Ops<T>::store_half(Ops<T>::round(o), ry, t * vrow + g4 * (int)sizeof(T));
             dev::lds_barrier();
         };
-        fetch_c(0, 0);
-        fetch_c(1, 1);
+        fetch(0, 0);
+        fetch(1, 1);
         __syncthreads();
         dev::lds_barrier();
         for (int c = 0; c < walk.chunks; c += 2) {
@@ -761,24 +830,11 @@ __global__ __launch_bounds__(kStripThreads, 3) void ssm_strip_kernel(SsmArgs a) 
                 *reinterpret_cast<Half*>(p) = Ops<T>::round(S[nt]);
             }
         };
-        // its first wave makes the gates
-        const float A = a.A[h], bias = a.dt_bias ? a.dt_bias[h] : 0.f;
-        float dts[2];
-        auto fetch_dt = [&](int c, int p) {
-            int64_t row;
-            int n;
-            walk.span(c, row, n);
-            dts[p] = load_step(a, row, wv == 0 ? n : 0, h, lane);
-        };
-        auto gates = [&](int c, int p) {
-            int64_t row;
-            int n;
-            walk.span(c, row, n);
-            if (wv == 0) make_gates(sm.gate[c & 3], dts[p], bias, A, a.dt_softplus, n, lane);
-        };
+        float decays[2];
+        auto fetch = [&](int c, int p) { decays[p] = load_float(record(c), kEgOff + 4 * (kC - 1)); };
         Exports exports(a, walk, i);
         auto body = [&](int c, int p) {
-            const float decay = sm.gate[c & 3].eg[kC - 1];
+            const float decay = c < walk.chunks ? decays[p] : 1.f;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -800,8 +856,7 @@ __global__ __launch_bounds__(kStripThreads, 3) void ssm_strip_kernel(SsmArgs a) 
                 }
             }
             share(p ^ 1);
-            gates(c + 2, p);
-            fetch_dt(c + 4, p);
+            fetch(c + 2, p);
             float* dst = exports.take(a, walk.end_of(c), state);
             if (dst) put(dst);
             dev::lds_barrier();
@@ -814,13 +869,9 @@ __global__ __launch_bounds__(kStripThreads, 3) void ssm_strip_kernel(SsmArgs a) 
 #pragma unroll
             for (int e = 0; e < 4; ++e) S[nt][e] = have ? (src + at(nt, e))[mine] : 0.f;
         share(0);
-        fetch_dt(0, 0);
-        fetch_dt(1, 1);
-        gates(0, 0);
-        fetch_dt(2, 0);
+        fetch(0, 0);
+        fetch(1, 1);
         __syncthreads();
-        gates(1, 1);
-        fetch_dt(3, 1);
         dev::lds_barrier();
         for (int c = 0; c < walk.chunks; c += 2) {
             body(c, 0);
@@ -834,6 +885,7 @@ __global__ __launch_bounds__(kStripThreads, 3) void ssm_strip_kernel(SsmArgs a) 
     const int ltid = tid - 512, xr = ltid >> 2, xc = 4 * (ltid & 3);      // staging: a row and four columns of x
     Staged<T, DK, 256> sb[2], sc[2];
     Half sx[2];
+    float ds[2];
     auto fetch = [&](int c, int p) {
         int64_t row;
         int n;
@@ -841,9 +893,9 @@ __global__ __launch_bounds__(kStripThreads, 3) void ssm_strip_kernel(SsmArgs a) 
         sb[p].load(head_rows<T>(a.b, row, n, a.H_k, kh, DK, 0, DK), krow, ltid);
         if constexpr (SM::kStageC) sc[p].load(head_rows<T>(a.c, row, n, a.H_k, kh, DK, 0, DK), krow, ltid);
         sx[p] = Ops<T>::load_half(head_rows<T>(a.x, row, n, a.H_v, h, DV, col0, kStrip), xr * vrow + xc * (int)sizeof(T));
+        ds[p] = load_float(record(c), kDOff + 4 * xr);
     };
     auto stage = [&](int c, int p) {
-        const float w = sm.gate[c & 3].w[xr];
         const int at = xr * SM::XP + Ops<T>::column(xr, xc);
         sb[p].store(sm.b[p], SM::BP, ltid);
         if constexpr (SM::kStageC) sc[p].store_operands(sm.c[p], ltid);
@@ -852,7 +904,7 @@ __global__ __launch_bounds__(kStripThreads, 3) void ssm_strip_kernel(SsmArgs a) 
         if (!(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))) < __builtin_inff()) ||
             !(v[0] == v[0] && v[1] == v[1] && v[2] == v[2] && v[3] == v[3])) sm.bad[p] = c + 1;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] *= w;
+        for (int e = 0; e < 4; ++e) v[e] *= ds[p];
         Half part[TERMS];
         Ops<T>::split(v, part);
 #pragma unroll
@@ -949,15 +1001,24 @@ hipError_t decode_typed(const SsmArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
+// Strips while they, at one workgroup each, do not outnumber the compute units by far.
+bool in_strips(int64_t chains, int d_v) { return chains * (d_v / kStrip) <= 4 * (int64_t)device_cus(); }
+
 template <typename T, int DK, int DV>
 hipError_t prefill_typed(const SsmArgs& a, hipStream_t stream) {
     constexpr int CT = DV / 64;
     const int64_t chains = (int64_t)a.num_seqs * a.H_v;
-    // Strips while they, at one workgroup each, do not outnumber the compute units by far.
-    if (chains * (DV / kStrip) <= 4 * (int64_t)device_cus())
-        hipLaunchKernelGGL((ssm_strip_kernel<T, DK, DV>), dim3((unsigned)(chains * (DV / kStrip))), dim3(kStripThreads), 0, stream, a);
-    else
+    if (!in_strips(chains, DV)) {
         hipLaunchKernelGGL((ssm_head_kernel<T, DK, DV, CT>), dim3((unsigned)chains), dim3(4 * DV / CT), 0, stream, a);
+        return hipGetLastError();
+    }
+    const int R = a.H_v / a.H_k;
+    const int64_t blocks = record_count(a.num_seqs, a.total_tokens) * a.H_k * ((R + kHeadBatch - 1) / kHeadBatch);
+    if (blocks > 0x7fffffffLL) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL((ssm_weights_kernel<T, DK>), dim3((unsigned)blocks), dim3(256), 0, stream, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((ssm_strip_kernel<T, DK, DV>), dim3((unsigned)(chains * (DV / kStrip))), dim3(kStripThreads), 0, stream, a);
     return hipGetLastError();
 }
 
@@ -979,7 +1040,10 @@ hipError_t decode_dims(const SsmArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-size_t ssm_workspace_bytes(int, int, int, int, int, int64_t) { return 0; }
+size_t ssm_workspace_bytes(int H_v, int, int d_v, int dtype, int num_seqs, int64_t total_tokens) {
+    if (!in_strips((int64_t)num_seqs * H_v, d_v)) return 0;
+    return (size_t)record_count(num_seqs, total_tokens) * (size_t)H_v * (dtype == 1 ? sizeof(Weights<__bf16>) : sizeof(Weights<float>));
+}
 
 hipError_t launch_ssm_decode(const SsmArgs& a, hipStream_t stream) {
     return a.dtype == 1 ? decode_dims<__bf16>(a, stream) : decode_dims<float>(a, stream);
