@@ -327,6 +327,15 @@ __device__ __forceinline__ float load_step(const SsmArgs& a, int64_t row, int n,
     return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, lane * a.H_v * 4, 0, 0));
 }
 
+// Where lane l's part of block s lies in operand order (a block: 32 columns of bf16, 16 of fp32).
+// A wave stages a few rows of every block at once, and the blocks are a multiple of the LDS's
+// width apart: moving each block's rows along spreads them over the banks.
+template <typename T, int N>
+__device__ __forceinline__ int swizzled(int s, int l) {
+    constexpr int BLOCKS = N * (int)sizeof(T) / 64;
+    return l ^ (16 / BLOCKS * s);
+}
+
 // A 64 x N block on its way from memory to LDS through the registers of TH threads.
 template <typename T, int N, int TH>
 struct Staged {
@@ -349,18 +358,19 @@ struct Staged {
             if (VECS % TH == 0 || u < VECS) *reinterpret_cast<u32x4*>(m + row * pitch + Ops<T>::column(row, (u % PER_ROW) * V)) = v[k];
         }
     }
-    // as operands of rows: the two (bf16) or one (fp32) halves of a lane side by side
+    // as operands of rows: the two (bf16) or one (fp32) halves of a lane side by side, the lanes
+    // of block s where swizzled() says
     __device__ __forceinline__ void store_operands(T* m, int tid) const {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int u = tid + k * TH, row = u / PER_ROW, c = (u % PER_ROW) * V;
             if constexpr (sizeof(T) == 2) {
                 // pair block (row tile, c / 32), lane (row % 16, group), half (c / 16) % 2
-                T* p = m + ((row >> 4) * (N / 32) + (c >> 5)) * 512 + ((row & 15) + 16 * ((c & 15) >> 2)) * 8 + ((c >> 4) & 1) * 4;
+                T* p = m + ((row >> 4) * (N / 32) + (c >> 5)) * 512 + swizzled<T, N>(c >> 5, (row & 15) + 16 * ((c & 15) >> 2)) * 8 + ((c >> 4) & 1) * 4;
                 *reinterpret_cast<u32x2*>(p) = u32x2{v[k][0], v[k][1]};
                 *reinterpret_cast<u32x2*>(p + 128) = u32x2{v[k][2], v[k][3]};
             } else {
-                T* p = m + ((row >> 4) * (N / 16) + (c >> 4)) * 256 + ((row & 15) + 16 * ((c & 15) >> 2)) * 4;
+                T* p = m + ((row >> 4) * (N / 16) + (c >> 4)) * 256 + swizzled<T, N>(c >> 4, (row & 15) + 16 * ((c & 15) >> 2)) * 4;
                 *reinterpret_cast<u32x4*>(p) = v[k];
             }
         }
@@ -375,16 +385,16 @@ struct Staged {
 };
 
 // A lane's two halves of pair s of an operand block stored by Staged::store_operands.
-template <typename T>
+template <typename T, int N>
 __device__ __forceinline__ void pair_of(const T* block, int s, int lane, typename Ops<T>::Half& h0, typename Ops<T>::Half& h1) {
     typedef typename Ops<T>::Half Half;
     if constexpr (sizeof(T) == 2) {
-        const bf16x8 v = *reinterpret_cast<const bf16x8*>(block + s * 512 + lane * 8);
+        const bf16x8 v = *reinterpret_cast<const bf16x8*>(block + s * 512 + swizzled<T, N>(s, lane) * 8);
         h0 = __builtin_shufflevector(v, v, 0, 1, 2, 3);
         h1 = __builtin_shufflevector(v, v, 4, 5, 6, 7);
     } else {
-        h0 = *reinterpret_cast<const Half*>(block + 2 * s * 256 + lane * 4);
-        h1 = *reinterpret_cast<const Half*>(block + (2 * s + 1) * 256 + lane * 4);
+        h0 = *reinterpret_cast<const Half*>(block + 2 * s * 256 + swizzled<T, N>(2 * s, lane) * 4);
+        h1 = *reinterpret_cast<const Half*>(block + (2 * s + 1) * 256 + swizzled<T, N>(2 * s + 1, lane) * 4);
     }
 }
 
@@ -508,7 +518,7 @@ __global__ __launch_bounds__(4 * DV / CT, sizeof(T) == 2 ? DV / CT / 32 : 1) voi
             if (blk < 10) {
                 const int it = blk >= 6 ? 3 : blk >= 3 ? 2 : blk >= 1 ? 1 : 0, jt = blk - it * (it + 1) / 2;
                 const T* cb = sm.c + it * 16 * DK;
-                const f32x4 s = score_tile<T, DK>(sm.b, SM::BP, jt, lane, [&](int p, Half& h0, Half& h1) { pair_of<T>(cb, p, lane, h0, h1); });
+                const f32x4 s = score_tile<T, DK>(sm.b, SM::BP, jt, lane, [&](int p, Half& h0, Half& h1) { pair_of<T, DK>(cb, p, lane, h0, h1); });
                 *reinterpret_cast<Half*>(sm.w + blk * 256 + lane * 4) = decayed<T>(g, s, it, jt, lane);
             }
             __builtin_amdgcn_sched_barrier(0);
@@ -530,7 +540,7 @@ __global__ __launch_bounds__(4 * DV / CT, sizeof(T) == 2 ? DV / CT / 32 : 1) voi
 #pragma unroll
             for (int it = 0; it < TT; ++it) {
                 Half c0, c1;
-                pair_of<T>(sm.c + it * 16 * DK, s, lane, c0, c1);
+                pair_of<T, DK>(sm.c + it * 16 * DK, s, lane, c0, c1);
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) y[it][ct] = Ops<T>::mma(s0[ct], s1[ct], c0, c1, y[it][ct]);
             }
@@ -695,7 +705,7 @@ __global__ __launch_bounds__(256) void ssm_weights_kernel(SsmArgs a) {
         if (blk >= 10) break;
         const int it = blk >= 6 ? 3 : blk >= 3 ? 2 : blk >= 1 ? 1 : 0, jt = blk - it * (it + 1) / 2;
         const T* cb = smc + it * 16 * DK;
-        const f32x4 s = score_tile<T, DK>(smb, BP, jt, lane, [&](int p, Half& h0, Half& h1) { pair_of<T>(cb, p, lane, h0, h1); });
+        const f32x4 s = score_tile<T, DK>(smb, BP, jt, lane, [&](int p, Half& h0, Half& h1) { pair_of<T, DK>(cb, p, lane, h0, h1); });
         for (int r = 0; r < heads; ++r) *reinterpret_cast<Half*>(out[r].w + blk * 256 + lane * 4) = decayed<T>(gate[r], s, it, jt, lane);
     }
 }
@@ -766,14 +776,14 @@ __global__ __launch_bounds__(kStripThreads, 3) void ssm_strip_kernel(SsmArgs a) 
             Half x[TT];
             if constexpr (SM::kStageC)
 #pragma unroll
-                for (int s = 0; s < PAIRS; ++s) pair_of<T>(sm.c[p] + wv * 16 * DK, s, lane, cf[p][2 * s], cf[p][2 * s + 1]);
+                for (int s = 0; s < PAIRS; ++s) pair_of<T, DK>(sm.c[p] + wv * 16 * DK, s, lane, cf[p][2 * s], cf[p][2 * s + 1]);
 #pragma unroll
             for (int t = 0; t < TT; ++t) x[t] = Ops<T>::col_half(sm.x[p], SM::XP, 16 * t, 0, lane);
             f32x4 y = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int s = 0; s < PAIRS; ++s) {
                 Half s0, s1;
-                pair_of<T>(sm.s[p], s, lane, s0, s1);
+                pair_of<T, DK>(sm.s[p], s, lane, s0, s1);
                 y = Ops<T>::mma(s0, s1, cf[p][2 * s], cf[p][2 * s + 1], y);
             }
 #pragma unroll
@@ -826,7 +836,8 @@ __global__ __launch_bounds__(kStripThreads, 3) void ssm_strip_kernel(SsmArgs a) 
     #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const int t = NT * wv + nt;
-                T* p = sizeof(T) == 2 ? sm.s[parity] + (t >> 1) * 512 + lane * 8 + (t & 1) * 4 : sm.s[parity] + t * 256 + lane * 4;
+                T* p = sizeof(T) == 2 ? sm.s[parity] + (t >> 1) * 512 + swizzled<T, DK>(t >> 1, lane) * 8 + (t & 1) * 4
+                                   : sm.s[parity] + t * 256 + swizzled<T, DK>(t, lane) * 4;
                 *reinterpret_cast<Half*>(p) = Ops<T>::round(S[nt]);
             }
         };
