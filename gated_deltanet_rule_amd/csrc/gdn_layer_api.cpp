@@ -297,7 +297,7 @@ gdn_status gdn_causal_conv_decode(const gdn_conv_shape* shape, int32_t num_rows,
 
 size_t gdn_ssm_chunk_prefill_workspace_size(const gdn_shape* shape, int32_t num_seqs, int64_t total_tokens) {
     if (gdn::check_shape(shape) != GDN_OK || num_seqs < 0 || total_tokens < 0) return 0;
-    return gdn::ssm_workspace_bytes(shape->num_k_heads, shape->num_v_heads, shape->d_k, shape->d_v, shape->dtype, num_seqs, total_tokens);
+    return gdn::ssm_workspace_bytes(shape->num_v_heads, shape->d_k, shape->d_v, shape->dtype, num_seqs, total_tokens);
 }
 
 gdn_status gdn_ssm_chunk_prefill(const gdn_shape* shape, const gdn_ssm_params* params, int32_t num_seqs,
@@ -322,7 +322,7 @@ gdn_status gdn_ssm_chunk_prefill(const gdn_shape* shape, const gdn_ssm_params* p
         st = check_ptrs({{"c", c, 16}, {"b", b, 16}, {"x", x, 16}, {"dt", dt, 4}, {"y", y, 16}});
         if (st != GDN_OK) return st;
     }
-    const size_t need = gdn::ssm_workspace_bytes(shape->num_k_heads, shape->num_v_heads, shape->d_k, shape->d_v, shape->dtype, num_seqs, total_tokens);
+    const size_t need = gdn::ssm_workspace_bytes(shape->num_v_heads, shape->d_k, shape->d_v, shape->dtype, num_seqs, total_tokens);
     if (workspace_bytes < need)
         return fail(GDN_ERR_INVALID_ARGUMENT, "workspace_bytes %zu is smaller than the %zu bytes required", workspace_bytes, need);
     if (need > 0) {

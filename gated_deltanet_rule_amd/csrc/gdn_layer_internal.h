@@ -80,7 +80,7 @@ struct SsmArgs {
     int64_t export_capacity;
     void* workspace;
 };
-size_t ssm_workspace_bytes(int H_k, int H_v, int d_k, int d_v, int dtype, int num_seqs, int64_t total_tokens);
+size_t ssm_workspace_bytes(int H_v, int d_k, int d_v, int dtype, int num_seqs, int64_t total_tokens);
 hipError_t launch_ssm_prefill(const SsmArgs& a, hipStream_t stream);
 hipError_t launch_ssm_decode(const SsmArgs& a, hipStream_t stream);
 

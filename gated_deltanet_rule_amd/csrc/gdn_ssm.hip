@@ -55,7 +55,6 @@ typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
 typedef __attribute__((address_space(3))) volatile u32x2 lds_vu32x2;
-typedef __attribute__((address_space(3))) void lds_void;
 typedef __amdgpu_buffer_rsrc_t rsrc_t;
 
 // ---------------------------------------------------------------- operands
@@ -67,11 +66,6 @@ __device__ __forceinline__ rsrc_t rows_rsrc(const void* base, int bytes) {
 }
 __device__ __forceinline__ u32x4 load16(rsrc_t r, int off) {
     return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
-}
-// The same into LDS: lane l's 16 bytes to dst + 16 l, past the buffer's end zeros too.  The loads
-// count as vector memory; nothing but an explicit wait orders them before other waves' reads.
-__device__ __forceinline__ void load_lds16(rsrc_t r, char* dst, int off) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)dst, 16, off, 0, 0, 0);
 }
 
 // What a lane holds of one 16-wide k tile (Half: four elements), and products over a pair
@@ -104,6 +98,7 @@ struct Ops<__bf16> {
     }
     // v = t[2] + t[1] + t[0] exactly: the leading 8 bits of what is left, three times
     static __device__ __forceinline__ void split(f32x4 v, Half (&t)[kTerms]) {
+#pragma clang fp contract(off)
 #pragma unroll
         for (int k = kTerms - 1; k >= 0; --k) {
             u32x4 w = __builtin_bit_cast(u32x4, v);
@@ -237,13 +232,14 @@ __device__ __forceinline__ typename Ops<T>::Half decayed(const Gates& g, f32x4 s
     return Ops<T>::round(w);
 }
 
-// The decayed steps times x of one tile half, in parts.
+// The decayed steps times x of one tile half, in parts.  (Without contraction: it would split
+// the unrounded product instead, where the compiler finds it.)
 template <typename T>
-__device__ __forceinline__ void weighted(const Gates& g, typename Ops<T>::Half x, int t, int lane, typename Ops<T>::Half (&out)[Ops<T>::kTerms]) {
-    const f32x4 w = *reinterpret_cast<const f32x4*>(g.w + 16 * t + 4 * (lane >> 4));
-    f32x4 v = Ops<T>::widen(x);
+__device__ __forceinline__ void weighted(f32x4 x, f32x4 w, typename Ops<T>::Half (&out)[Ops<T>::kTerms]) {
+#pragma clang fp contract(off)
+    f32x4 v;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] *= w[e];
+    for (int e = 0; e < 4; ++e) v[e] = x[e] * w[e];
     Ops<T>::split(v, out);
 }
 
@@ -625,8 +621,9 @@ __global__ __launch_bounds__(4 * DV / CT, sizeof(T) == 2 ? DV / CT / 32 : 1) voi
             Half v0[CT][TERMS], v1[CT][TERMS];
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
-                weighted<T>(g, x[ct][2 * s], 2 * s, lane, v0[ct]);
-                weighted<T>(g, x[ct][2 * s + 1], 2 * s + 1, lane, v1[ct]);
+                const float* w = g.w + 32 * s + g4;
+                weighted<T>(Ops<T>::widen(x[ct][2 * s]), *reinterpret_cast<const f32x4*>(w), v0[ct]);
+                weighted<T>(Ops<T>::widen(x[ct][2 * s + 1]), *reinterpret_cast<const f32x4*>(w + 16), v1[ct]);
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -658,17 +655,9 @@ struct Weights {
     float eg[kC];            // e^G
 };
 
-// Beside the records, per chunk and key head, C as operands of rows: [row tile][pair][lane][half].
-
 // Records of a sequence start here: far enough from those of the one before, whatever its skew.
 __device__ __forceinline__ int64_t first_record(int lo, int i) { return (lo >> 6) + 2 * (int64_t)i; }
-__host__ __device__ inline int64_t record_count(int num_seqs, int64_t total_tokens) { return (total_tokens >> 6) + 2 * (int64_t)num_seqs; }
-
-template <typename T>
-__device__ __forceinline__ T* c_operands(const SsmArgs& a, int64_t record, int kh, int d_k) {
-    T* base = reinterpret_cast<T*>(static_cast<Weights<T>*>(a.workspace) + record_count(a.num_seqs, a.total_tokens) * a.H_v);
-    return base + (record * a.H_k + kh) * (int64_t)(kC * d_k);
-}
+int64_t record_count(int num_seqs, int64_t total_tokens) { return (total_tokens >> 6) + 2 * (int64_t)num_seqs; }
 
 constexpr int kHeadBatch = 4;     // heads of one workgroup
 
@@ -679,8 +668,9 @@ __global__ __launch_bounds__(256) void ssm_weights_kernel(SsmArgs a) {
     __shared__ __attribute__((aligned(16))) T smb[kC * BP], smc[kC * DK];
     __shared__ Gates gate[kHeadBatch];
     const int R = a.H_v / a.H_k, batches = (R + kHeadBatch - 1) / kHeadBatch;
-    const int64_t record = blockIdx.x / (unsigned)(a.H_k * batches);
-    const int part = (int)(blockIdx.x - record * (a.H_k * batches)), kh = part / batches, r0 = kHeadBatch * (part - kh * batches);
+    const unsigned unit = xcd_run(blockIdx.x);      // a row's heads on one XCD: they lie on different L2 channels
+    const int64_t record = unit / (unsigned)(a.H_k * batches);
+    const int part = (int)(unit - record * (a.H_k * batches)), kh = part / batches, r0 = kHeadBatch * (part - kh * batches);
     const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
     int i = 0;
     for (int hi = a.num_seqs - 1; i < hi;) {      // the last sequence whose records start at this one or before
@@ -712,17 +702,6 @@ __global__ __launch_bounds__(256) void ssm_weights_kernel(SsmArgs a) {
     sb.store(smb, BP, tid);
     sc.store_operands(smc, tid);
     __syncthreads();
-    if (r0 == 0) {
-        T* co = c_operands<T>(a, record, kh, DK) + wv * 16 * DK;
-#pragma unroll
-        for (int s = 0; s < DK / 32; ++s) {
-            Half h0, h1;
-            pair_of<T, DK>(smc + wv * 16 * DK, s, lane, h0, h1);
-            Half* p = reinterpret_cast<Half*>(co) + (s * 64 + lane) * 2;
-            p[0] = h0;
-            p[1] = h1;
-        }
-    }
     const int heads = R - r0 < kHeadBatch ? R - r0 : kHeadBatch;
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
@@ -738,32 +717,14 @@ __global__ __launch_bounds__(256) void ssm_weights_kernel(SsmArgs a) {
 constexpr int kStrip = 16;
 constexpr int kStripThreads = 768;
 
-// B goes from memory to LDS directly, in dense rows whose 16-column blocks are moved about by
-// row, so that the transposing reads of 16 rows spread over the banks.
-template <typename T, int DK>
-__device__ __forceinline__ int block_key(int row) {
-    return sizeof(T) == 4 ? (row >> 2) & 3 : DK == 128 ? row & 7 : (row >> 1) & 3;
-}
-
-// Ops<T>::col_half of such rows.
-template <typename T, int DK>
-__device__ __forceinline__ typename Ops<T>::Half moved_half(const T* m, int r0, int c0, int lane) {
-    if constexpr (sizeof(T) == 2) {
-        const int row = lane >> 2, at = row * DK + (c0 ^ (16 * block_key<T, DK>(row))) + 4 * (lane & 3);
-        return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(m + at + r0 * DK)));
-    } else {
-        const int row = 4 * (lane >> 4);
-        const T* p = m + (row * DK + (c0 ^ (16 * block_key<T, DK>(row))) + (lane & 15)) + r0 * DK;
-        return f32x4{p[0], p[DK], p[2 * DK], p[3 * DK]};
-    }
-}
-
 template <typename T, int DK>
 struct StripSmem {
-    static constexpr int XP = kStrip + (sizeof(T) == 4 ? 4 : 0);
-    static constexpr int kRing = sizeof(T) == 2 ? 4 : 3;      // as many chunks of B as fit
-    alignas(16) T b[kRing][kC * DK];
-    T x[2][kC * XP];                      // by chunk parity, as all below
+    static constexpr int BP = DK + Ops<T>::kPad, XP = kStrip + (sizeof(T) == 4 ? 4 : 0);
+    // C comes from LDS (operand order) where it fits beside the rest, else each wave loads its own
+    static constexpr bool kStageC = sizeof(T) == 2;
+    alignas(16) T b[2][kC * BP];                    // by chunk parity, as all of it
+    T c[2][kStageC ? kC * DK : 8];
+    T x[2][kC * XP];
     T v[2][Ops<T>::kTerms][kC * XP];      // e^(G_last - G) d x, in parts
     T s[2][DK * kStrip];                  // the state as operand, rounded to T
     int bad[2];
@@ -798,30 +759,28 @@ __global__ __launch_bounds__(kStripThreads, 3) void ssm_strip_kernel(SsmArgs a) 
     if (tid < 2) sm.bad[tid] = 0;
     if (wave < 4) {
         const float D = a.D ? a.D[h] : 0.f;
-        const T* co = c_operands<T>(a, first_record(walk.lo, i), kh, DK) + wv * 16 * DK;
         Half cf[2][2 * PAIRS], w[2][TT];
         float egs[2];
         auto fetch = [&](int c, int p) {
+            int64_t row;
+            int n;
+            walk.span(c, row, n);
             const rsrc_t r = record(c);
 #pragma unroll
             for (int jt = 0; jt < TT; ++jt)      // tiles past the diagonal: past the buffer, zeros
                 w[p][jt] = Ops<T>::load_half(r, jt <= wv ? ((wv * (wv + 1) / 2 + jt) * 64 + lane) * kHalf : (int)sizeof(Weights<T>));
             egs[p] = load_float(r, kEgOff + 4 * (16 * wv + li));
-            const rsrc_t rc = rows_rsrc(co + (size_t)(c < walk.chunks ? c : 0) * a.H_k * kC * DK, c < walk.chunks ? 16 * DK * (int)sizeof(T) : 0);
+            if constexpr (!SM::kStageC) {
+                const rsrc_t rc = head_rows<T>(a.c, row, n, a.H_k, kh, DK, 0, DK);
 #pragma unroll
-            for (int s = 0; s < PAIRS; ++s) {
-                if constexpr (sizeof(T) == 2) {
-                    const u32x4 v = load16(rc, (s * 64 + lane) * 16);
-                    cf[p][2 * s] = __builtin_bit_cast(Half, u32x2{v[0], v[1]});
-                    cf[p][2 * s + 1] = __builtin_bit_cast(Half, u32x2{v[2], v[3]});
-                } else {
-                    cf[p][2 * s] = Ops<T>::load_half(rc, (s * 64 + lane) * 32);
-                    cf[p][2 * s + 1] = Ops<T>::load_half(rc, (s * 64 + lane) * 32 + 16);
-                }
+                for (int t = 0; t < 2 * PAIRS; ++t) cf[p][t] = Ops<T>::load_half(rc, (16 * wv + li) * krow + (16 * t + g4) * (int)sizeof(T));
             }
         };
         auto body = [&](int c, int p) {
             Half x[TT];
+            if constexpr (SM::kStageC)
+#pragma unroll
+                for (int s = 0; s < PAIRS; ++s) pair_of<T, DK>(sm.c[p] + wv * 16 * DK, s, lane, cf[p][2 * s], cf[p][2 * s + 1]);
 #pragma unroll
             for (int t = 0; t < TT; ++t) x[t] = Ops<T>::col_half(sm.x[p], SM::XP, 16 * t, 0, lane);
             f32x4 y = {0.f, 0.f, 0.f, 0.f};
@@ -886,7 +845,6 @@ __global__ __launch_bounds__(kStripThreads, 3) void ssm_strip_kernel(SsmArgs a) 
                 *reinterpret_cast<Half*>(p) = Ops<T>::round(S[nt]);
             }
         };
-        int ring = 0;
         float decays[2];
         auto fetch = [&](int c, int p) { decays[p] = load_float(record(c), kEgOff + 4 * (kC - 1)); };
         Exports exports(a, walk, i);
@@ -907,12 +865,11 @@ __global__ __launch_bounds__(kStripThreads, 3) void ssm_strip_kernel(SsmArgs a) 
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     const int n0 = 16 * (NT * wv + nt);
-                    const Half b0 = moved_half<T, DK>(sm.b[ring], 32 * s, n0, lane), b1 = moved_half<T, DK>(sm.b[ring], 32 * s + 16, n0, lane);
+                    const Half b0 = Ops<T>::col_half(sm.b[p], SM::BP, 32 * s, n0, lane), b1 = Ops<T>::col_half(sm.b[p], SM::BP, 32 * s + 16, n0, lane);
 #pragma unroll
                     for (int k = 0; k < TERMS; ++k) S[nt] = Ops<T>::mma(b0, b1, v0[k], v1[k], S[nt]);
                 }
             }
-            ring = ring + 1 == SM::kRing ? 0 : ring + 1;
             share(p ^ 1);
             fetch(c + 2, p);
             float* dst = exports.take(a, walk.end_of(c), state);
@@ -941,71 +898,46 @@ __global__ __launch_bounds__(kStripThreads, 3) void ssm_strip_kernel(SsmArgs a) 
     }
 
     const int ltid = tid - 512, xr = ltid >> 2, xc = 4 * (ltid & 3);      // staging: a row and four columns of x
-    // B's chunks go kRing - 1 ahead; a wave's loads into LDS cover 1 KiB each, lanes in order
-    constexpr int kLoads = kC * DK * (int)sizeof(T) / 4096;
-    int src[kLoads];
-#pragma unroll
-    for (int k = 0; k < kLoads; ++k) {
-        const int at = ((kLoads * wv + k) * 1024 + lane * 16) / (int)sizeof(T), row = at / DK;
-        src[k] = row * krow + ((at % DK) ^ (16 * block_key<T, DK>(row))) * (int)sizeof(T);
-    }
-    int ring = 0;
-    auto fetch_b = [&](int c) {
-        int64_t row;
-        int n;
-        walk.span(c, row, n);
-        const rsrc_t r = head_rows<T>(a.b, row, n, a.H_k, kh, DK, 0, DK);
-        char* dst = reinterpret_cast<char*>(sm.b[ring]) + kLoads * wv * 1024;
-#pragma unroll
-        for (int k = 0; k < kLoads; ++k) load_lds16(r, dst + k * 1024, src[k]);
-        ring = ring + 1 == SM::kRing ? 0 : ring + 1;
-    };
+    Staged<T, DK, 256> sb[2], sc[2];
     Half sx[2];
     float ds[2];
     auto fetch = [&](int c, int p) {
         int64_t row;
         int n;
         walk.span(c, row, n);
+        sb[p].load(head_rows<T>(a.b, row, n, a.H_k, kh, DK, 0, DK), krow, ltid);
+        if constexpr (SM::kStageC) sc[p].load(head_rows<T>(a.c, row, n, a.H_k, kh, DK, 0, DK), krow, ltid);
         sx[p] = Ops<T>::load_half(head_rows<T>(a.x, row, n, a.H_v, h, DV, col0, kStrip), xr * vrow + xc * (int)sizeof(T));
         ds[p] = load_float(record(c), kDOff + 4 * xr);
     };
     auto stage = [&](int c, int p) {
         const int at = xr * SM::XP + Ops<T>::column(xr, xc);
+        sb[p].store(sm.b[p], SM::BP, ltid);
+        if constexpr (SM::kStageC) sc[p].store_operands(sm.c[p], ltid);
         *reinterpret_cast<Half*>(sm.x[p] + at) = sx[p];
-        f32x4 v = Ops<T>::widen(sx[p]);
+        const f32x4 v = Ops<T>::widen(sx[p]);
         if (!(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))) < __builtin_inff()) ||
             !(v[0] == v[0] && v[1] == v[1] && v[2] == v[2] && v[3] == v[3])) sm.bad[p] = c + 1;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] *= ds[p];
         Half part[TERMS];
-        Ops<T>::split(v, part);
+        weighted<T>(v, f32x4{ds[p], ds[p], ds[p], ds[p]}, part);
 #pragma unroll
         for (int k = 0; k < TERMS; ++k) *reinterpret_cast<Half*>(sm.v[p][k] + at) = part[k];
     };
-    // what may be in flight when a chunk's B has to be there: the loads of the chunks after it,
-    // and the two register loads behind its own
-    constexpr int kInFlight = 2 + (SM::kRing - 2) * (kLoads + 2);
     auto body = [&](int c, int p) {
-        fetch_b(c + SM::kRing - 1);
-        __builtin_amdgcn_sched_barrier(0);
         stage(c + 1, p ^ 1);
         fetch(c + 3, p ^ 1);
-        __builtin_amdgcn_s_waitcnt((kInFlight & 15) | 0x0F70 | ((kInFlight >> 4) << 14));
         dev::lds_barrier();
     };
-    for (int c = 0; c < SM::kRing - 1; ++c) fetch_b(c);
     fetch(0, 0);
     fetch(1, 1);
     __syncthreads();
     stage(0, 0);
     fetch(2, 0);
-    __builtin_amdgcn_s_waitcnt(0x0F70);
     dev::lds_barrier();
     for (int c = 0; c < walk.chunks; c += 2) {
         body(c, 0);
         body(c + 1, 1);
     }
-    __builtin_amdgcn_s_waitcnt(0x0F70);      // nothing may be on its way into LDS when the workgroup ends
 }
 
 // ---------------------------------------------------------------- decode
@@ -1082,14 +1014,22 @@ hipError_t decode_typed(const SsmArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// Strips while they, at one workgroup each, do not outnumber the compute units by far.
-bool in_strips(int64_t chains, int d_v) { return chains * (d_v / kStrip) <= 4 * (int64_t)device_cus(); }
+// Strips for calls with few chains.  A compute unit takes one strip at a time, in about 1.1 us a
+// chunk and 10 us for the launches; a whole head takes 5.3 us a chunk (bf16, 128 x 128), however
+// many compute units have one.  So strips pay for up to four rounds of them, the more rounds the
+// longer the sequences have to be (us, heads / strips: one round of 64 tokens 15 / 17, of 256
+// 27 / 19, of 4096 342 / 76; two of 256 28 / 22, of 4096 347 / 145; four of 256 30 / 36, of 1024
+// 92 / 83; eight of 4096 357 / 615).
+bool in_strips(int H_v, int d_v, int num_seqs, int64_t total_tokens) {
+    const int64_t strips = (int64_t)num_seqs * H_v * (d_v / kStrip), cus = device_cus(), rounds = (strips + cus - 1) / cus;
+    return rounds <= 4 && total_tokens >= 64 * (rounds * rounds + 1) * num_seqs;
+}
 
 template <typename T, int DK, int DV>
 hipError_t prefill_typed(const SsmArgs& a, hipStream_t stream) {
     constexpr int CT = DV / 64;
     const int64_t chains = (int64_t)a.num_seqs * a.H_v;
-    if (!in_strips(chains, DV)) {
+    if (!in_strips(a.H_v, DV, a.num_seqs, a.total_tokens)) {
         hipLaunchKernelGGL((ssm_head_kernel<T, DK, DV, CT>), dim3((unsigned)chains), dim3(4 * DV / CT), 0, stream, a);
         return hipGetLastError();
     }
@@ -1121,10 +1061,9 @@ hipError_t decode_dims(const SsmArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-size_t ssm_workspace_bytes(int H_k, int H_v, int d_k, int d_v, int dtype, int num_seqs, int64_t total_tokens) {
-    if (!in_strips((int64_t)num_seqs * H_v, d_v)) return 0;
-    const size_t weights = (size_t)H_v * (dtype == 1 ? sizeof(Weights<__bf16>) : sizeof(Weights<float>)), c = (size_t)H_k * kC * d_k * (dtype == 1 ? 2 : 4);
-    return (size_t)record_count(num_seqs, total_tokens) * (weights + c);
+size_t ssm_workspace_bytes(int H_v, int, int d_v, int dtype, int num_seqs, int64_t total_tokens) {
+    if (!in_strips(H_v, d_v, num_seqs, total_tokens)) return 0;
+    return (size_t)record_count(num_seqs, total_tokens) * (size_t)H_v * (dtype == 1 ? sizeof(Weights<__bf16>) : sizeof(Weights<float>));
 }
 
 hipError_t launch_ssm_decode(const SsmArgs& a, hipStream_t stream) {
