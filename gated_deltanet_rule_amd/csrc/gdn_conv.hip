@@ -21,6 +21,8 @@
 namespace gdn {
 namespace {
 
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kGroup = 4;
@@ -78,24 +80,38 @@ struct Taps {
         }
     }
 
-    // The lanes of a head are consecutive and either all active or all not.
-    __device__ __forceinline__ void apply(const ConvArgs& a, int l2_dim, const float (*in)[V], float (&u)[V]) const {
+    // Outputs of N tokens from their W - 1 + N inputs.  The lanes of a head are consecutive and
+    // either all active or all not; the tokens' sums go over them side by side.
+    template <int N>
+    __device__ __forceinline__ void apply(const ConvArgs& a, int l2_dim, const float (*in)[V], float (&u)[N][V]) const {
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            u[e] = b[e];
+        for (int k = 0; k < N; ++k)
 #pragma unroll
-            for (int j = 0; j < W; ++j) u[e] = fmaf(w[e * W + j], in[j][e], u[e]);
-        }
+            for (int e = 0; e < V; ++e) {
+                u[k][e] = b[e];
+#pragma unroll
+                for (int j = 0; j < W; ++j) u[k][e] = fmaf(w[e * W + j], in[k + j][e], u[k][e]);
+            }
         if (a.silu)
 #pragma unroll
-            for (int e = 0; e < V; ++e) u[e] = dev::silu(u[e]);
+            for (int k = 0; k < N; ++k)
+#pragma unroll
+                for (int e = 0; e < V; ++e) u[k][e] = dev::silu(u[k][e]);
         if (l2_dim > 0) {
-            float s = 0.f;
+            float s[N];
 #pragma unroll
-            for (int e = 0; e < V; ++e) s = fmaf(u[e], u[e], s);
-            const float r = dev::inv_sqrt(dev::group_sum(s, l2_dim / V) + a.l2_eps);
+            for (int k = 0; k < N; ++k) {
+                s[k] = 0.f;
 #pragma unroll
-            for (int e = 0; e < V; ++e) u[e] *= r;
+                for (int e = 0; e < V; ++e) s[k] = fmaf(u[k][e], u[k][e], s[k]);
+            }
+            dev::group_sums(s, l2_dim / V);
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const float r = dev::inv_sqrt(s[k] + a.l2_eps);
+#pragma unroll
+                for (int e = 0; e < V; ++e) u[k][e] *= r;
+            }
         }
     }
 };
@@ -142,7 +158,7 @@ __global__ __launch_bounds__(kThreads) void conv_prefill_kernel(ConvArgs a, int 
     const bool last = blockIdx.x + 1 == gridDim.x;
     Taps<T, W> taps;
     if (a.total_tokens > 0) taps.load(a, w.c);
-    const int l2_dim = a.l2_dim[w.seg];
+    const int seg = __builtin_amdgcn_readfirstlane(w.seg), l2_dim = a.l2_dim[seg], width = a.channels[seg];
     // the first sequence that starts at t0 or later
     int i = 0;
     {
@@ -169,30 +185,33 @@ __global__ __launch_bounds__(kThreads) void conv_prefill_kernel(ConvArgs a, int 
         if (owned && to < W - 1) to = len < W - 1 ? len : W - 1;
         const int slot = owned ? slot_or_none(a.init_slot, i, a.num_slots) : -1;
         if (from < to) {
-            float in[W - 1 + kGroup][V], next[kGroup][V];
+            // Rows as buffers of their own, empty past the tile's last one: loads there give zeros,
+            // stores are dropped, and no branch stands between the loads and their use.
+            float in[W - 1 + kGroup][V];
+            u32x4 next[kGroup];
 #pragma unroll
             for (int j = 0; j < W - 1; ++j) input_at<T, W>(a, lo, from - (W - 1) + j, slot, w.c, in[j]);
-            const T* x = static_cast<const T*>(a.x) + (size_t)lo * a.x_stride + w.c;
-            T* y = static_cast<T*>(a.y[w.seg]) + (size_t)lo * a.channels[w.seg] + w.ch;
+            const T* x = static_cast<const T*>(a.x);
+            T* y = static_cast<T*>(a.y[seg]);
+            auto row = [&](const void* base, int64_t p, int64_t stride, int width) {
+                return __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(static_cast<const T*>(base) + (p < to ? lo + p : 0) * stride), (short)0,
+                                                         p < to ? width * (int)sizeof(T) : 0, 0x00020000);
+            };
             auto fetch = [&](int64_t p) {
 #pragma unroll
                 for (int k = 0; k < kGroup; ++k)
-                    if (p + k < to) dev::load_vec(x + (size_t)(p + k) * a.x_stride, next[k]);
+                    next[k] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(row(x, p + k, a.x_stride, a.C), w.c * (int)sizeof(T), 0, 0));
             };
             fetch(from);
             for (int64_t p = from; p < to; p += kGroup) {
 #pragma unroll
-                for (int k = 0; k < kGroup; ++k)
-#pragma unroll
-                    for (int e = 0; e < V; ++e) in[W - 1 + k][e] = next[k][e];
+                for (int k = 0; k < kGroup; ++k) dev::widen_vec<T>(next[k], in[W - 1 + k]);
                 fetch(p + kGroup);
+                float u[kGroup][V];
+                taps.apply(a, l2_dim, in, u);
 #pragma unroll
                 for (int k = 0; k < kGroup; ++k)
-                    if (p + k < to) {
-                        float u[V];
-                        taps.apply(a, l2_dim, in + k, u);
-                        dev::store_vec(y + (size_t)(p + k) * a.channels[w.seg], u);
-                    }
+                    __builtin_amdgcn_raw_buffer_store_b128(dev::narrow_vec<T>(u[k]), row(y, p + k, width, width), w.ch * (int)sizeof(T), 0, 0);
 #pragma unroll
                 for (int j = 0; j < W - 1; ++j)
 #pragma unroll
@@ -221,11 +240,11 @@ __global__ __launch_bounds__(kThreads) void conv_decode_kernel(ConvArgs a) {
     const int b = blockIdx.x;
     const int slot = slot_or_none(a.init_slot, b, a.num_slots), fin = slot_or_none(a.final_slot, b, a.num_slots);
     T* y = static_cast<T*>(a.y[w.seg]) + (size_t)b * a.channels[w.seg] + w.ch;
-    float in[W][V], u[V];
+    float in[W][V], u[1][V];
     if (slot < 0) {                              // padding row
 #pragma unroll
-        for (int e = 0; e < V; ++e) u[e] = 0.f;
-        dev::store_vec(y, u);
+        for (int e = 0; e < V; ++e) u[0][e] = 0.f;
+        dev::store_vec(y, u[0]);
         return;
     }
     Taps<T, W> taps;
@@ -233,7 +252,7 @@ __global__ __launch_bounds__(kThreads) void conv_decode_kernel(ConvArgs a) {
 #pragma unroll
     for (int j = 0; j < W; ++j) input_at<T, W>(a, b, j - (W - 1), slot, w.c, in[j]);
     taps.apply(a, a.l2_dim[w.seg], in, u);
-    dev::store_vec(y, u);
+    dev::store_vec(y, u[0]);
     if (fin < 0) return;
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) dev::store_vec(static_cast<T*>(a.pool) + ((size_t)fin * (W - 1) + j) * a.C + w.c, in[j + 1]);

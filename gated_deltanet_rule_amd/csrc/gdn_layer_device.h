@@ -44,6 +44,32 @@ __device__ __forceinline__ void store_vec(__bf16* p, const float (&v)[8]) {
     *reinterpret_cast<bf16x8_t*>(p) = x;
 }
 
+// The same from and to 16 bytes in registers.
+typedef unsigned u32x4_t __attribute__((ext_vector_type(4)));
+template <typename T>
+__device__ __forceinline__ void widen_vec(u32x4_t w, float (&v)[kVec<T>]) {
+    if constexpr (sizeof(T) == 4) {
+        const f32x4_t x = __builtin_bit_cast(f32x4_t, w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = x[i];
+    } else {
+        const bf16x8_t x = __builtin_bit_cast(bf16x8_t, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = (float)x[i];
+    }
+}
+template <typename T>
+__device__ __forceinline__ u32x4_t narrow_vec(const float (&v)[kVec<T>]) {
+    if constexpr (sizeof(T) == 4) {
+        return __builtin_bit_cast(u32x4_t, f32x4_t{v[0], v[1], v[2], v[3]});
+    } else {
+        bf16x8_t x;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = (__bf16)v[i];
+        return __builtin_bit_cast(u32x4_t, x);
+    }
+}
+
 // e^v as 2^(v log2 e): one rounding of the exponent (|v| 2^-24 relative) and the hardware's
 // exp2, good to one unit in the last place; 0 and infinity where the exponent leaves fp32.
 __device__ __forceinline__ float exp_fast(float v) { return __builtin_amdgcn_exp2f(v * 1.4426950408889634f); }
@@ -76,6 +102,19 @@ __device__ __forceinline__ float group_sum(float x, int lanes) {
     if (lanes > 16) x += __shfl_xor(x, 16);
     if (lanes > 32) x += __shfl_xor(x, 32);
     return x;
+}
+
+// group_sum of N values side by side.
+template <int N>
+__device__ __forceinline__ void group_sums(float (&x)[N], int lanes) {
+#define GDN_EACH(term) _Pragma("unroll") for (int k = 0; k < N; ++k) x[k] += term
+    if (lanes > 1) GDN_EACH(dpp_move<0xB1>(x[k]));
+    if (lanes > 2) GDN_EACH(dpp_move<0x4E>(x[k]));
+    if (lanes > 4) GDN_EACH(dpp_move<0x141>(x[k]));
+    if (lanes > 8) GDN_EACH(dpp_move<0x140>(x[k]));
+    if (lanes > 16) GDN_EACH(__shfl_xor(x[k], 16));
+    if (lanes > 32) GDN_EACH(__shfl_xor(x[k], 32));
+#undef GDN_EACH
 }
 
 }  // namespace dev
