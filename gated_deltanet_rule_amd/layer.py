@@ -70,15 +70,21 @@ def library():
 
 # ---------------------------------------------------------------- marshalling
 
+# A small call's time is its marshalling, not its kernel: tensors are checked in one condition
+# (the reason is worked out only for a refusal), and the current stream is taken as the handle
+# it is instead of through a Stream object.
+
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _enqueue(name, device, stream, *args):
     fn = getattr(_lib or library(), name)
-    if torch.cuda.current_device() == device.index:
-        s = torch.cuda.current_stream(device) if stream is None else stream
-        status = fn(*args, s.cuda_stream)
+    index = device.index
+    if torch.cuda.current_device() == index:
+        status = fn(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
     else:
         with torch.cuda.device(device):
-            s = torch.cuda.current_stream(device) if stream is None else stream
-            status = fn(*args, s.cuda_stream)
+            status = fn(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
     if status:
         binding._check(status)
 
@@ -98,17 +104,21 @@ def _code(t, name="tensors"):
     raise ValueError("%s must be bfloat16 or float32, got %s" % (name, t.dtype))
 
 
-def _dense(t, name, dtype, device, *shape):
-    """Address of a contiguous tensor of this dtype, device and shape."""
+def _refuse(t, name, dtype, device, shape):
     if t.dtype is not dtype:
         raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if t.device != device:
         raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
     if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-    return t.data_ptr()
+
+
+def _dense(t, name, dtype, device, *shape):
+    """Address of a contiguous tensor of this dtype, device and shape."""
+    if t.dtype is dtype and t.device == device and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, name, dtype, device, shape)
+    raise ValueError("%s must be contiguous" % name)
 
 
 def _maybe(t, name, dtype, device, *shape):
@@ -117,19 +127,15 @@ def _maybe(t, name, dtype, device, *shape):
 
 def _rows(t, name, dtype, device, *shape):
     """Address and row stride of a tensor whose rows are dense but may be part of wider ones."""
-    if t.dtype is not dtype:
-        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.device != device:
-        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
-    if t.shape != shape:
-        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.dtype is not dtype or t.device != device or t.shape != shape:
+        _refuse(t, name, dtype, device, shape)
+    strides = t.stride()
     width = 1
-    for size, step in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+    for size, step in zip(shape[:0:-1], strides[:0:-1]):
         if size != 1 and step != width:
-            raise ValueError("%s must have dense rows, got strides %s" % (name, t.stride()))
+            raise ValueError("%s must have dense rows, got strides %s" % (name, strides))
         width *= size
-    stride = t.stride(0) if t.shape[0] > 1 else -(-width // 8) * 8
-    return t.data_ptr(), stride
+    return t.data_ptr(), strides[0] if shape[0] > 1 else -(-width // 8) * 8
 
 
 def _activation(name):
@@ -205,6 +211,9 @@ def gdn_step_plan(computed, new_tokens, state_table, run_slot, *, num_decode_row
 
 # ---------------------------------------------------------------- short causal convolution
 
+_OUTS = ("outs[0]", "outs[1]", "outs[2]")
+
+
 def _conv_common(x, weight, bias, outs, conv_pool, activation, l2_dims, l2_eps):
     dev = _device(x, "x")
     if x.dim() != 2 or weight.dim() != 2 or conv_pool.dim() != 3:
@@ -212,16 +221,13 @@ def _conv_common(x, weight, bias, outs, conv_pool, activation, l2_dims, l2_eps):
     if not 1 <= len(outs) <= 3 or len(l2_dims) < len(outs):
         raise ValueError("one to three outputs are taken, with an l2_dims entry for each")
     (tokens, channels), width, dtype = x.shape, weight.shape[1], x.dtype
-    shape = GdnConvShape()
-    y, total = [None, None, None], 0
+    y, runs, l2 = [None, None, None], [0, 0, 0], [0, 0, 0]
     for i, o in enumerate(outs):
-        c = o.shape[-1]
-        y[i] = _dense(o, "outs[%d]" % i, dtype, dev, tokens, c)
-        shape.channels[i], shape.l2_dim[i] = c, int(l2_dims[i])
-        total += c
-    if total != channels:
-        raise ValueError("the outputs hold %d channels, x has %d" % (total, channels))
-    shape.width, shape.dtype, shape.activation, shape.l2_eps = width, _code(x, "x"), _activation(activation), l2_eps
+        runs[i], l2[i] = o.shape[-1], int(l2_dims[i])
+        y[i] = _dense(o, _OUTS[i], dtype, dev, tokens, runs[i])
+    if sum(runs) != channels:
+        raise ValueError("the outputs hold %d channels, x has %d" % (sum(runs), channels))
+    shape = GdnConvShape(tuple(runs), tuple(l2), width, _code(x, "x"), _activation(activation), l2_eps)
     px, stride = _rows(x, "x", dtype, dev, tokens, channels)
     slots = conv_pool.shape[0]
     return dev, shape, tokens, (px, stride, _dense(weight, "weight", torch.float32, dev, channels, width),
