@@ -59,10 +59,20 @@ typedef __amdgpu_buffer_rsrc_t rsrc_t;
 
 // ---------------------------------------------------------------- operands
 
+// A value that is the same in every lane, in a scalar register for certain: loaded values are
+// otherwise kept in vector registers, and buffers made from them are taken apart lane by lane.
+__device__ __forceinline__ int uniform(int x) {
+    x = __builtin_amdgcn_readfirstlane(x);
+    asm("" : "+s"(x));
+    return x;
+}
+
 // A chunk's rows of a token-major tensor as a raw buffer of `bytes`: loads past it give
 // zeros and stores past it are dropped, which is how rows beyond a chunk's end enter.
 __device__ __forceinline__ rsrc_t rows_rsrc(const void* base, int bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, bytes, 0x00020000);
+    const uintptr_t p = reinterpret_cast<uintptr_t>(base);
+    const uint64_t at = (uint64_t)(unsigned)uniform((int)(p >> 32)) << 32 | (unsigned)uniform((int)p);
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(at), (short)0, uniform(bytes), 0x00020000);
 }
 __device__ __forceinline__ u32x4 load16(rsrc_t r, int off) {
     return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
@@ -269,9 +279,9 @@ struct Walk {
     int64_t start;
     __device__ __forceinline__ Walk(const SsmArgs& a, int i) {
         dev::seq_range(a.cu_seqlens, i, a.total_tokens, lo, len);
-        lo = __builtin_amdgcn_readfirstlane(lo);
-        len = __builtin_amdgcn_readfirstlane(len);
-        start = a.start_pos ? __builtin_amdgcn_readfirstlane(a.start_pos[i]) : 0;
+        lo = uniform(lo);
+        len = uniform(len);
+        start = uniform(a.start_pos ? a.start_pos[i] : 0);
         skew = (int)(start & (kC - 1));
         chunks = dev::seq_chunks(len, skew);
     }
