@@ -51,6 +51,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
@@ -134,12 +135,13 @@ struct Ops<__bf16> {
         const int row = lane >> 2, at = row * pitch + ((4 * (lane & 3)) ^ (row & 8));
         return __builtin_bit_cast(Half, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(m + at + (r0 * pitch + c0))));
     }
-    static __device__ __forceinline__ unsigned exponents(u32x4 w) {
-        unsigned m = 0;
+    // larger of m's and w's exponents, two bf16 to a word; whether one says infinity or NaN
+    static __device__ __forceinline__ unsigned exponents(u32x4 w, unsigned m) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) m = max(m, max(w[i] & 0x7f800000u, (w[i] << 16) & 0x7f800000u));
+        for (int i = 0; i < 4; ++i) m = __builtin_bit_cast(unsigned, __builtin_elementwise_max(__builtin_bit_cast(u16x2, m), __builtin_bit_cast(u16x2, w[i] & 0x7f807f80u)));
         return m;
     }
+    static __device__ __forceinline__ bool not_finite(unsigned m) { return (m >> 16) == 0x7f80u || (m & 0xffffu) == 0x7f80u; }
 };
 
 template <>
@@ -170,12 +172,12 @@ struct Ops<float> {
         const float* p = m + (4 * (lane >> 4) * pitch + (lane & 15)) + (r0 * pitch + c0);
         return f32x4{p[0], p[pitch], p[2 * pitch], p[3 * pitch]};
     }
-    static __device__ __forceinline__ unsigned exponents(u32x4 w) {
-        unsigned m = 0;
+    static __device__ __forceinline__ unsigned exponents(u32x4 w, unsigned m) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) m = max(m, w[i] & 0x7f800000u);
         return m;
     }
+    static __device__ __forceinline__ bool not_finite(unsigned m) { return m == 0x7f800000u; }
 };
 
 // ---------------------------------------------------------------- steps and decays of a chunk
@@ -391,8 +393,8 @@ struct Staged {
         unsigned m = 0;
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            if (VECS % TH == 0 || tid + k * TH < VECS) m = max(m, Ops<T>::exponents(v[k]));
-        return m == 0x7f800000u;
+            if (VECS % TH == 0 || tid + k * TH < VECS) m = Ops<T>::exponents(v[k], m);
+        return Ops<T>::not_finite(m);
     }
 };
 
@@ -524,17 +526,18 @@ __global__ __launch_bounds__(4 * DV / CT, sizeof(T) == 2 ? DV / CT / 32 : 1) voi
         dev::lds_barrier();
         fetch(c + 1);
         // lower tiles of W, in turn
-#pragma unroll
-        for (int k = 0; k < (10 + NW - 1) / NW; ++k) {
-            const int blk = wv + NW * k;
-            if (blk < 10) {
-                const int it = blk >= 6 ? 3 : blk >= 3 ? 2 : blk >= 1 ? 1 : 0, jt = blk - it * (it + 1) / 2;
-                const T* cb = sm.c + it * 16 * DK;
-                const f32x4 s = score_tile<T, DK>(sm.b, SM::BP, jt, lane, [&](int p, Half& h0, Half& h1) { pair_of<T, DK>(cb, p, lane, h0, h1); });
-                *reinterpret_cast<Half*>(sm.w + blk * 256 + lane * 4) = decayed<T>(g, s, it, jt, lane);
-            }
-            __builtin_amdgcn_sched_barrier(0);
-        }
+        auto form = [&](int blk) {
+            const int it = blk >= 6 ? 3 : blk >= 3 ? 2 : blk >= 1 ? 1 : 0, jt = blk - it * (it + 1) / 2;
+            const T* cb = sm.c + it * 16 * DK;
+            const f32x4 s = score_tile<T, DK>(sm.b, SM::BP, jt, lane, [&](int p, Half& h0, Half& h1) { pair_of<T, DK>(cb, p, lane, h0, h1); });
+            *reinterpret_cast<Half*>(sm.w + blk * 256 + lane * 4) = decayed<T>(g, s, it, jt, lane);
+        };
+        static_assert(NW == 4, "ten tiles go round the waves");
+        form(wv);
+        form(wv + 4);
+        __builtin_amdgcn_sched_barrier(0);
+        if (wv < 2) form(wv + 8);
+        __builtin_amdgcn_sched_barrier(0);
         // Y^T = S^T C^T, then the rows' e^G
         f32x4 y[TT][CT];
 #pragma unroll
@@ -577,12 +580,17 @@ __global__ __launch_bounds__(4 * DV / CT, sizeof(T) == 2 ? DV / CT / 32 : 1) voi
         for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
             for (int t = 0; t < TT; ++t) x[ct][t] = Ops<T>::col_half(sm.x, SM::XP, 16 * t, col0 + 16 * ct, lane);
-        int bad[CT];
+        const bool poisoned = sm.bad[c & 1] == c + 1;
+        if (poisoned)
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct) bad[ct] = kC;
-        if (sm.bad[c & 1] == c + 1)
+            for (int ct = 0; ct < CT; ++ct) {
+                const int bad = take_out<T>(x[ct], lane);
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) bad[ct] = take_out<T>(x[ct], lane);
+                for (int it = 0; it < TT; ++it)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (__shfl(bad, g4 + e) <= 16 * it + li) y[it][ct][e] = __builtin_nanf("");
+            }
 #pragma unroll
         for (int it = 0; it < TT; ++it)
 #pragma unroll
@@ -606,15 +614,11 @@ __global__ __launch_bounds__(4 * DV / CT, sizeof(T) == 2 ? DV / CT / 32 : 1) voi
                 f32x4 o;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[e] = fmaf(a.scale, y[it][ct][e], D * xt[e]);
-                if (sm.bad[c & 1] == c + 1)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (__shfl(bad[ct], g4 + e) <= t) o[e] = __builtin_nanf("");
                 Ops<T>::store_half(Ops<T>::round(o), ry, t * vrow + p * (int)sizeof(T));
             }
         __builtin_amdgcn_sched_barrier(0);
         // S <- e^(G_last) S + B^T (w X), x as it came
-        if (sm.bad[c & 1] == c + 1)
+        if (poisoned)
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
