@@ -532,11 +532,12 @@ __global__ __launch_bounds__(4 * DV / CT, sizeof(T) == 2 ? DV / CT / 32 : 1) voi
             const f32x4 s = score_tile<T, DK>(sm.b, SM::BP, jt, lane, [&](int p, Half& h0, Half& h1) { pair_of<T, DK>(cb, p, lane, h0, h1); });
             *reinterpret_cast<Half*>(sm.w + blk * 256 + lane * 4) = decayed<T>(g, s, it, jt, lane);
         };
-        static_assert(NW == 4, "ten tiles go round the waves");
-        form(wv);
-        form(wv + 4);
-        __builtin_amdgcn_sched_barrier(0);
-        if (wv < 2) form(wv + 8);
+        static_assert(NW == 4, "ten tiles: three to each wave, one to the last, which makes the gates");
+        form(wv < 3 ? wv : 9);
+        if (wv < 3) {
+            form(wv + 3);
+            form(wv + 6);
+        }
         __builtin_amdgcn_sched_barrier(0);
         // Y^T = S^T C^T, then the rows' e^G
         f32x4 y[TT][CT];
