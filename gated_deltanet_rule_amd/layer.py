@@ -12,6 +12,7 @@ be columns of a wider matrix.  Weights and per-head parameters are float32.
 from __future__ import annotations
 
 import ctypes
+import functools
 import threading
 from typing import Optional, Sequence
 
@@ -53,6 +54,7 @@ SIGNATURES = {
 
 _lock = threading.Lock()
 _lib = None
+_entry = {}          # the declared entry points by name, once the library is loaded
 
 
 def library():
@@ -64,6 +66,7 @@ def library():
             for name, (res, args) in SIGNATURES.items():
                 fn = getattr(lib, name)
                 fn.restype, fn.argtypes = res, args
+                _entry[name] = fn
             _lib = lib
     return _lib
 
@@ -71,14 +74,14 @@ def library():
 # ---------------------------------------------------------------- marshalling
 
 # A small call's time is its marshalling, not its kernel: tensors are checked in one condition
-# (the reason is worked out only for a refusal), and the current stream is taken as the handle
-# it is instead of through a Stream object.
+# (the reason is worked out only for a refusal), shapes are kept as C structures by their values,
+# and the current stream is taken as the handle it is instead of through a Stream object.
 
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _enqueue(name, device, stream, *args):
-    fn = getattr(_lib or library(), name)
+    fn = _entry.get(name) or getattr(library(), name)
     index = device.index
     if torch.cuda.current_device() == index:
         status = fn(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
@@ -214,6 +217,16 @@ def gdn_step_plan(computed, new_tokens, state_table, run_slot, *, num_decode_row
 _OUTS = ("outs[0]", "outs[1]", "outs[2]")
 
 
+@functools.lru_cache(maxsize=256)
+def _conv_shape(channels, l2_dim, width, dtype, activation, l2_eps):
+    return GdnConvShape(channels, l2_dim, width, dtype, activation, l2_eps)
+
+
+@functools.lru_cache(maxsize=256)
+def _head_shape(groups, heads, d_k, d_v, dtype, scale):
+    return GdnShape(groups, heads, d_k, d_v, dtype, scale)
+
+
 def _conv_common(x, weight, bias, outs, conv_pool, activation, l2_dims, l2_eps):
     dev = _device(x, "x")
     if x.dim() != 2 or weight.dim() != 2 or conv_pool.dim() != 3:
@@ -227,7 +240,7 @@ def _conv_common(x, weight, bias, outs, conv_pool, activation, l2_dims, l2_eps):
         y[i] = _dense(o, _OUTS[i], dtype, dev, tokens, runs[i])
     if sum(runs) != channels:
         raise ValueError("the outputs hold %d channels, x has %d" % (sum(runs), channels))
-    shape = GdnConvShape(tuple(runs), tuple(l2), width, _code(x, "x"), _activation(activation), l2_eps)
+    shape = _conv_shape(tuple(runs), tuple(l2), width, _code(x, "x"), _activation(activation), float(l2_eps))
     px, stride = _rows(x, "x", dtype, dev, tokens, channels)
     slots = conv_pool.shape[0]
     return dev, shape, tokens, (px, stride, _dense(weight, "weight", torch.float32, dev, channels, width),
@@ -266,7 +279,7 @@ def _ssm_common(c, b, x, dt, A, y, state_pool, dt_bias, D, dt_softplus, scale):
     if x.dim() != 3 or c.dim() != 3:
         raise ValueError("x and c must have 3 dims, got %s and %s" % (tuple(x.shape), tuple(c.shape)))
     (tokens, heads, d_v), groups, d_k, dtype, f32 = x.shape, c.shape[1], c.shape[2], x.dtype, torch.float32
-    shape = GdnShape(groups, heads, d_k, d_v, _code(x, "x"), scale)
+    shape = _head_shape(groups, heads, d_k, d_v, _code(x, "x"), float(scale))
     params = GdnSsmParams(_dense(A, "A", f32, dev, heads), _maybe(dt_bias, "dt_bias", f32, dev, heads),
                           _maybe(D, "D", f32, dev, heads), 1 if dt_softplus else 0)
     slots = state_pool.shape[0]
