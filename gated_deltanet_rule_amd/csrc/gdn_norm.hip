@@ -5,11 +5,12 @@
 //
 // Memory-bound: every operand crosses HBM once.  The values of a norm stay in registers
 // between its sum and its output; TPG threads share one norm, R vectors of V elements each,
-// as many vectors as its dim needs: 16 lanes for short norms (four to a wave), one wave,
+// as many vectors as its dim needs: one lane, 16 lanes (four norms to a wave), one wave,
 // then one workgroup of four or sixteen waves.  A sum is taken per thread in order, then
-// over the lanes and the waves in a fixed tree, so a row's bits depend on its dim and
-// alignment alone.  131072 x 32 gated rows of 128 bf16 values: 538 us, 6.0 TB/s; 16384 residual
-// rows of 4096 with an fp32 residual: 173 us, 5.4 TB/s (a large copy: 4.95 TB/s).
+// over the lanes and the waves in a fixed tree, so a row's bits depend on its dim alone.  131072 x 32 gated rows of 128 bf16 values: 538 us, 6.0 TB/s; 16384 residual
+// rows of 4096 with an fp32 residual: 173 us, 5.4 TB/s (a large copy: 4.95 TB/s).  Rows of any other dim or alignment take unaligned
+// vectors: 6709 residual rows of 5001 bf16 values 118 us (element by element: 261), 4096 gated
+// rows of 4096 at an odd stride 24 us (96).
 #include <hip/hip_runtime.h>
 
 #include "gdn_layer_device.h"
@@ -20,25 +21,67 @@ namespace {
 
 constexpr int kThreads = 256;
 
-template <typename T, int V>
-__device__ __forceinline__ void load_some(const T* p, float (&v)[V]) {
-    if constexpr (V == 1) v[0] = (float)*p;
-    else if constexpr (V * sizeof(T) == 16) dev::load_vec(p, v);
-    else dev::load_floats(p, v);
+// Global memory takes vectors at any element's address, so a row that starts or ends anywhere
+// costs little more than an aligned one.  Vectors of a row whose last one is not whole: that
+// one is moved back to end with the row, and its first `skip` elements, which the vector
+// before holds too, are left out of sums (both lanes compute and store the same values).
+struct Place {
+    int e, skip;
+};
+template <int V, bool WIDE>
+__device__ __forceinline__ Place place(int e, int dim) {
+    if (WIDE || dim < V || e + V <= dim) return {e, 0};
+    return {dim - V, e + V - dim};
 }
 
-template <typename T, int V>
-__device__ __forceinline__ void store_some(T* p, const float (&v)[V]) {
-    if constexpr (V == 1) {
-        *p = (T)v[0];
-    } else if constexpr (V * sizeof(T) == 16) {
-        dev::store_vec(p, v);
+template <int V, bool WIDE>
+__device__ __forceinline__ float add_squares(const float (&x)[V], int skip, float s) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const float v = WIDE || i >= skip ? x[i] : 0.f;
+        s = fmaf(v, v, s);
+    }
+    return s;
+}
+
+// V elements at p, of which `left` belong to the row: all of them but for rows shorter than V.
+template <typename T, int V, bool WIDE>
+__device__ __forceinline__ void load_some(const T* p, int left, float (&v)[V]) {
+    constexpr int N = dev::kVec<T>;
+    if (WIDE || left >= V) {
+#pragma unroll
+        for (int i = 0; i < V; i += N) {
+            dev::u32x4_t w;
+            float q[N];
+            if constexpr (WIDE) w = *reinterpret_cast<const dev::u32x4_t*>(p + i);
+            else __builtin_memcpy(&w, p + i, 16);
+            dev::widen_vec<T>(w, q);
+#pragma unroll
+            for (int k = 0; k < N; ++k) v[i + k] = q[k];
+        }
     } else {
 #pragma unroll
-        for (int i = 0; i < V; i += 4) {
-            const float q[4] = {v[i], v[i + 1], v[i + 2], v[i + 3]};
-            dev::store_vec(p + i, q);
+        for (int i = 0; i < V; ++i) v[i] = i < left ? (float)p[i] : 0.f;
+    }
+}
+
+template <typename T, int V, bool WIDE>
+__device__ __forceinline__ void store_some(T* p, int left, const float (&v)[V]) {
+    constexpr int N = dev::kVec<T>;
+    if (WIDE || left >= V) {
+#pragma unroll
+        for (int i = 0; i < V; i += N) {
+            float q[N];
+#pragma unroll
+            for (int k = 0; k < N; ++k) q[k] = v[i + k];
+            const dev::u32x4_t w = dev::narrow_vec<T>(q);
+            if constexpr (WIDE) *reinterpret_cast<dev::u32x4_t*>(p + i) = w;
+            else __builtin_memcpy(p + i, &w, 16);
         }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i < left) p[i] = (T)v[i];
     }
 }
 
@@ -77,9 +120,9 @@ __device__ __forceinline__ float norm_sum(float x, float* sums) {
 }
 
 // U norms per thread, all of their loads issued first.
-template <typename T, int V, int TPG, int R, int U>
+template <typename T, bool WIDE, int TPG, int R, int U>
 __global__ __launch_bounds__(TPG > kThreads ? TPG : kThreads) void gated_norm_kernel(GatedNormArgs a) {
-    constexpr int PER = TPG > kThreads ? 1 : kThreads / TPG;
+    constexpr int V = dev::kVec<T>, PER = TPG > kThreads ? 1 : kThreads / TPG;
     __shared__ float sums[TPG > 64 ? TPG / 64 : 1];
     const unsigned total = (unsigned)(a.num_rows * a.groups);
     const int lane = threadIdx.x % TPG;
@@ -96,10 +139,10 @@ __global__ __launch_bounds__(TPG > kThreads ? TPG : kThreads) void gated_norm_ke
         const T* pz = static_cast<const T*>(a.z) + row[u] * a.z_stride + (size_t)g[u] * a.dim;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const int e = (lane + r * TPG) * V;
-            if (idx[u] < total && e < a.dim) {
-                load_some(px + e, x[u][r]);
-                if (a.z) load_some(pz + e, z[u][r]);
+            const int e0 = (lane + r * TPG) * V, e = place<V, WIDE>(e0, a.dim).e;
+            if (idx[u] < total && e0 < a.dim) {
+                load_some<T, V, WIDE>(px + e, a.dim - e, x[u][r]);
+                if (a.z) load_some<T, V, WIDE>(pz + e, a.dim - e, z[u][r]);
             } else {
 #pragma unroll
                 for (int i = 0; i < V; ++i) x[u][r][i] = z[u][r][i] = 0.f;
@@ -119,32 +162,30 @@ __global__ __launch_bounds__(TPG > kThreads ? TPG : kThreads) void gated_norm_ke
         }
         float s = 0.f;
 #pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-            for (int i = 0; i < V; ++i) s = fmaf(x[u][r][i], x[u][r][i], s);
+        for (int r = 0; r < R; ++r) s = add_squares<V, WIDE>(x[u][r], place<V, WIDE>((lane + r * TPG) * V, a.dim).skip, s);
         const float n = dev::inv_sqrt(fmaf(norm_sum<TPG>(s, sums), inv_dim, a.eps));
         const float* pw = a.weight + (a.weight_per_group ? (size_t)g[u] * a.dim : 0);
         T* py = static_cast<T*>(a.y) + ((size_t)row[u] * a.groups + g[u]) * a.dim;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const int e = (lane + r * TPG) * V;
-            if (idx[u] < total && e < a.dim) {
+            const int e0 = (lane + r * TPG) * V, e = place<V, WIDE>(e0, a.dim).e;
+            if (idx[u] < total && e0 < a.dim) {
                 float w[V];
-                load_some(pw + e, w);
+                load_some<float, V, WIDE>(pw + e, a.dim - e, w);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     w[i] *= x[u][r][i] * n;
                     if (a.z && !a.gate_first) w[i] *= z[u][r][i];
                 }
-                store_some(py + e, w);
+                store_some<T, V, WIDE>(py + e, a.dim - e, w);
             }
         }
     }
 }
 
-template <typename T, typename RT, int V, int TPG, int R>
+template <typename T, typename RT, bool WIDE, int TPG, int R>
 __global__ __launch_bounds__(TPG > kThreads ? TPG : kThreads) void residual_norm_kernel(ResidualNormArgs a) {
-    constexpr int PER = TPG > kThreads ? 1 : kThreads / TPG;
+    constexpr int V = dev::kVec<T>, PER = TPG > kThreads ? 1 : kThreads / TPG;
     __shared__ float sums[TPG > 64 ? TPG / 64 : 1];
     const int64_t row = (int64_t)blockIdx.x * PER + threadIdx.x / TPG;
     const int lane = threadIdx.x % TPG;
@@ -157,11 +198,11 @@ __global__ __launch_bounds__(TPG > kThreads ? TPG : kThreads) void residual_norm
     float x[R][V], q[R][V], z[R][V];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        const int e = (lane + r * TPG) * V;
-        if (live && e < a.dim) {
-            load_some(px + e, x[r]);
-            load_some(pr + e, q[r]);
-            if (a.gate) load_some(pz + e, z[r]);
+        const int e0 = (lane + r * TPG) * V, e = place<V, WIDE>(e0, a.dim).e;
+        if (live && e0 < a.dim) {
+            load_some<T, V, WIDE>(px + e, a.dim - e, x[r]);
+            load_some<RT, V, WIDE>(pr + e, a.dim - e, q[r]);
+            if (a.gate) load_some<T, V, WIDE>(pz + e, a.dim - e, z[r]);
         } else {
 #pragma unroll
             for (int i = 0; i < V; ++i) x[r][i] = q[r][i] = z[r][i] = 0.f;
@@ -170,25 +211,27 @@ __global__ __launch_bounds__(TPG > kThreads ? TPG : kThreads) void residual_norm
     if (a.post_weight) {
         float s = 0.f;
 #pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-            for (int i = 0; i < V; ++i) s = fmaf(x[r][i], x[r][i], s);
+        for (int r = 0; r < R; ++r) s = add_squares<V, WIDE>(x[r], place<V, WIDE>((lane + r * TPG) * V, a.dim).skip, s);
         const float n = dev::inv_sqrt(fmaf(norm_sum<TPG>(s, sums), inv_dim, a.eps));
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const int e = (lane + r * TPG) * V;
-            if (e < a.dim) {
+            const int e0 = (lane + r * TPG) * V, e = place<V, WIDE>(e0, a.dim).e;
+            if (e0 < a.dim) {
                 float w[V];
-                load_some(a.post_weight + e, w);
+                load_some<float, V, WIDE>(a.post_weight + e, a.dim - e, w);
 #pragma unroll
                 for (int i = 0; i < V; ++i) x[r][i] *= n * w[i];
             }
         }
     }
+    // a residual in place: its shared elements are all read before one of them is written
+    if (!WIDE && TPG > 64) __syncthreads();
     float s = 0.f;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        const int e = (lane + r * TPG) * V;
+        const int e0 = (lane + r * TPG) * V;
+        const Place at = place<V, WIDE>(e0, a.dim);
+        const int e = at.e;
         if (a.gate) {
             gate(z[r], a.activation);
 #pragma unroll
@@ -197,10 +240,9 @@ __global__ __launch_bounds__(TPG > kThreads ? TPG : kThreads) void residual_norm
 #pragma unroll
         for (int i = 0; i < V; ++i) q[r][i] = fmaf(a.residual_scale, x[r][i], q[r][i]);
         round_to<RT>(q[r]);
-        if (live && e < a.dim) {
-            store_some(po + e, q[r]);
-#pragma unroll
-            for (int i = 0; i < V; ++i) s = fmaf(q[r][i], q[r][i], s);
+        if (live && e0 < a.dim) {
+            store_some<RT, V, WIDE>(po + e, a.dim - e, q[r]);
+            s = add_squares<V, WIDE>(q[r], at.skip, s);
         }
     }
     if (!a.y) return;
@@ -208,53 +250,58 @@ __global__ __launch_bounds__(TPG > kThreads ? TPG : kThreads) void residual_norm
     T* py = static_cast<T*>(a.y) + (size_t)row * a.dim;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        const int e = (lane + r * TPG) * V;
-        if (live && e < a.dim) {
+        const int e0 = (lane + r * TPG) * V, e = place<V, WIDE>(e0, a.dim).e;
+        if (live && e0 < a.dim) {
             float w[V];
-            load_some(a.pre_weight + e, w);
+            load_some<float, V, WIDE>(a.pre_weight + e, a.dim - e, w);
 #pragma unroll
             for (int i = 0; i < V; ++i) w[i] *= q[r][i] * n;
-            store_some(py + e, w);
+            store_some<T, V, WIDE>(py + e, a.dim - e, w);
         }
     }
 }
 
-template <typename T, int V, int TPG, int R>
+template <typename T, bool WIDE, int TPG, int R>
 void gated(const GatedNormArgs& a, hipStream_t stream) {
     constexpr int PER = TPG > kThreads ? 1 : kThreads / TPG, THREADS = TPG > kThreads ? TPG : kThreads;
     const int64_t n = (a.num_rows * a.groups + PER - 1) / PER;
-    hipLaunchKernelGGL((gated_norm_kernel<T, V, TPG, R, 1>), dim3((unsigned)n), dim3(THREADS), 0, stream, a);
+    hipLaunchKernelGGL((gated_norm_kernel<T, WIDE, TPG, R, 1>), dim3((unsigned)n), dim3(THREADS), 0, stream, a);
 }
 
 // Threads and vectors by the number of vectors in a norm: the smallest that holds it.
-template <typename T, int V>
+template <typename T, bool WIDE>
 void gated_by_dim(const GatedNormArgs& a, hipStream_t stream) {
+    constexpr int V = dev::kVec<T>;
     const int n = (a.dim + V - 1) / V;
-    if (n <= 16) gated<T, V, 16, 1>(a, stream);
-    else if (n <= 64) gated<T, V, 64, 1>(a, stream);
-    else if (n <= 256) gated<T, V, 64, 4>(a, stream);
-    else if (n <= 1024) gated<T, V, 256, 4>(a, stream);
-    else gated<T, V, 1024, V == 1 ? 16 : 4>(a, stream);
+    if (n <= 1) gated<T, WIDE, 1, 1>(a, stream);
+    else if (n <= 16) gated<T, WIDE, 16, 1>(a, stream);
+    else if (n <= 64) gated<T, WIDE, 64, 1>(a, stream);
+    else if (n <= 256) gated<T, WIDE, 64, 4>(a, stream);
+    else if (n <= 1024) gated<T, WIDE, 256, 4>(a, stream);
+    else gated<T, WIDE, 1024, 4>(a, stream);
 }
 
-template <typename T, typename RT, int V, int TPG, int R>
+template <typename T, typename RT, bool WIDE, int TPG, int R>
 void residual(const ResidualNormArgs& a, hipStream_t stream) {
     constexpr int PER = TPG > kThreads ? 1 : kThreads / TPG, THREADS = TPG > kThreads ? TPG : kThreads;
     const int64_t n = (a.num_rows + PER - 1) / PER;
-    hipLaunchKernelGGL((residual_norm_kernel<T, RT, V, TPG, R>), dim3((unsigned)n), dim3(THREADS), 0, stream, a);
+    hipLaunchKernelGGL((residual_norm_kernel<T, RT, WIDE, TPG, R>), dim3((unsigned)n), dim3(THREADS), 0, stream, a);
 }
 
-template <typename T, typename RT, int V>
+template <typename T, typename RT, bool WIDE>
 void residual_by_dim(const ResidualNormArgs& a, hipStream_t stream) {
+    constexpr int V = dev::kVec<T>;
     const int n = (a.dim + V - 1) / V;
-    if (n <= 64) residual<T, RT, V, 64, 1>(a, stream);
-    else if (n <= 256) residual<T, RT, V, 256, 1>(a, stream);
-    else if (n <= 512) residual<T, RT, V, 256, 2>(a, stream);
-    else if (n <= 1024) residual<T, RT, V, 256, 4>(a, stream);
-    else residual<T, RT, V, 1024, V == 1 ? 16 : 4>(a, stream);
+    if (n <= 1) residual<T, RT, WIDE, 1, 1>(a, stream);
+    else if (n <= 16) residual<T, RT, WIDE, 16, 1>(a, stream);
+    else if (n <= 64) residual<T, RT, WIDE, 64, 1>(a, stream);
+    else if (n <= 256) residual<T, RT, WIDE, 256, 1>(a, stream);
+    else if (n <= 512) residual<T, RT, WIDE, 256, 2>(a, stream);
+    else if (n <= 1024) residual<T, RT, WIDE, 256, 4>(a, stream);
+    else residual<T, RT, WIDE, 1024, 4>(a, stream);
 }
 
-// Whether rows of `dim` elements at this address and row stride can be read in 16-byte vectors.
+// Whether rows of `dim` elements at this address and row stride are whole, aligned 16-byte vectors.
 bool wide(const void* p, int64_t stride, int64_t rows, int dim, size_t size) {
     const size_t v = 16 / size;
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && dim % v == 0 && (rows == 1 || stride % v == 0);
@@ -266,16 +313,16 @@ void residual_typed(const ResidualNormArgs& a, hipStream_t stream) {
                     wide(a.residual_out, a.dim, 1, a.dim, sizeof(T)) && (!a.y || wide(a.y, a.dim, 1, a.dim, sizeof(T))) &&
                     (!a.gate || wide(a.gate, a.gate_stride, a.num_rows, a.dim, sizeof(T))) &&
                     reinterpret_cast<uintptr_t>(a.post_weight) % 16 == 0 && reinterpret_cast<uintptr_t>(a.pre_weight) % 16 == 0;
-    if (ok) residual_by_dim<T, RT, dev::kVec<T>>(a, stream);
-    else residual_by_dim<T, RT, 1>(a, stream);
+    if (ok) residual_by_dim<T, RT, true>(a, stream);
+    else residual_by_dim<T, RT, false>(a, stream);
 }
 
 template <typename T>
 void gated_typed(const GatedNormArgs& a, hipStream_t stream) {
     const bool ok = wide(a.x, a.x_stride, a.num_rows, a.dim, sizeof(T)) && wide(a.y, a.dim, 1, a.dim, sizeof(T)) &&
                     (!a.z || wide(a.z, a.z_stride, a.num_rows, a.dim, sizeof(T))) && reinterpret_cast<uintptr_t>(a.weight) % 16 == 0;
-    if (ok) gated_by_dim<T, dev::kVec<T>>(a, stream);
-    else gated_by_dim<T, 1>(a, stream);
+    if (ok) gated_by_dim<T, true>(a, stream);
+    else gated_by_dim<T, false>(a, stream);
 }
 
 }  // namespace

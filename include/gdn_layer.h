@@ -191,8 +191,8 @@ gdn_status gdn_ssm_recurrent_decode(const gdn_shape* shape, const gdn_ssm_params
  *   weight device fp32 [dim], shared by the groups, or [num_groups, dim] with
  *          weight_per_group
  *   y      device [num_rows, num_groups, dim] (dtype), dense; may be x itself when x is dense
- * Any 1 <= dim <= 16384; rows that are 16-byte aligned with dim a multiple of a 16-byte
- * vector take the wide loads.
+ * Any 1 <= dim <= 16384, any row stride and alignment to an element; aligned rows of whole
+ * 16-byte vectors are the fastest.
  */
 gdn_status gdn_gated_norm(int64_t num_rows, int32_t num_groups, int32_t dim, int32_t dtype,
                           const void* x, int64_t x_stride, const void* z, int64_t z_stride,

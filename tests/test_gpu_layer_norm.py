@@ -150,3 +150,28 @@ def test_refusals():
         layer.gdn_residual_norm(f, f.contiguous(), f.contiguous(), f.contiguous())
     with pytest.raises(layer.GdnError, match="residual_dtype"):
         layer.gdn_residual_norm(f, f.contiguous().bfloat16(), f.contiguous().bfloat16())
+
+
+@pytest.mark.parametrize("dtype,res", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+@pytest.mark.parametrize("dim", [3, 7, 9, 37, 129, 999, 2051, 4099, 9999])
+@pytest.mark.parametrize("post", [True, False])
+def test_rows_that_end_inside_a_vector_in_place(dtype, res, dim, post):
+    """Odd rows in place (the residual over itself, the gated norm over its input): the same bits as
+    into other memory, and nothing past the last row."""
+    g = torch.Generator().manual_seed(dim)
+    rows = 70
+    x, r = normal(g, rows, dim, dtype=dtype), normal(g, rows, dim, dtype=res)
+    w = 1.0 + normal(g, dim, dtype="f32") * 0.1
+    out, y = torch.empty_like(r), torch.empty_like(x)
+    kw = dict(post_weight=w if post else None, pre_weight=w, residual_scale=0.5)
+    layer.gdn_residual_norm(x, r, out, y, **kw)
+    guard = torch.full((rows + 1, dim), 7.0, dtype=r.dtype, device="cuda")
+    guard[:rows] = r
+    y2 = torch.full((rows + 1, dim), 7.0, dtype=x.dtype, device="cuda")
+    layer.gdn_residual_norm(x, guard[:rows], guard[:rows], y2[:rows], **kw)
+    assert torch.equal(guard[:rows], out) and torch.equal(y2[:rows], y) and (guard[rows] == 7).all() and (y2[rows] == 7).all()
+    layer.gdn_gated_norm(x[:, None], x[:, None], w, y[:, None])
+    same = torch.full((rows + 1, dim), 7.0, dtype=x.dtype, device="cuda")
+    same[:rows] = x
+    layer.gdn_gated_norm(same[:rows, None], x[:, None], w, same[:rows, None])
+    assert torch.equal(same[:rows], y) and (same[rows] == 7).all()
