@@ -465,6 +465,7 @@ __global__ __launch_bounds__(4 * DV / CT, sizeof(T) == 2 ? DV / CT / 32 : 1) voi
     const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int li = lane & 15, g4 = 4 * (lane >> 4), col0 = 16 * CT * wv;
     const size_t state = (size_t)a.H_v * DK * DV;
+    const int sin = a.init_slot[i], fin = a.final_slot[i];      // on their way beside the walk's loads
     const Walk walk(a, i);
     const float A = a.A[h], bias = a.dt_bias ? a.dt_bias[h] : 0.f, D = a.D ? a.D[h] : 0.f;
     const int krow = a.H_k * DK * (int)sizeof(T), vrow = a.H_v * DV * (int)sizeof(T);
@@ -475,7 +476,6 @@ __global__ __launch_bounds__(4 * DV / CT, sizeof(T) == 2 ? DV / CT / 32 : 1) voi
     // an address per element in registers)
     const unsigned mine = (unsigned)(g4 * DV + col0 + li);
     auto at = [](int nt, int ct, int e) { return (16 * nt + e) * DV + 16 * ct; };
-    const int sin = a.init_slot[i];
     const bool have = sin >= 0 && sin < a.num_slots;
     {
         const float* src = have ? a.pool + (size_t)sin * state + (size_t)h * DK * DV : nullptr;
@@ -668,7 +668,6 @@ __global__ __launch_bounds__(4 * DV / CT, sizeof(T) == 2 ? DV / CT / 32 : 1) voi
         if (dst) put(dst);
         dev::lds_barrier();
     }
-    const int fin = a.final_slot[i];
     if (fin >= 0 && fin < a.num_slots) put(a.pool + (size_t)fin * state);
 }
 
@@ -772,6 +771,7 @@ __global__ __launch_bounds__(kStripThreads, 3) void ssm_strip_kernel(SsmArgs a) 
     const int wv = wave & 3;             // its quarter of the tokens, of the state's rows, of the staging
     const int li = lane & 15, g4 = 4 * (lane >> 4);
     const size_t state = (size_t)a.H_v * DK * DV;
+    const int sin = a.init_slot[i], fin = a.final_slot[i];      // on their way beside the walk's loads
     const Walk walk(a, i);
     const int krow = a.H_k * DK * (int)sizeof(T), vrow = a.H_v * DV * (int)sizeof(T);
 
@@ -905,7 +905,6 @@ __global__ __launch_bounds__(kStripThreads, 3) void ssm_strip_kernel(SsmArgs a) 
             if (dst) put(dst);
             dev::lds_barrier();
         };
-        const int sin = a.init_slot[i];
         const bool have = sin >= 0 && sin < a.num_slots;
         const float* src = have ? a.pool + (size_t)sin * state + (size_t)h * DK * DV : nullptr;
 #pragma unroll
@@ -921,7 +920,6 @@ __global__ __launch_bounds__(kStripThreads, 3) void ssm_strip_kernel(SsmArgs a) 
             body(c, 0);
             body(c + 1, 1);
         }
-        const int fin = a.final_slot[i];
         if (fin >= 0 && fin < a.num_slots) put(a.pool + (size_t)fin * state);
         return;
     }
