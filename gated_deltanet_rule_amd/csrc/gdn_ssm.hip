@@ -10,8 +10,8 @@
 //     S   <- e^(G_last) S + B^T diag(e^(G_last - G) d) X
 // Only S goes from chunk to chunk.  Two workgroup shapes run the same arithmetic per
 // element, so a sequence's bits do not depend on which one its call takes:
-//   whole heads   one workgroup per (sequence, head), each of its four waves a quarter of
-//                 the columns with its part of S in accumulators; W is formed once and
+//   whole heads   one workgroup per (sequence, head), each of its waves 16 or 32 of the
+//                 columns with its part of S in accumulators; W is formed once and
 //                 shared in LDS, the last wave making the gates a chunk ahead.  For calls with
 //                 enough chains to fill the card.  16 x 8192 tokens of 32 heads (128 x 128,
 //                 bf16): 958 us, 3.66 TB/s (a large copy: 4.95 TB/s, 708 us for these
@@ -25,7 +25,7 @@
 //                 form Y, each a quarter of the chunk's tokens, four advance S, each a quarter
 //                 of its rows, and four stage; S passes between them in LDS, by chunk parity,
 //                 so one barrier per chunk is enough.  One prompt of 8192 tokens: 146 us, of
-//                 them 19 for W; a chunk takes 1.0 us against 5.3 us in whole heads.
+//                 them 19 for W; a chunk takes 1.0 us against 3.6 us in whole heads.
 //                 Bound by the 40 KB that each strip takes in per chunk, of which B and C are
 //                 32: with 16 compute units reading the same lines at once about 20 B a cycle
 //                 arrive at each.  Forming W in the strips took 188 us, B and C copied into
@@ -455,7 +455,7 @@ struct HeadSmem {
 };
 
 template <typename T, int DK, int DV, int CT>
-__global__ __launch_bounds__(4 * DV / CT, sizeof(T) == 2 ? DV / CT / 32 : 1) void ssm_head_kernel(SsmArgs a) {
+__global__ __launch_bounds__(4 * DV / CT, sizeof(T) == 2 ? 2 : 1) void ssm_head_kernel(SsmArgs a) {
     typedef typename Ops<T>::Half Half;
     typedef HeadSmem<T, DK, DV> SM;
     constexpr int NW = DV / (16 * CT), TH = 64 * NW, NT = DK / 16, TT = kC / 16, TERMS = Ops<T>::kTerms;
@@ -546,11 +546,17 @@ __global__ __launch_bounds__(4 * DV / CT, sizeof(T) == 2 ? DV / CT / 32 : 1) voi
             const f32x4 s = score_tile<T, DK>(sm.b, SM::BP, jt, lane, [&](int p, Half& h0, Half& h1) { pair_of<T, DK>(cb, p, lane, h0, h1); });
             *reinterpret_cast<Half*>(sm.w + blk * 256 + lane * 4) = decayed<T>(g, s, it, jt, lane);
         };
-        static_assert(NW == 4, "ten tiles: three to each wave, one to the last, which makes the gates");
-        form(wv < 3 ? wv : 9);
-        if (wv < 3) {
-            form(wv + 3);
-            form(wv + 6);
+        // ten tiles: the last wave, which makes the gates, forms one of them or none
+        static_assert(NW == 4 || NW == 8, "");
+        if constexpr (NW == 4) {
+            form(wv < 3 ? wv : 9);
+            if (wv < 3) {
+                form(wv + 3);
+                form(wv + 6);
+            }
+        } else {
+            if (wv < 7) form(wv);
+            if (wv < 3) form(wv + 7);
         }
         __builtin_amdgcn_sched_barrier(0);
         // Y^T = S^T C^T, then the rows' e^G
@@ -1042,22 +1048,35 @@ hipError_t decode_typed(const SsmArgs& a, hipStream_t stream) {
 }
 
 // Strips for calls with few chains.  A compute unit takes one strip at a time, in about 1.1 us a
-// chunk and 10 us for the launches; a whole head takes 5.3 us a chunk (bf16, 128 x 128), however
-// many compute units have one.  So strips pay for up to four rounds of them, the more rounds the
-// longer the sequences have to be (us, heads / strips: one round of 64 tokens 15 / 17, of 256
-// 27 / 19, of 4096 342 / 76; two of 256 28 / 22, of 4096 347 / 145; four of 256 30 / 36, of 1024
-// 92 / 83; eight of 4096 357 / 615).
-bool in_strips(int H_v, int d_v, int num_seqs, int64_t total_tokens) {
+// chunk (bf16, 128 x 128) behind two launches; a whole head takes 3.6 us a chunk, however many
+// compute units have one.  So strips pay for few rounds of them over the card, the more rounds
+// the longer the sequences have to be.  Measured (us, heads / strips, equal sequences), bf16 of
+// 128 x 128: one round of 128 tokens 13 / 16, of 320 24 / 17, of 4096 237 / 76; two of 320 25 / 26,
+// of 512 36 / 30; three of 832 54 / 57, of 4096 246 / 222, and of 64 x 64 156 / 197.  fp32: one round
+// of 128 30 / 17; two of 128 32 / 25, of 64 x 64 17 / 19; three of 512 106 / 72 and 52 / 50; four of
+// 1600 323 / 263 and 154 / 185.  What counts is the longest sequence; lengths spread evenly from
+// nothing up make it 2 n / (n + 1) times the mean of n.
+bool in_strips(int H_v, int d_v, int dtype, int num_seqs, int64_t total_tokens) {
     const int64_t strips = (int64_t)num_seqs * H_v * (d_v / kStrip), cus = device_cus(), rounds = (strips + cus - 1) / cus;
-    return rounds <= 4 && total_tokens >= 64 * (rounds * rounds + 1) * num_seqs;
+    if (rounds > (dtype == 1 ? 2 : 3)) return false;
+    const int64_t chunks = dtype == 1 ? 3 * rounds + 1 : (int64_t)1 << rounds;
+    return 2 * total_tokens >= chunks * kC * (num_seqs + 1);
 }
 
 template <typename T, int DK, int DV>
 hipError_t prefill_typed(const SsmArgs& a, hipStream_t stream) {
-    constexpr int CT = DV / 64;
     const int64_t chains = (int64_t)a.num_seqs * a.H_v;
-    if (!in_strips(a.H_v, DV, a.num_seqs, a.total_tokens)) {
-        hipLaunchKernelGGL((ssm_head_kernel<T, DK, DV, CT>), dim3((unsigned)chains), dim3(4 * DV / CT), 0, stream, a);
+    if (!in_strips(a.H_v, DV, a.dtype, a.num_seqs, a.total_tokens)) {
+        // Eight waves of 16 columns where a compute unit has one head at a time anyway (bf16 with no
+        // more heads than compute units; fp32, by its LDS), four of 32 where two heads share one
+        // (us, eight / four, 1024 tokens of 32 heads of 128 x 128: bf16 8 sequences 80 / 87, 12
+        // sequences 138 / 118; fp32 217 / 252 and 419 / 485).
+        if constexpr (DV == 128 && sizeof(T) == 2)
+            if (chains > device_cus()) {
+                hipLaunchKernelGGL((ssm_head_kernel<T, DK, DV, 2>), dim3((unsigned)chains), dim3(256), 0, stream, a);
+                return hipGetLastError();
+            }
+        hipLaunchKernelGGL((ssm_head_kernel<T, DK, DV, 1>), dim3((unsigned)chains), dim3(4 * DV), 0, stream, a);
         return hipGetLastError();
     }
     const int R = a.H_v / a.H_k;
@@ -1089,7 +1108,7 @@ hipError_t decode_dims(const SsmArgs& a, hipStream_t stream) {
 }  // namespace
 
 size_t ssm_workspace_bytes(int H_v, int, int d_v, int dtype, int num_seqs, int64_t total_tokens) {
-    if (!in_strips(H_v, d_v, num_seqs, total_tokens)) return 0;
+    if (!in_strips(H_v, d_v, dtype, num_seqs, total_tokens)) return 0;
     return (size_t)record_count(num_seqs, total_tokens) * (size_t)H_v * (dtype == 1 ? sizeof(Weights<__bf16>) : sizeof(Weights<float>));
 }
 
