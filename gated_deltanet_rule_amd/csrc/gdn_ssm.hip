@@ -40,7 +40,8 @@
 // the state keeps fp32 accuracy; W and the S that multiplies C are rounded once to bf16 (each
 // by at most 2^-8 relative to its own product, on a y that is rounded to bf16 itself).  fp32: fp32
 // matrix products, nothing rounded below fp32.  G is summed in 64 bits and kept as a pair, as
-// its differences are what counts.
+// its differences are what counts: behind one large step a single fp32 G is off by more than
+// the small steps that follow it.
 // A non-finite x must not reach earlier tokens through the zeros of W: a chunk that holds one
 // takes it out of the product and sets its column to NaN from its token on.
 //
@@ -220,12 +221,17 @@ __device__ __forceinline__ double wave_sum64(double x) {
     return x;
 }
 
+// Smallest exponent (to base 2) that a token's decay is taken to have: 2^-2^20 is 0 in any sum,
+// and 64 of them keep G, and so all differences of it, exact to 2^-26 in 64 bits.
+constexpr double kLeast = -1048576.0;
+
 // One wave, lane l for the chunk's token l of n.
 __device__ __forceinline__ void make_gates(Gates& g, float dt, float bias, float A, int softplus, int n, int lane) {
     const float raw = dt + bias;
     float d = softplus ? dev::softplus(raw) : raw;
     if (lane >= n) d = 0.f;
-    const double G = wave_sum64((double)d * (double)A * 1.4426950408889634074);
+    const double own = (double)d * (double)A * 1.4426950408889634074;
+    const double G = wave_sum64(own < kLeast ? kLeast : own);      // (NaN stays)
     const u32x2 w = __builtin_bit_cast(u32x2, G);
     const double last = __builtin_bit_cast(double, u32x2{(unsigned)__builtin_amdgcn_readlane((int)w[0], kC - 1),
                                                          (unsigned)__builtin_amdgcn_readlane((int)w[1], kC - 1)});
@@ -241,17 +247,11 @@ __device__ __forceinline__ void make_gates(Gates& g, float dt, float bias, float
 template <typename T>
 __device__ __forceinline__ typename Ops<T>::Half decayed(const Gates& g, f32x4 sc, int it, int jt, int lane) {
     const int i = 16 * it + (lane & 15), j0 = 16 * jt + 4 * (lane >> 4);
-    const f32x4 hi = *reinterpret_cast<const f32x4*>(g.hi + j0), d = *reinterpret_cast<const f32x4*>(g.d + j0);
-    const float gi = g.hi[i];
+    const f32x4 hi = *reinterpret_cast<const f32x4*>(g.hi + j0), lo = *reinterpret_cast<const f32x4*>(g.lo + j0), d = *reinterpret_cast<const f32x4*>(g.d + j0);
+    const float gi = g.hi[i], gl = g.lo[i];
     f32x4 diff;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) diff[e] = gi - hi[e];
-    if constexpr (sizeof(T) == 4) {      // beside bf16's rounding the low parts do not count
-        const f32x4 lo = *reinterpret_cast<const f32x4*>(g.lo + j0);
-        const float gl = g.lo[i];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) diff[e] += gl - lo[e];
-    }
+    for (int e = 0; e < 4; ++e) diff[e] = (gi - hi[e]) + (gl - lo[e]);
     f32x4 w;
 #pragma unroll
     for (int e = 0; e < 4; ++e) w[e] = j0 + e <= i ? sc[e] * (__builtin_amdgcn_exp2f(diff[e]) * d[e]) : 0.f;
