@@ -300,6 +300,11 @@ size_t gdn_ssm_chunk_prefill_workspace_size(const gdn_shape* shape, int32_t num_
     return gdn::ssm_workspace_bytes(shape->num_v_heads, shape->d_k, shape->d_v, shape->dtype, num_seqs, total_tokens);
 }
 
+size_t gdn_ssm_chunk_prefill_workspace_bound(const gdn_shape* shape, int32_t max_seqs, int64_t max_tokens) {
+    if (gdn::check_shape(shape) != GDN_OK || max_seqs < 0 || max_tokens < 0) return 0;
+    return gdn::ssm_workspace_bound(shape->num_v_heads, shape->d_v, shape->dtype, max_seqs, max_tokens);
+}
+
 gdn_status gdn_ssm_chunk_prefill(const gdn_shape* shape, const gdn_ssm_params* params, int32_t num_seqs,
                                  int64_t total_tokens, const int32_t* cu_seqlens, const void* c, const void* b,
                                  const void* x, const float* dt, void* y, float* state_pool, int32_t num_slots,

@@ -81,6 +81,7 @@ struct SsmArgs {
     void* workspace;
 };
 size_t ssm_workspace_bytes(int H_v, int d_k, int d_v, int dtype, int num_seqs, int64_t total_tokens);
+size_t ssm_workspace_bound(int H_v, int d_v, int dtype, int max_seqs, int64_t max_tokens);
 hipError_t launch_ssm_prefill(const SsmArgs& a, hipStream_t stream);
 hipError_t launch_ssm_decode(const SsmArgs& a, hipStream_t stream);
 

@@ -1056,9 +1056,10 @@ hipError_t decode_typed(const SsmArgs& a, hipStream_t stream) {
 // of 128 30 / 17; two of 128 32 / 25, of 64 x 64 17 / 19; three of 512 106 / 72 and 52 / 50; four of
 // 1600 323 / 263 and 154 / 185.  What counts is the longest sequence; lengths spread evenly from
 // nothing up make it 2 n / (n + 1) times the mean of n.
+constexpr int kMaxRounds = 3;
 bool in_strips(int H_v, int d_v, int dtype, int num_seqs, int64_t total_tokens) {
     const int64_t strips = (int64_t)num_seqs * H_v * (d_v / kStrip), cus = device_cus(), rounds = (strips + cus - 1) / cus;
-    if (rounds > (dtype == 1 ? 2 : 3)) return false;
+    if (strips == 0 || rounds > (dtype == 1 ? 2 : kMaxRounds)) return false;
     const int64_t chunks = dtype == 1 ? 3 * rounds + 1 : (int64_t)1 << rounds;
     return 2 * total_tokens >= chunks * kC * (num_seqs + 1);
 }
@@ -1110,6 +1111,16 @@ hipError_t decode_dims(const SsmArgs& a, hipStream_t stream) {
 size_t ssm_workspace_bytes(int H_v, int, int d_v, int dtype, int num_seqs, int64_t total_tokens) {
     if (!in_strips(H_v, d_v, dtype, num_seqs, total_tokens)) return 0;
     return (size_t)record_count(num_seqs, total_tokens) * (size_t)H_v * (dtype == 1 ? sizeof(Weights<__bf16>) : sizeof(Weights<float>));
+}
+
+// Strips that pay for some tokens pay for more, and records grow with both counts: the most is
+// at all the tokens and the largest count of sequences that still takes strips.
+size_t ssm_workspace_bound(int H_v, int d_v, int dtype, int max_seqs, int64_t max_tokens) {
+    const int64_t cus = device_cus(), per_seq = (int64_t)H_v * (d_v / kStrip);
+    int64_t n = kMaxRounds * cus / per_seq;
+    for (n = n < max_seqs ? n : max_seqs; n > 0; --n)
+        if (in_strips(H_v, d_v, dtype, (int)n, max_tokens)) return ssm_workspace_bytes(H_v, 0, d_v, dtype, (int)n, max_tokens);
+    return 0;
 }
 
 hipError_t launch_ssm_decode(const SsmArgs& a, hipStream_t stream) {

@@ -44,6 +44,7 @@ SIGNATURES = {
                                 + [_vp] * 3 + [_i64, _vp]),
     "gdn_causal_conv_decode": (ctypes.c_int, [_conv, _i32, _vp, _i64] + [_vp] * 6 + [_i32] + [_vp] * 3),
     "gdn_ssm_chunk_prefill_workspace_size": (_sz, [_shape, _i32, _i64]),
+    "gdn_ssm_chunk_prefill_workspace_bound": (_sz, [_shape, _i32, _i64]),
     "gdn_ssm_chunk_prefill": (ctypes.c_int, [_shape, _ssm, _i32, _i64] + [_vp] * 7 + [_i32, _vp, _vp, _vp, _i32]
                               + [_vp] * 3 + [_i64, _vp, _sz, _vp]),
     "gdn_ssm_recurrent_decode": (ctypes.c_int, [_shape, _ssm, _i32] + [_vp] * 6 + [_i32] + [_vp] * 3),
@@ -290,11 +291,14 @@ def _ssm_common(c, b, x, dt, A, y, state_pool, dt_bias, D, dt_softplus, scale):
         _dense(state_pool, "state_pool", f32, dev, slots, heads, d_k, d_v), slots), (heads, d_k, d_v)
 
 
-def alloc_ssm_workspace(c, x, num_seqs: int) -> Optional[torch.Tensor]:
+def alloc_ssm_workspace(c, x, num_seqs: int, *, smaller_calls: bool = False) -> Optional[torch.Tensor]:
     """A uint8 device buffer of the size gdn_ssm_chunk_prefill needs for these inputs and
-    num_seqs sequences, or None when it needs none."""
+    num_seqs sequences, or None when it needs none.  With smaller_calls it serves every call
+    with at most as many sequences and tokens too (which may need more than this one)."""
     shape = GdnShape(c.shape[1], x.shape[1], c.shape[2], x.shape[2], _code(x, "x"), 1.0)
-    n = int(library().gdn_ssm_chunk_prefill_workspace_size(shape, int(num_seqs), x.shape[0]))
+    query = library().gdn_ssm_chunk_prefill_workspace_bound if smaller_calls else library().gdn_ssm_chunk_prefill_workspace_size
+    with torch.cuda.device(_device(x, "x")):
+        n = int(query(shape, int(num_seqs), x.shape[0]))
     return torch.empty(n, dtype=torch.uint8, device=x.device) if n else None
 
 

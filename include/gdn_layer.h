@@ -145,9 +145,16 @@ typedef struct {
     int32_t dt_softplus;
 } gdn_ssm_params;
 
-/* Bytes of device workspace gdn_ssm_chunk_prefill needs (0 for an unsupported shape). */
+/* Bytes of device workspace gdn_ssm_chunk_prefill needs (0 for an unsupported shape) on the
+ * current device, for exactly this many sequences and tokens: a call with fewer may need
+ * more, since calls with few sequences take another launch than calls with many. */
 size_t gdn_ssm_chunk_prefill_workspace_size(const gdn_shape* shape, int32_t num_seqs,
                                             int64_t total_tokens);
+
+/* The most that any call with at most max_seqs sequences and max_tokens tokens needs: the
+ * size of a workspace that is allocated once for steps of all sizes. */
+size_t gdn_ssm_chunk_prefill_workspace_bound(const gdn_shape* shape, int32_t max_seqs,
+                                             int64_t max_tokens);
 
 /*
  * Selective state space scan of packed sequences.  Per value head, with step d and state
@@ -162,7 +169,7 @@ size_t gdn_ssm_chunk_prefill_workspace_size(const gdn_shape* shape, int32_t num_
  *   state_pool device [num_slots, num_v_heads, d_k, d_v] fp32
  *   the remaining arguments, the zero-length sequences and the split of a prompt across
  *   calls are gdn_chunk_prefill's.  workspace is 256-byte aligned and holds
- *   gdn_ssm_chunk_prefill_workspace_size() bytes (NULL when that is 0).
+ *   at least gdn_ssm_chunk_prefill_workspace_size() bytes (may be NULL when that is 0).
  */
 gdn_status gdn_ssm_chunk_prefill(const gdn_shape* shape, const gdn_ssm_params* params,
                                  int32_t num_seqs, int64_t total_tokens, const int32_t* cu_seqlens,
