@@ -269,6 +269,7 @@ template <typename T, int W>
 hipError_t launch_typed(const ConvArgs& a, hipStream_t stream) {
     const unsigned p = (unsigned)pieces<T>(a), py = (p + kWaves - 1) / kWaves;
     if (!a.cu_seqlens) {
+        if (!grid_fits(a.total_tokens, kThreads)) return hipErrorInvalidConfiguration;
         hipLaunchKernelGGL((conv_decode_kernel<T, W>), dim3((unsigned)a.total_tokens, py), dim3(kThreads), 0, stream, a);
         return hipGetLastError();
     }
@@ -276,6 +277,7 @@ hipError_t launch_typed(const ConvArgs& a, hipStream_t stream) {
     int tile = kTile;
     while (tile > kGroup && (a.total_tokens + tile - 1) / tile * p < 8 * (int64_t)device_cus()) tile /= 2;
     const int64_t tiles = (a.total_tokens + tile - 1) / tile;
+    if (!grid_fits(tiles, kThreads)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((conv_prefill_kernel<T, W>), dim3((unsigned)(tiles < 1 ? 1 : tiles), py), dim3(kThreads), 0, stream, a, tile);
     return hipGetLastError();
 }

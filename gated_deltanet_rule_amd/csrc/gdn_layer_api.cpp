@@ -19,6 +19,12 @@ using gdn::hip_status;
 constexpr int64_t kMaxTokens = 0x7fffffffLL - 2 * GDN_CHUNK;
 constexpr int kMaxDim = 16384;
 
+// A launcher's result: a call too large for one launch is the caller's to split.
+gdn_status launched(hipError_t e, const char* what) {
+    if (e == hipErrorInvalidConfiguration) return fail(GDN_ERR_UNSUPPORTED, "%s exceeds the launch grid of 2^32 - 1 threads", what);
+    return hip_status(e, what);
+}
+
 size_t elem(int32_t dtype) { return dtype == GDN_BF16 ? 2 : 4; }
 
 gdn_status check_dtype(int32_t dtype, const char* name) {
@@ -170,7 +176,7 @@ gdn_status check_norm(int64_t num_rows, int64_t groups, int32_t dim, int32_t dty
     if (groups <= 0) return fail(GDN_ERR_INVALID_ARGUMENT, "num_groups %lld is not positive", (long long)groups);
     if (dim <= 0) return fail(GDN_ERR_INVALID_ARGUMENT, "dim %d is not positive", dim);
     if (dim > kMaxDim) return fail(GDN_ERR_UNSUPPORTED, "dim %d exceeds %d", dim, kMaxDim);
-    if (num_rows > 0x7fffffffLL / groups)
+    if (num_rows > 0x7fffffffLL / groups)      // (the launchers know how many threads a norm takes)
         return fail(GDN_ERR_UNSUPPORTED, "num_rows %lld x num_groups %lld exceeds the launch grid", (long long)num_rows, (long long)groups);
     if (activation != GDN_ACT_NONE && activation != GDN_ACT_SILU && activation != GDN_ACT_SIGMOID)
         return fail(GDN_ERR_UNSUPPORTED, "activation %d: must be 0 (none), 1 (SiLU) or 2 (sigmoid)", activation);
@@ -235,7 +241,7 @@ gdn_status gdn_step_plan(int32_t num_requests, int32_t num_decode_rows, const in
                        run_slot, kv_table, kv_table_width, kv_block, token_capacity, export_capacity, slot_in, slot_out,
                        cu_seqlens, start_pos, init_slot, final_slot, export_offsets, export_slots, token_request,
                        token_position, token_kv_slot};
-    return hip_status(gdn::launch_plan(a, stream), "step plan launch");
+    return launched(gdn::launch_plan(a, stream), "step plan launch");
 }
 
 gdn_status gdn_causal_conv_prefill(const gdn_conv_shape* shape, int32_t num_seqs, int64_t total_tokens,
@@ -269,7 +275,7 @@ gdn_status gdn_causal_conv_prefill(const gdn_conv_shape* shape, int32_t num_seqs
     a.export_states = export_grid > 0 && !export_slots ? export_states : nullptr;
     a.export_offsets = export_grid > 0 ? export_offsets : nullptr;
     a.export_capacity = export_grid > 0 && (a.export_states || a.export_slots) ? num_export_states : 0;
-    return hip_status(gdn::launch_conv(a, stream), "convolution launch");
+    return launched(gdn::launch_conv(a, stream), "convolution launch");
 }
 
 gdn_status gdn_causal_conv_decode(const gdn_conv_shape* shape, int32_t num_rows, const void* x, int64_t x_stride,
@@ -292,7 +298,7 @@ gdn_status gdn_causal_conv_decode(const gdn_conv_shape* shape, int32_t num_rows,
     a.total_tokens = num_rows;
     a.init_slot = slot_in;
     a.final_slot = slot_out;
-    return hip_status(gdn::launch_conv(a, stream), "convolution decode launch");
+    return launched(gdn::launch_conv(a, stream), "convolution decode launch");
 }
 
 size_t gdn_ssm_chunk_prefill_workspace_size(const gdn_shape* shape, int32_t num_seqs, int64_t total_tokens) {
@@ -347,7 +353,7 @@ gdn_status gdn_ssm_chunk_prefill(const gdn_shape* shape, const gdn_ssm_params* p
     a.export_offsets = export_grid > 0 ? export_offsets : nullptr;
     a.export_capacity = export_grid > 0 && (a.export_states || a.export_slots) ? num_export_states : 0;
     a.workspace = workspace;
-    return hip_status(gdn::launch_ssm_prefill(a, stream), "scan launch");
+    return launched(gdn::launch_ssm_prefill(a, stream), "scan launch");
 }
 
 gdn_status gdn_ssm_recurrent_decode(const gdn_shape* shape, const gdn_ssm_params* params, int32_t num_rows,
@@ -370,7 +376,7 @@ gdn_status gdn_ssm_recurrent_decode(const gdn_shape* shape, const gdn_ssm_params
     a.total_tokens = num_rows;
     a.init_slot = slot_in;
     a.final_slot = slot_out;
-    return hip_status(gdn::launch_ssm_decode(a, stream), "scan decode launch");
+    return launched(gdn::launch_ssm_decode(a, stream), "scan decode launch");
 }
 
 gdn_status gdn_gated_norm(int64_t num_rows, int32_t num_groups, int32_t dim, int32_t dtype, const void* x,
@@ -389,7 +395,7 @@ gdn_status gdn_gated_norm(int64_t num_rows, int32_t num_groups, int32_t dim, int
     if (st != GDN_OK) return st;
     gdn::GatedNormArgs a = {num_rows, num_groups, dim, dtype, x, x_stride, z, z_stride, weight, weight_per_group != 0,
                             eps, gate_first != 0, activation, y};
-    return hip_status(gdn::launch_gated_norm(a, stream), "gated norm launch");
+    return launched(gdn::launch_gated_norm(a, stream), "gated norm launch");
 }
 
 gdn_status gdn_residual_norm(int64_t num_rows, int32_t dim, int32_t dtype, int32_t residual_dtype, const void* x,
@@ -416,7 +422,7 @@ gdn_status gdn_residual_norm(int64_t num_rows, int32_t dim, int32_t dtype, int32
     if (st != GDN_OK) return st;
     gdn::ResidualNormArgs a = {num_rows, dim, dtype, residual_dtype, x, x_stride, post_weight, gate, gate_stride, activation,
                                residual_scale, residual, residual_out, pre_weight, eps, y};
-    return hip_status(gdn::launch_residual_norm(a, stream), "residual norm launch");
+    return launched(gdn::launch_residual_norm(a, stream), "residual norm launch");
 }
 
 }  // extern "C"

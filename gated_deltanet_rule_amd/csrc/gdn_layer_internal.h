@@ -9,6 +9,11 @@
 
 namespace gdn {
 
+// Whether a launch may have this many workgroups (of at most 2^32 - 1 threads in all).  The
+// launchers return hipErrorInvalidConfiguration for calls that do not fit, before they enqueue
+// anything.
+inline bool grid_fits(int64_t blocks, int threads) { return blocks <= 0xffffffffLL / threads; }
+
 struct PlanArgs {
     int num_requests, num_decode_rows;
     const int32_t* computed;

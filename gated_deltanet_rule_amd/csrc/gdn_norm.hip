@@ -262,43 +262,47 @@ __global__ __launch_bounds__(TPG > kThreads ? TPG : kThreads) void residual_norm
 }
 
 template <typename T, bool WIDE, int TPG, int R>
-void gated(const GatedNormArgs& a, hipStream_t stream) {
+hipError_t gated(const GatedNormArgs& a, hipStream_t stream) {
     constexpr int PER = TPG > kThreads ? 1 : kThreads / TPG, THREADS = TPG > kThreads ? TPG : kThreads;
     const int64_t n = (a.num_rows * a.groups + PER - 1) / PER;
+    if (!grid_fits(n, THREADS)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((gated_norm_kernel<T, WIDE, TPG, R, 1>), dim3((unsigned)n), dim3(THREADS), 0, stream, a);
+    return hipGetLastError();
 }
 
 // Threads and vectors by the number of vectors in a norm: the smallest that holds it.
 template <typename T, bool WIDE>
-void gated_by_dim(const GatedNormArgs& a, hipStream_t stream) {
+hipError_t gated_by_dim(const GatedNormArgs& a, hipStream_t stream) {
     constexpr int V = dev::kVec<T>;
     const int n = (a.dim + V - 1) / V;
-    if (n <= 1) gated<T, WIDE, 1, 1>(a, stream);
-    else if (n <= 16) gated<T, WIDE, 16, 1>(a, stream);
-    else if (n <= 64) gated<T, WIDE, 64, 1>(a, stream);
-    else if (n <= 256) gated<T, WIDE, 64, 4>(a, stream);
-    else if (n <= 1024) gated<T, WIDE, 256, 4>(a, stream);
-    else gated<T, WIDE, 1024, 4>(a, stream);
+    if (n <= 1) return gated<T, WIDE, 1, 1>(a, stream);
+    if (n <= 16) return gated<T, WIDE, 16, 1>(a, stream);
+    if (n <= 64) return gated<T, WIDE, 64, 1>(a, stream);
+    if (n <= 256) return gated<T, WIDE, 64, 4>(a, stream);
+    if (n <= 1024) return gated<T, WIDE, 256, 4>(a, stream);
+    return gated<T, WIDE, 1024, 4>(a, stream);
 }
 
 template <typename T, typename RT, bool WIDE, int TPG, int R>
-void residual(const ResidualNormArgs& a, hipStream_t stream) {
+hipError_t residual(const ResidualNormArgs& a, hipStream_t stream) {
     constexpr int PER = TPG > kThreads ? 1 : kThreads / TPG, THREADS = TPG > kThreads ? TPG : kThreads;
     const int64_t n = (a.num_rows + PER - 1) / PER;
+    if (!grid_fits(n, THREADS)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((residual_norm_kernel<T, RT, WIDE, TPG, R>), dim3((unsigned)n), dim3(THREADS), 0, stream, a);
+    return hipGetLastError();
 }
 
 template <typename T, typename RT, bool WIDE>
-void residual_by_dim(const ResidualNormArgs& a, hipStream_t stream) {
+hipError_t residual_by_dim(const ResidualNormArgs& a, hipStream_t stream) {
     constexpr int V = dev::kVec<T>;
     const int n = (a.dim + V - 1) / V;
-    if (n <= 1) residual<T, RT, WIDE, 1, 1>(a, stream);
-    else if (n <= 16) residual<T, RT, WIDE, 16, 1>(a, stream);
-    else if (n <= 64) residual<T, RT, WIDE, 64, 1>(a, stream);
-    else if (n <= 256) residual<T, RT, WIDE, 256, 1>(a, stream);
-    else if (n <= 512) residual<T, RT, WIDE, 256, 2>(a, stream);
-    else if (n <= 1024) residual<T, RT, WIDE, 256, 4>(a, stream);
-    else residual<T, RT, WIDE, 1024, 4>(a, stream);
+    if (n <= 1) return residual<T, RT, WIDE, 1, 1>(a, stream);
+    if (n <= 16) return residual<T, RT, WIDE, 16, 1>(a, stream);
+    if (n <= 64) return residual<T, RT, WIDE, 64, 1>(a, stream);
+    if (n <= 256) return residual<T, RT, WIDE, 256, 1>(a, stream);
+    if (n <= 512) return residual<T, RT, WIDE, 256, 2>(a, stream);
+    if (n <= 1024) return residual<T, RT, WIDE, 256, 4>(a, stream);
+    return residual<T, RT, WIDE, 1024, 4>(a, stream);
 }
 
 // Whether rows of `dim` elements at this address and row stride are whole, aligned 16-byte vectors.
@@ -308,36 +312,30 @@ bool wide(const void* p, int64_t stride, int64_t rows, int dim, size_t size) {
 }
 
 template <typename T, typename RT>
-void residual_typed(const ResidualNormArgs& a, hipStream_t stream) {
+hipError_t residual_typed(const ResidualNormArgs& a, hipStream_t stream) {
     const bool ok = wide(a.x, a.x_stride, a.num_rows, a.dim, sizeof(T)) && wide(a.residual, a.dim, 1, a.dim, sizeof(T)) &&
                     wide(a.residual_out, a.dim, 1, a.dim, sizeof(T)) && (!a.y || wide(a.y, a.dim, 1, a.dim, sizeof(T))) &&
                     (!a.gate || wide(a.gate, a.gate_stride, a.num_rows, a.dim, sizeof(T))) &&
                     reinterpret_cast<uintptr_t>(a.post_weight) % 16 == 0 && reinterpret_cast<uintptr_t>(a.pre_weight) % 16 == 0;
-    if (ok) residual_by_dim<T, RT, true>(a, stream);
-    else residual_by_dim<T, RT, false>(a, stream);
+    return ok ? residual_by_dim<T, RT, true>(a, stream) : residual_by_dim<T, RT, false>(a, stream);
 }
 
 template <typename T>
-void gated_typed(const GatedNormArgs& a, hipStream_t stream) {
+hipError_t gated_typed(const GatedNormArgs& a, hipStream_t stream) {
     const bool ok = wide(a.x, a.x_stride, a.num_rows, a.dim, sizeof(T)) && wide(a.y, a.dim, 1, a.dim, sizeof(T)) &&
                     (!a.z || wide(a.z, a.z_stride, a.num_rows, a.dim, sizeof(T))) && reinterpret_cast<uintptr_t>(a.weight) % 16 == 0;
-    if (ok) gated_by_dim<T, true>(a, stream);
-    else gated_by_dim<T, false>(a, stream);
+    return ok ? gated_by_dim<T, true>(a, stream) : gated_by_dim<T, false>(a, stream);
 }
 
 }  // namespace
 
 hipError_t launch_gated_norm(const GatedNormArgs& a, hipStream_t stream) {
-    if (a.dtype == 1) gated_typed<__bf16>(a, stream);
-    else gated_typed<float>(a, stream);
-    return hipGetLastError();
+    return a.dtype == 1 ? gated_typed<__bf16>(a, stream) : gated_typed<float>(a, stream);
 }
 
 hipError_t launch_residual_norm(const ResidualNormArgs& a, hipStream_t stream) {
-    if (a.dtype == 0) residual_typed<float, float>(a, stream);
-    else if (a.residual_dtype == 0) residual_typed<__bf16, float>(a, stream);
-    else residual_typed<__bf16, __bf16>(a, stream);
-    return hipGetLastError();
+    if (a.dtype == 0) return residual_typed<float, float>(a, stream);
+    return a.residual_dtype == 0 ? residual_typed<__bf16, float>(a, stream) : residual_typed<__bf16, __bf16>(a, stream);
 }
 
 }  // namespace gdn

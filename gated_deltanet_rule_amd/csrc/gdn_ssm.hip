@@ -1042,8 +1042,9 @@ __global__ __launch_bounds__(kThreads) void ssm_decode_kernel(SsmArgs a) {
 
 template <typename T, int DK, int DV>
 hipError_t decode_typed(const SsmArgs& a, hipStream_t stream) {
-    const unsigned blocks = (unsigned)a.num_seqs * (unsigned)a.H_v * (unsigned)(DV / kCols);
-    hipLaunchKernelGGL((ssm_decode_kernel<T, DK, DV>), dim3(blocks), dim3(kThreads), 0, stream, a);
+    const int64_t blocks = (int64_t)a.num_seqs * a.H_v * (DV / kCols);
+    if (!grid_fits(blocks, kThreads)) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL((ssm_decode_kernel<T, DK, DV>), dim3((unsigned)blocks), dim3(kThreads), 0, stream, a);
     return hipGetLastError();
 }
 
@@ -1068,6 +1069,7 @@ template <typename T, int DK, int DV>
 hipError_t prefill_typed(const SsmArgs& a, hipStream_t stream) {
     const int64_t chains = (int64_t)a.num_seqs * a.H_v;
     if (!in_strips(a.H_v, DV, a.dtype, a.num_seqs, a.total_tokens)) {
+        if (!grid_fits(chains, 4 * DV)) return hipErrorInvalidConfiguration;
         // Eight waves of 16 columns where a compute unit has one head at a time anyway (bf16 with no
         // more heads than compute units; fp32, by its LDS), four of 32 where two heads share one
         // (us, eight / four, 1024 tokens of 32 heads of 128 x 128: bf16 8 sequences 80 / 87, 12
@@ -1082,7 +1084,7 @@ hipError_t prefill_typed(const SsmArgs& a, hipStream_t stream) {
     }
     const int R = a.H_v / a.H_k;
     const int64_t blocks = record_count(a.num_seqs, a.total_tokens) * a.H_k * ((R + kHeadBatch - 1) / kHeadBatch);
-    if (blocks > 0x7fffffffLL) return hipErrorInvalidConfiguration;
+    if (!grid_fits(blocks, 256)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((ssm_weights_kernel<T, DK>), dim3((unsigned)blocks), dim3(256), 0, stream, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
