@@ -261,8 +261,6 @@ gdn_status gdn_causal_conv_prefill(const gdn_conv_shape* shape, int32_t num_seqs
         st = check_conv_tensors(shape, x, x_stride, weight, bias, y);
         if (st != GDN_OK) return st;
     }
-    if (num_seqs + num_export_states > 0x7fffffffLL)
-        return fail(GDN_ERR_UNSUPPORTED, "num_seqs %d + num_export_states %lld exceeds the launch grid", num_seqs, (long long)num_export_states);
     gdn::ConvArgs a = conv_args(shape, x, x_stride, weight, bias, y0, y1, y2, conv_pool, num_slots);
     a.num_seqs = num_seqs;
     a.total_tokens = total_tokens;

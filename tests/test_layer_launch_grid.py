@@ -30,3 +30,12 @@ def test_refused(name, args, what):
     status = getattr(L.library(), name)(*args)
     message = B.gdn_last_error()
     assert status == B.GDN_ERR_UNSUPPORTED and what in message and "launch grid" in message, (status, message)
+
+
+@pytest.mark.parametrize("count", [1 << 31, 1 << 40, (1 << 63) - 1])
+def test_export_capacity_takes_no_launch(count):
+    """However many exports the caller has room for, they cost no threads: the same call is refused
+    for its tokens alone."""
+    args = A.conv_prefill(shape=ONE, tokens=1 << 29, stride=8, grid=64, eslots=F, count=count)
+    assert L.library().gdn_causal_conv_prefill(*args) == B.GDN_ERR_UNSUPPORTED
+    assert "threads" in B.gdn_last_error(), B.gdn_last_error()
