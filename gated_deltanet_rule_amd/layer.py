@@ -183,7 +183,8 @@ def gdn_step_plan(computed, new_tokens, state_table, run_slot, *, num_decode_row
                   cu_seqlens, start_pos, init_slot, final_slot, export_offsets, export_slots=None, token_request=None,
                   token_position=None, token_kv_slot=None, kv_table=None, kv_block: int = 0, stream=None) -> None:
     """One step's slots, packed offsets, export list and token maps from the requests' lengths
-    and block tables (see include/gdn_layer.h; outputs: alloc_step_plan)."""
+    and block tables (see include/gdn_layer.h; outputs: alloc_step_plan).  A decode row continues
+    a cached state (computed >= 1); a request's first token is planned as a prefill."""
     dev = _device(computed, "computed")
     i32 = torch.int32
     r, b = computed.shape[0], int(num_decode_rows)

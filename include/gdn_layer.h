@@ -49,6 +49,9 @@ typedef enum { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1, GDN_ACT_SIGMOID = 2 } gdn_act
  *               counts as 0).
  *   new_tokens  device [num_requests] int32: tokens of this step.  A decode row takes one
  *               token; with 0 or less it is a padding row.  A prefill may be empty.
+ *               A decode row continues a cached state, so its computed has to be at least 1:
+ *               with 0 its slot_in is -1, which the decode entry points take as padding, and
+ *               its token is lost.  A request's first token is a prefill, of one token or more.
  *   state_table device [num_requests, state_table_width] int32: the cache slot of each
  *               request's state after (j + 1) * state_block tokens, j = 0..; state_block
  *               is a positive multiple of 64 (the prefix-cache block).
