@@ -26,10 +26,19 @@
  *   Strides     Where an argument has a row stride (in elements), its rows may be columns
  *               of a wider matrix (a projection's output); everything else is dense.
  *   Arithmetic  All sums, softplus / SiLU evaluations, norms and states are fp32 or
- *               wider.  A row's or a sequence's results are bitwise the same whatever
- *               shares its call.
+ *               wider.  Two operands of the scan's bf16 prefill are rounded to bf16 on their
+ *               way into the matrix cores: the decayed scores and the copy of the state that
+ *               C is multiplied with, by at most 2^-8 of each product.  The state itself, fp32
+ *               prefills and decode round nothing below fp32.  A row's or a sequence's results
+ *               are bitwise the same whatever shares its call.
  *   Range       No operand is narrowed below its own dtype's range: the scan's bf16 path
  *               feeds the matrix cores bf16 operands, so bf16's range is the only bound.
+ *               Sums of squares are fp32: a head or row whose sum passes fp32's range comes
+ *               out as zeros; under the root (with eps) what is below 2^-126 counts as 2^-126.
+ *   Non-finite  A non-finite input of the scan reaches no earlier token and no other sequence.
+ *               One in x makes its column of y NaN from its token to the chunk's end, and the
+ *               column's state, and so y after that, not finite, also where the recurrence
+ *               would give an infinity of a sign.
  */
 #ifndef GDN_LAYER_H
 #define GDN_LAYER_H
