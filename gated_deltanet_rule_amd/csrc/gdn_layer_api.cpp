@@ -325,8 +325,10 @@ gdn_status gdn_ssm_chunk_prefill(const gdn_shape* shape, const gdn_ssm_params* p
     if ((int64_t)num_seqs * shape->num_v_heads * (shape->d_v / 16) > 0x7fffffffLL)
         return fail(GDN_ERR_UNSUPPORTED, "num_seqs %d x num_v_heads %d exceeds the launch grid", num_seqs, shape->num_v_heads);
     // a chunk's rows are addressed by 31-bit byte offsets
-    if ((int64_t)shape->num_v_heads * shape->d_v > (1 << 22) || (int64_t)shape->num_k_heads * shape->d_k > (1 << 22))
+    if ((int64_t)shape->num_v_heads * shape->d_v > (1 << 22))
         return fail(GDN_ERR_UNSUPPORTED, "rows of num_v_heads %d x d_v %d values exceed the supported 2^22", shape->num_v_heads, shape->d_v);
+    if ((int64_t)shape->num_k_heads * shape->d_k > (1 << 22))
+        return fail(GDN_ERR_UNSUPPORTED, "rows of num_k_heads %d x d_k %d values exceed the supported 2^22", shape->num_k_heads, shape->d_k);
     if (total_tokens > 0) {
         st = check_ptrs({{"c", c, 16}, {"b", b, 16}, {"x", x, 16}, {"dt", dt, 4}, {"y", y, 16}});
         if (st != GDN_OK) return st;

@@ -32,6 +32,13 @@ def test_refused(name, args, what):
     assert status == B.GDN_ERR_UNSUPPORTED and what in message and "launch grid" in message, (status, message)
 
 
+@pytest.mark.parametrize("k_heads,d_k,d_v,needle", [(20000, 128, 128, "num_v_heads 40000 x d_v 128"), (40000, 128, 64, "num_k_heads 40000 x d_k 128")])
+def test_rows_too_wide_name_their_heads(k_heads, d_k, d_v, needle):
+    shape = B.make_shape(k_heads, 40000, d_k, d_v, 1, 1.0)
+    assert L.library().gdn_ssm_chunk_prefill(*A.ssm_prefill(shape=shape, n=1, y=None)) == B.GDN_ERR_UNSUPPORTED
+    assert needle in B.gdn_last_error(), B.gdn_last_error()
+
+
 @pytest.mark.parametrize("count", [1 << 31, 1 << 40, (1 << 63) - 1])
 def test_export_capacity_takes_no_launch(count):
     """However many exports the caller has room for, they cost no threads: the same call is refused
