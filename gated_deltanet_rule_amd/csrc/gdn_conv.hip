@@ -13,7 +13,7 @@
 // no other one reads the old state and a resume in place needs no second launch.
 //
 // 8 prompts of 64 to 4096 tokens, 8192 channels, bf16, states kept every 64 tokens: 149 us,
-// 3.75 TB/s (a large copy: 4.95).  The vector ALU is busy 55 % of that, half of it the SiLU's
+// 3.75 TB/s (a large copy: 6.6).  The vector ALU is busy 55 % of that, half of it the SiLU's
 // two quarter-rate instructions; at the 137 registers of width 4 three waves fit on a SIMD.
 // Measured beside it and no faster: four waves with spills (153 us), tiles of 64 tokens (157)
 // or as long as one round of resident workgroups takes (152), a tile's pieces side by side in

@@ -7,10 +7,12 @@
 // between its sum and its output; TPG threads share one norm, R vectors of V elements each,
 // as many vectors as its dim needs: one lane, 16 lanes (four norms to a wave), one wave,
 // then one workgroup of four or sixteen waves.  A sum is taken per thread in order, then
-// over the lanes and the waves in a fixed tree, so a row's bits depend on its dim alone.  131072 x 32 gated rows of 128 bf16 values: 538 us, 6.0 TB/s; 16384 residual
-// rows of 4096 with an fp32 residual: 173 us, 5.4 TB/s (a large copy: 4.95 TB/s).  Rows of any other dim or alignment take unaligned
-// vectors: 6709 residual rows of 5001 bf16 values 118 us (element by element: 261), 4096 gated
-// rows of 4096 at an odd stride 24 us (96).
+// over the lanes and the waves in a fixed tree, so a row's bits depend on its dim alone.
+// 131072 x 32 gated rows of 128 bf16 values: 554 us, 5.8 TB/s; 16384 residual rows of 4096 with
+// an fp32 residual: 174 us, 5.4 TB/s (a large copy: 6.6 TB/s; two arrays added into a third by
+// torch: 6.05).  Rows of any other dim or alignment take unaligned vectors: 6709 residual rows
+// of 5001 bf16 values 118 us (element by element: 261), 4096 gated rows of 4096 at an odd stride
+// 24 us (96).
 #include <hip/hip_runtime.h>
 
 #include "gdn_layer_device.h"

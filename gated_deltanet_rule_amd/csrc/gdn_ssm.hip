@@ -14,10 +14,12 @@
 //                 columns with its part of S in accumulators; W is formed once and
 //                 shared in LDS, the last wave making the gates a chunk ahead.  For calls with
 //                 enough chains to fill the card.  16 x 8192 tokens of 32 heads (128 x 128,
-//                 bf16): 958 us, 3.66 TB/s (a large copy: 4.95 TB/s, 708 us for these
-//                 bytes).  Bound by issue with two waves on a SIMD: the vector ALU 47 % of the
-//                 time, the matrix cores 33 %, LDS 30 %; four waves on a SIMD (16 columns
-//                 each) cost twice the operand reads and took 1537 us.
+//                 bf16): 981 us, 3.6 TB/s (a large copy: 6.6 TB/s, 534 us for these bytes).
+//                 No unit is full (vector ALU 48 % of the time, matrix cores 33 %, LDS 31 %):
+//                 with two waves on a SIMD their phases' waits show, a quarter of a wave's
+//                 time for memory and barriers, 41 % for the next instruction to issue.  Four
+//                 waves on a SIMD (16 columns each) cost twice the operand reads and took
+//                 1537 us.
 //   strips        one workgroup per (sequence, head, 16 columns), for calls with few chains,
 //                 bound by the length of the longest one.  W and the decays do not depend on
 //                 S: a launch of their own forms them for all chunks side by side, once for
@@ -1055,8 +1057,12 @@ hipError_t decode_typed(const SsmArgs& a, hipStream_t stream) {
 // 128 x 128: one round of 128 tokens 13 / 16, of 320 24 / 17, of 4096 237 / 76; two of 320 25 / 26,
 // of 512 36 / 30; three of 832 54 / 57, of 4096 246 / 222, and of 64 x 64 156 / 197.  fp32: one round
 // of 128 30 / 17; two of 128 32 / 25, of 64 x 64 17 / 19; three of 512 106 / 72 and 52 / 50; four of
-// 1600 323 / 263 and 154 / 185.  What counts is the longest sequence; lengths spread evenly from
-// nothing up make it 2 n / (n + 1) times the mean of n.
+// 1600 323 / 263 and 154 / 185.  What counts is the longest sequence, which the host
+// does not know: lengths spread evenly from nothing up make it 2 n / (n + 1) times the mean of n.
+// Where they are not, the rule is off: every sequence counts for a full set of strips, so a prompt
+// of 8192 tokens (bf16, 32 heads of 128 x 128) that takes 150 us alone takes 265 beside one single
+// token, as its strips share half of the XCDs, and 465 in whole heads beside two.  Nor does it look
+// at d_k and d_v: where 128 x 128 and 64 x 64 above point to different launches, both take heads.
 constexpr int kMaxRounds = 3;
 bool in_strips(int H_v, int d_v, int dtype, int num_seqs, int64_t total_tokens) {
     const int64_t strips = (int64_t)num_seqs * H_v * (d_v / kStrip), cus = device_cus(), rounds = (strips + cus - 1) / cus;
