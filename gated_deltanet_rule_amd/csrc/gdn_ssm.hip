@@ -224,7 +224,7 @@ __device__ __forceinline__ double wave_sum64(double x) {
 }
 
 // Smallest exponent (to base 2) that a token's decay is taken to have: 2^-2^20 is 0 in any sum,
-// and 64 of them keep G, and so all differences of it, exact to 2^-26 in 64 bits.
+// and 64 of them leave G known to 2^-24 (six additions of 64 bits below 2^26), its pair to 2^-22.
 constexpr double kLeast = -1048576.0;
 
 // One wave, lane l for the chunk's token l of n.

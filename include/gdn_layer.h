@@ -21,6 +21,8 @@
  * allocated, work only enqueued on `stream`, no synchronisation, capturable, slots
  * bounds-checked on the device, host arguments validated before anything is enqueued,
  * gdn_last_error() for the message).  Differences and additions:
+ *   Size        A call whose launch would take more than 2^32 - 1 threads (16 million rows of a
+ *               wide norm, 2^29 tokens) returns GDN_ERR_UNSUPPORTED.
  *   Parameters  Weights, biases and every per-head parameter are fp32, whatever the
  *               activations' dtype.
  *   Strides     Where an argument has a row stride (in elements), its rows may be columns
