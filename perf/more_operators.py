@@ -406,8 +406,9 @@ def exact(case, seed):
         v = (x / scale).float().double()
         if fmt == "int8":
             return v.round().clamp(-127, 127) * scale
-        exponent = torch.frexp(v).exponent.clamp(min=-5) - 1               # of 1.xxx, at least that of the smallest normal number
-        step = torch.ldexp(torch.ones_like(v), exponent - 3)
+        # the step of each value's binade, 2^-9 below the smallest normal number 2^-6; from a list, so that powers are exact
+        powers = torch.tensor([2.0 ** i for i in range(-9, 8)], dtype=torch.float64, device=v.device)
+        step = powers[torch.frexp(v).exponent.clamp(-5, 11).long() + 5]
         return ((v / step).round() * step).clamp(-448, 448) * scale
 
     def cache(s):
