@@ -1,0 +1,144 @@
+// gdn_rotary.hip -- rotary positions for gfx950.
+//
+//     (a, b) <- factor (a cos t - b sin t, b cos t + a sin t),   t = p f_i
+//
+// Memory-bound: every value crosses HBM once each way.  A workgroup takes TB tokens: its threads
+// first form the tokens' cosines and sines, one frequency each, into LDS, where all heads
+// share them; then they turn the heads' pairs, V pairs to a thread as two 16-byte vectors.
+#include <hip/hip_runtime.h>
+
+#include "gdn_attention_internal.h"
+#include "gdn_layer_device.h"
+#include "gdn_layer_internal.h"
+#include "gdn_pages.h"
+
+namespace gdn {
+namespace {
+
+constexpr int kThreads = 256;
+
+struct RotaryKernelArgs {
+    RotaryArgs a;
+    Divisor units_of_head, units_of_token;
+    int turned;      // of a head's units, those that turn; the rest copy (none in place)
+};
+
+// V elements of T as floats, one 16-byte vector or a single element
+template <typename T, int V>
+__device__ __forceinline__ void load(const T* p, float (&v)[V]) {
+    if constexpr (V == 1) v[0] = (float)p[0];
+    else dev::load_vec(p, v);
+}
+template <typename T, int V>
+__device__ __forceinline__ void store(T* p, const float (&v)[V]) {
+    if constexpr (V == 1) p[0] = (T)v[0];
+    else dev::store_vec(p, v);
+}
+
+// cos and sin of p f, the product exact to 2^-53 and reduced to half a turn either way while it
+// is in 64 bits; sincospif is good to about one unit in the last place.
+__device__ __forceinline__ float2 turn(int p, float f, float factor) {
+    const double turns = (double)p * (double)f * 0.15915494309189533577;
+    float s, c;
+    sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
+    return {c * factor, s * factor};
+}
+
+// A head's units: pairs V j .. V j + V - 1 for j < turned, then 2 V elements each that only copy.
+template <typename T, int V, bool INTERLEAVED, int TB>
+__global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryKernelArgs k) {
+    extern __shared__ float2 turns[];
+    const gdn_rotary_shape& s = k.a.shape;
+    const int half = s.rotary_dim / 2, heads = s.num_q_heads + s.num_k_heads;
+    const int64_t first = (int64_t)blockIdx.x * TB;
+    const int tokens = (int)(k.a.num_tokens - first < TB ? k.a.num_tokens - first : TB);
+    for (int i = threadIdx.x; i < tokens * half; i += kThreads) {
+        const int t = TB == 1 ? 0 : i / half, f = i - t * half;
+        turns[i] = turn(k.a.positions[first + t], k.a.inv_freq[f], s.factor);
+    }
+    __syncthreads();
+    const int units = heads * (int)k.units_of_head.d;
+    for (int i = threadIdx.x; i < tokens * units; i += kThreads) {
+        const int t = TB == 1 ? 0 : (int)dev::divide(i, k.units_of_token), in_token = i - t * units;
+        if (k.a.positions[first + t] < 0) continue;
+        const int head = (int)dev::divide(in_token, k.units_of_head), unit = in_token - head * (int)k.units_of_head.d;
+        const int which = head >= s.num_q_heads, h = which ? head - s.num_q_heads : head;
+        const T* in = static_cast<const T*>(k.a.in[which]) + (first + t) * k.a.in_stride[which] + (int64_t)h * s.head_dim;
+        T* out = static_cast<T*>(k.a.out[which]) + (first + t) * k.a.out_stride[which] + (int64_t)h * s.head_dim;
+        float a[V], b[V];
+        if (unit >= k.turned) {
+            const int e = s.rotary_dim + (unit - k.turned) * 2 * V;
+            load<T, V>(in + e, a);
+            const bool both = e + 2 * V <= s.head_dim;
+            if (both) load<T, V>(in + e + V, b);
+            store<T, V>(out + e, a);
+            if (both) store<T, V>(out + e + V, b);
+            continue;
+        }
+        const int ea = INTERLEAVED ? 2 * V * unit : V * unit, eb = INTERLEAVED ? ea + V : ea + half;
+        const float2* cs = turns + t * half + V * unit;
+        load<T, V>(in + ea, a);
+        load<T, V>(in + eb, b);
+        float x[V], y[V];
+        if constexpr (INTERLEAVED) {
+            // the 2 V elements as pairs in order
+            float v[2 * V], w[2 * V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) { v[j] = a[j]; v[V + j] = b[j]; }
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float2 c = cs[j];
+                w[2 * j] = v[2 * j] * c.x - v[2 * j + 1] * c.y;
+                w[2 * j + 1] = v[2 * j + 1] * c.x + v[2 * j] * c.y;
+            }
+#pragma unroll
+            for (int j = 0; j < V; ++j) { x[j] = w[j]; y[j] = w[V + j]; }
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float2 c = cs[j];
+                x[j] = a[j] * c.x - b[j] * c.y;
+                y[j] = b[j] * c.x + a[j] * c.y;
+            }
+        }
+        store<T, V>(out + ea, x);
+        store<T, V>(out + eb, y);
+    }
+}
+
+template <typename T, int V, int TB>
+hipError_t launch(const RotaryArgs& a, hipStream_t stream) {
+    const gdn_rotary_shape& s = a.shape;
+    const bool in_place = (s.num_q_heads == 0 || a.in[0] == a.out[0]) && (s.num_k_heads == 0 || a.in[1] == a.out[1]);
+    RotaryKernelArgs k = {a, Divisor(), Divisor(), s.rotary_dim / (2 * V)};
+    const int copied = in_place ? 0 : (s.head_dim - s.rotary_dim + 2 * V - 1) / (2 * V);
+    k.units_of_head = Divisor(k.turned + copied);
+    k.units_of_token = Divisor((s.num_q_heads + s.num_k_heads) * (k.turned + copied));
+    const int64_t blocks = (a.num_tokens + TB - 1) / TB;
+    if (!grid_fits(blocks, kThreads)) return hipErrorInvalidConfiguration;
+    const size_t lds = (size_t)TB * (s.rotary_dim / 2) * sizeof(float2);
+    if (s.interleaved) rotary_kernel<T, V, true, TB><<<(unsigned)blocks, kThreads, lds, stream>>>(k);
+    else rotary_kernel<T, V, false, TB><<<(unsigned)blocks, kThreads, lds, stream>>>(k);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch(const RotaryArgs& a, hipStream_t stream) {
+    constexpr int V = dev::kVec<T>;
+    const gdn_rotary_shape& s = a.shape;
+    bool wide = s.rotary_dim % (2 * V) == 0 && s.head_dim % V == 0;
+    for (int i = 0; i < 2; ++i) {
+        if ((i ? s.num_k_heads : s.num_q_heads) == 0) continue;
+        wide = wide && a.in_stride[i] % V == 0 && a.out_stride[i] % V == 0 && (uintptr_t)a.in[i] % 16 == 0 && (uintptr_t)a.out[i] % 16 == 0;
+    }
+    if (!wide) return launch<T, 1, 1>(a, stream);
+    return launch<T, V, 1>(a, stream);
+}
+
+}  // namespace
+
+hipError_t launch_rotary(const RotaryArgs& a, hipStream_t stream) {
+    return a.shape.dtype == GDN_BF16 ? launch<__bf16>(a, stream) : launch<float>(a, stream);
+}
+
+}  // namespace gdn
