@@ -15,7 +15,8 @@ namespace gdn {
 // m d exceeds 2^(31 + l) by less than 2^l, so n m / 2^(31 + l) is n / d and less than 1 / d more.
 struct Divisor {
     uint32_t d, m, l;
-    explicit Divisor(uint32_t by = 1) : d(by), m(0), l(0) {
+    Divisor() : Divisor(1) {}
+    explicit Divisor(uint32_t by) : d(by), m(0), l(0) {
         while ((1ull << l) < d) ++l;
         m = (uint32_t)(((1ull << (31 + l)) + d - 1) / d);
     }
