@@ -14,7 +14,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libgdn.so")
 SOURCES = ["gdn_api.cpp", "gdn_decode.hip", "gdn_prefill.hip", "gdn_prefill_bf16.hip",
            "gdn_layer_api.cpp", "gdn_plan.hip", "gdn_conv.hip", "gdn_ssm.hip", "gdn_norm.hip",
-           "gdn_attention_api.cpp", "gdn_rotary.hip", "gdn_kv_cache.hip", "gdn_attention.hip"]
+           "gdn_attention_api.cpp", "gdn_rotary.hip", "gdn_kv_cache.hip", "gdn_attention.hip",
+           "gdn_attention_wide.hip"]
 PROBE_LIB = os.path.join(HERE, "libgdn_probe.so")
 PROBE_SOURCES = ["gdn_probe.hip"]
 ARCH = "gfx950"

@@ -28,48 +28,6 @@ using dev::f32x4_t;
 using dev::u32x4_t;
 
 constexpr int kThreads = 256, kWaves = 4, kTile = 32;
-constexpr int kMaxSpans = 64;
-constexpr float kLog2e = 1.4426950408889634f;
-
-// Keys of a span: at least this many for so many rows of a head, doubled until kMaxSpans suffice.
-__host__ __device__ inline int least_span(int rows) { return rows <= 16 ? 256 : (rows <= 64 ? 512 : 1024); }
-__host__ __device__ inline int span_keys(int rows, int keys) {
-    int span = least_span(rows);
-    while (keys > kMaxSpans * (int64_t)span) span *= 2;
-    return span;
-}
-
-struct KernelArgs {
-    AttentionArgs a;
-    Divisor block, group, rows;    // kv_block, query heads of a head, tokens_per_row
-    int spans;                     // decode: of the workspace, the most that a row may have
-    int row_tiles;                 // decode: workgroups for the rows of a head
-    float* part;                   // [tokens][H_q][spans][D]
-    float2* stats;                 // [tokens][H_q][spans]: running maximum, sum
-};
-
-// Where a workgroup's rows come from.
-struct Unit {
-    int seq, h;             // sequence (row of the call), cache head
-    int64_t first;          // its first token in q and o
-    int tokens, past;       // new tokens, cached tokens (clipped to what the table holds)
-    int row0, rows;         // first row of the tile, rows of the sequence's head
-    int lo, hi;             // keys [lo, hi)
-    int span, spans;        // which of the row's spans; spans of the row
-};
-
-template <typename T, int D>
-__device__ __forceinline__ void fill_rows(const KernelArgs& k, const Unit& u, int count, float value) {
-    const int G = (int)k.group.d;
-    for (int i = threadIdx.x; i < count * (D / 4); i += kThreads) {
-        const int r = u.row0 + i / (D / 4), e = i % (D / 4) * 4;
-        if (r >= u.rows) break;
-        const int t = (int)dev::divide(r, k.group);
-        T* o = static_cast<T*>(k.a.o) + ((u.first + t) * k.a.H_q + u.h * G + (r - t * G)) * D + e;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] = (T)value;
-    }
-}
 
 // V's rows in LDS: bf16 rows are D values, their 16-byte chunks exchanged by key so that neither the
 // stores (16 keys, one chunk) nor the transposing loads (4 keys, two chunks to a group of 16 lanes)
@@ -207,7 +165,7 @@ struct Lds {
 };
 
 template <typename T, int FORMAT, int D, int NT>
-__device__ __forceinline__ void attend(const KernelArgs& k, const Unit& u, char* lds) {
+__device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit& u, char* lds) {
     using S = Stored<T, FORMAT, D>;
     constexpr int kDims = D / 16;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane % 16, quad = lane / 16, G = (int)k.group.d;
@@ -230,12 +188,7 @@ __device__ __forceinline__ void attend(const KernelArgs& k, const Unit& u, char*
             const T* p = static_cast<const T*>(k.a.q) + (u.first + t) * k.a.q_stride + (int64_t)(u.h * G + (r - t * G)) * D;
 #pragma unroll
             for (int f = 0; f < S::kFrags; ++f) q[n][f] = S::query(p, f, lane);
-            if (k.a.tree_mask) {
-                const uint64_t all = u.tokens >= 64 ? ~0ull : (1ull << u.tokens) - 1;
-                sees[n] = {u.past, u.past, (uint64_t)k.a.tree_mask[u.first + t] & all};
-            } else {
-                sees[n].all = u.past + t + 1;
-            }
+            sees[n] = row_sees(k, u, r);
         } else {
 #pragma unroll
             for (int f = 0; f < S::kFrags; ++f) q[n][f] = dev::frag_t<T>{};
@@ -424,46 +377,24 @@ __device__ __forceinline__ void attend(const KernelArgs& k, const Unit& u, char*
     }
 }
 
-// Keys of a decode row, all of its tokens' among them, as far as its table goes; < 0 for a padding row.
-__device__ __forceinline__ int row_keys(const AttentionArgs& a, int past) {
-    if (past < 0) return -1;
-    const int64_t keys = (int64_t)past + a.tokens_per_row;
-    return (int)(keys < a.capacity ? keys : a.capacity);
+template <typename T, int FORMAT, int D, int NT>
+__global__ __launch_bounds__(kThreads) void decode_kernel(AttentionKernelArgs k) {
+    extern __shared__ __align__(16) char lds[];
+    Unit u;
+    if (decode_unit<T, D>(k, 16 * NT, kThreads, u)) attend<T, FORMAT, D, NT>(k, u, lds);
 }
 
 template <typename T, int FORMAT, int D, int NT>
-__global__ __launch_bounds__(kThreads) void decode_kernel(KernelArgs k) {
+__global__ __launch_bounds__(kThreads) void prompt_kernel(AttentionKernelArgs k) {
     extern __shared__ __align__(16) char lds[];
-    // the row tiles of one span of keys stand 8 apart: on the same XCD, whose L2 then holds its keys
-    const unsigned id = blockIdx.x, tile = id / 8 % (unsigned)k.row_tiles, at = id / (8 * (unsigned)k.row_tiles) * 8 + id % 8;
-    const unsigned H = (unsigned)k.a.cache.num_heads, by_head = at / H, spans = (unsigned)k.spans;
+    const unsigned H = (unsigned)k.a.cache.num_heads, tile = blockIdx.x / H;
     Unit u;
-    u.h = (int)(at - by_head * H);
-    u.seq = (int)(by_head / spans);
-    u.span = (int)(by_head - (unsigned)u.seq * spans);
-    if (u.seq >= k.a.num_seqs) return;
-    u.past = k.a.past[u.seq];
-    u.tokens = k.a.tokens_per_row;
-    u.first = (int64_t)u.seq * u.tokens;
-    u.rows = u.tokens * (int)k.group.d;
-    u.row0 = (int)tile * 16 * NT;
-    const int keys = row_keys(k.a, u.past);
-    if (keys <= 0 || keys > k.a.max_keys) {
-        if (u.span == 0) fill_rows<T, D>(k, u, 16 * NT, keys > 0 ? NAN : 0.f);
-        return;
-    }
-    const int span = span_keys(u.rows, keys);
-    u.spans = (keys + span - 1) / span;
-    if (u.span >= u.spans) return;
-    u.past = u.past < k.a.capacity ? u.past : k.a.capacity;
-    u.lo = u.span * span;
-    u.hi = keys - u.lo < span ? keys : u.lo + span;
-    attend<T, FORMAT, D, NT>(k, u, lds);
+    if (prompt_unit(k, 16 * NT, (int)tile, (int)(blockIdx.x - tile * H), u)) attend<T, FORMAT, D, NT>(k, u, lds);
 }
 
 // A row's spans joined: one wave for each query head of a token.
 template <typename T, int D>
-__global__ __launch_bounds__(kThreads) void join_kernel(KernelArgs k) {
+__global__ __launch_bounds__(kThreads) void join_kernel(AttentionKernelArgs k) {
     const int64_t at = (int64_t)blockIdx.x * (kThreads / 64) + threadIdx.x / 64;
     const int lane = threadIdx.x & 63;
     if (at >= k.a.total_tokens * k.a.H_q) return;
@@ -492,52 +423,10 @@ __global__ __launch_bounds__(kThreads) void join_kernel(KernelArgs k) {
     for (int i = 0; i < N; ++i) o[i] = (T)(x[i] * inv);
 }
 
-// Packed prompts: tiles of 16 NT rows, the first of sequence i is number cu[i] G / (16 NT) + i, so that a
-// tile's sequence is found by bisection and no two share a tile.
-template <typename T, int FORMAT, int D, int NT>
-__global__ __launch_bounds__(kThreads) void prompt_kernel(KernelArgs k) {
-    extern __shared__ __align__(16) char lds[];
-    const unsigned H = (unsigned)k.a.cache.num_heads, tile = blockIdx.x / H;
-    const int G = (int)k.group.d;
-    const int64_t T_ = k.a.total_tokens;
-    const auto first_tile = [&](int i) {
-        int64_t c = k.a.cu_seqlens[i];
-        c = c < 0 ? 0 : (c > T_ ? T_ : c);
-        return c * G / (16 * NT) + i;
-    };
-    int lo = 0, hi = k.a.num_seqs;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (first_tile(mid) <= (int64_t)tile) lo = mid; else hi = mid;
-    }
-    Unit u;
-    u.seq = lo;
-    u.h = (int)(blockIdx.x - tile * H);
-    int64_t b = k.a.cu_seqlens[lo], e = k.a.cu_seqlens[lo + 1];
-    b = b < 0 ? 0 : (b > T_ ? T_ : b);
-    e = e < b ? b : (e > T_ ? T_ : e);
-    const int64_t row0 = ((int64_t)tile - first_tile(lo)) * 16 * NT;
-    if (row0 < 0 || row0 >= (e - b) * G) return;
-    u.first = b;
-    u.tokens = (int)(e - b);
-    u.rows = u.tokens * G;
-    u.row0 = (int)row0;
-    int past = k.a.past ? k.a.past[lo] : 0;
-    past = past < 0 ? 0 : past;
-    u.past = past < k.a.capacity ? past : k.a.capacity;
-    const int last = (u.row0 + 16 * NT < u.rows ? u.row0 + 16 * NT : u.rows) - 1;
-    const int64_t keys = (int64_t)u.past + (int)dev::divide(last, k.group) + 1;
-    u.lo = 0;
-    u.hi = (int)(keys < k.a.capacity ? keys : k.a.capacity);
-    u.span = 0;
-    u.spans = 1;
-    attend<T, FORMAT, D, NT>(k, u, lds);
-}
-
 // ---------------------------------------------------------------- launches
 
-KernelArgs kernel_args(const AttentionArgs& a) {
-    KernelArgs k = {};
+AttentionKernelArgs kernel_args(const AttentionArgs& a) {
+    AttentionKernelArgs k = {};
     k.a = a;
     if (a.cache.num_rows == 0) {        // no key is there
         k.a.capacity = 0;
@@ -554,46 +443,52 @@ int most_spans(int rows, int64_t keys) {
 }
 
 template <typename T, int FORMAT, int D, int NT>
+hipError_t launch_rows(AttentionKernelArgs k, hipStream_t stream) {
+    const int rows = k.a.tokens_per_row * (int)k.group.d;
+    k.row_tiles = (rows + 16 * NT - 1) / (16 * NT);
+    const int64_t blocks = ((int64_t)k.a.num_seqs * k.spans * k.a.cache.num_heads + 7) / 8 * 8 * k.row_tiles;
+    if (!grid_fits(blocks, kThreads)) return hipErrorInvalidConfiguration;
+    decode_kernel<T, FORMAT, D, NT><<<(unsigned)blocks, kThreads, Lds<T, D>::kTotal, stream>>>(k);
+    return hipGetLastError();
+}
+
+template <typename T, int FORMAT, int D>
 hipError_t launch_decode(const AttentionArgs& a, hipStream_t stream) {
-    KernelArgs k = kernel_args(a);
+    AttentionKernelArgs k = kernel_args(a);
     const int rows = a.tokens_per_row * (int)k.group.d;
     k.rows = Divisor((uint32_t)a.tokens_per_row);
-    k.spans = most_spans(rows, a.max_keys);
-    k.row_tiles = (rows + 16 * NT - 1) / (16 * NT);
-    const int64_t heads = a.total_tokens * a.H_q;
+    k.spans = most_spans(rows, k.a.max_keys);
+    const int64_t heads = a.total_tokens * a.H_q, joins = (heads + kThreads / 64 - 1) / (kThreads / 64);
+    if (!grid_fits(joins, kThreads)) return hipErrorInvalidConfiguration;
     k.part = static_cast<float*>(a.workspace);
     k.stats = reinterpret_cast<float2*>(k.part + (k.spans > 1 ? heads * k.spans * D : 0));
-    const int64_t units = ((int64_t)a.num_seqs * k.spans * a.cache.num_heads + 7) / 8 * 8;
-    const int64_t blocks = units * k.row_tiles, joins = (heads + kThreads / 64 - 1) / (kThreads / 64);
-    if (!grid_fits(blocks, kThreads) || !grid_fits(joins, kThreads)) return hipErrorInvalidConfiguration;
-    decode_kernel<T, FORMAT, D, NT><<<(unsigned)blocks, kThreads, Lds<T, D>::kTotal, stream>>>(k);
-    hipError_t e = hipGetLastError();
+    // as many row tiles to a wave as the rows fill and the registers hold
+    constexpr int most = (sizeof(T) == 2 ? 512 : 256) / D;
+    hipError_t e;
+    if (sizeof(T) == 2 && rows > 64) e = launch_attention_wide(k, stream);
+    else if (rows <= 16 || most == 1) e = launch_rows<T, FORMAT, D, 1>(k, stream);
+    else if (rows <= 32 || most == 2) e = launch_rows<T, FORMAT, D, (most > 1 ? 2 : 1)>(k, stream);
+    else e = launch_rows<T, FORMAT, D, (most > 2 ? 4 : 1)>(k, stream);
     if (e != hipSuccess || k.spans == 1) return e;
     join_kernel<T, D><<<(unsigned)joins, kThreads, 0, stream>>>(k);
     return hipGetLastError();
 }
 
-template <typename T, int FORMAT, int D, int NT>
+template <int FORMAT, int D>
 hipError_t launch_prompt(const AttentionArgs& a, hipStream_t stream) {
-    const KernelArgs k = kernel_args(a);
+    constexpr int NT = D <= 64 ? 4 : (D <= 128 ? 2 : 1);
+    const AttentionKernelArgs k = kernel_args(a);
     const int64_t tiles = a.total_tokens * (int)k.group.d / (16 * NT) + a.num_seqs, blocks = tiles * a.cache.num_heads;
     if (!grid_fits(blocks, kThreads) || a.total_tokens * (int64_t)k.group.d > 0x7fffffffLL) return hipErrorInvalidConfiguration;
-    prompt_kernel<T, FORMAT, D, NT><<<(unsigned)blocks, kThreads, Lds<T, D>::kTotal, stream>>>(k);
+    prompt_kernel<float, FORMAT, D, NT><<<(unsigned)blocks, kThreads, Lds<float, D>::kTotal, stream>>>(k);
     return hipGetLastError();
 }
 
-// As many row tiles to a wave as the rows fill and the registers hold.
 template <typename T, int FORMAT, int D>
 hipError_t launch(const AttentionArgs& a, hipStream_t stream) {
-    constexpr int most = (sizeof(T) == 2 ? 512 : 256) / D;       // 4 at 128 dims in bf16
-    if (a.tokens_per_row == 0) return launch_prompt<T, FORMAT, D, most < 4 ? most : 4>(a, stream);
-    const int rows = a.tokens_per_row * (a.H_q / a.cache.num_heads);
-    if (rows <= 16 || most == 1) return launch_decode<T, FORMAT, D, 1>(a, stream);
-    if constexpr (most >= 2) {
-        if (rows <= 32 || most == 2) return launch_decode<T, FORMAT, D, 2>(a, stream);
-        if constexpr (most >= 4) return launch_decode<T, FORMAT, D, 4>(a, stream);
-    }
-    return hipErrorInvalidValue;
+    if (a.tokens_per_row > 0) return launch_decode<T, FORMAT, D>(a, stream);
+    if constexpr (sizeof(T) == 2) return launch_attention_wide(kernel_args(a), stream);
+    else return launch_prompt<FORMAT, D>(a, stream);
 }
 
 template <typename T, int FORMAT>

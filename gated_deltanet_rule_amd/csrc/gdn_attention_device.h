@@ -120,4 +120,130 @@ struct Sees {
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) < INFINITY; }
 
 }  // namespace dev
+
+// Keys of a span of a long context: at least this many for so many rows of a head, doubled until kMaxSpans suffice.
+constexpr int kMaxSpans = 64;
+__host__ __device__ inline int least_span(int rows) { return rows <= 16 ? 256 : (rows <= 64 ? 512 : 1024); }
+__host__ __device__ inline int span_keys(int rows, int keys) {
+    int span = least_span(rows);
+    while (keys > kMaxSpans * (int64_t)span) span *= 2;
+    return span;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct AttentionKernelArgs {
+    AttentionArgs a;
+    Divisor block, group, rows;    // kv_block, query heads of a head, tokens_per_row
+    int spans;                     // decode: of the workspace, the most that a row may have
+    int row_tiles;                 // decode: workgroups for the rows of a head
+    float* part;                   // [tokens][H_q][spans][D]
+    float2* stats;                 // [tokens][H_q][spans]: running maximum, sum
+};
+
+// Where a workgroup's rows come from.
+struct Unit {
+    int seq, h;             // sequence (row of the call), cache head
+    int64_t first;          // its first token in q and o
+    int tokens, past;       // new tokens, cached tokens (clipped to what the table holds)
+    int row0, rows;         // first row of the tile, rows of the sequence's head
+    int lo, hi;             // keys [lo, hi)
+    int span, spans;        // which of the row's spans; spans of the row
+};
+
+// gdn_attention_wide.hip: bf16 prompts, and decode rows (without the join of their spans).
+hipError_t launch_attention_wide(const AttentionKernelArgs& k, hipStream_t stream);
+
+// Keys of a decode row, all of its tokens' among them, as far as its table goes; < 0 for a padding row.
+__device__ __forceinline__ int row_keys(const AttentionArgs& a, int past) {
+    if (past < 0) return -1;
+    const int64_t keys = (int64_t)past + a.tokens_per_row;
+    return (int)(keys < a.capacity ? keys : a.capacity);
+}
+
+// Outputs of `count` rows of a tile set to one value, by `threads` threads.
+template <typename T, int D>
+__device__ __forceinline__ void fill_rows(const AttentionKernelArgs& k, const Unit& u, int count, int threads, float value) {
+    const int G = (int)k.group.d;
+    for (int i = threadIdx.x; i < count * (D / 4); i += threads) {
+        const int r = u.row0 + i / (D / 4), e = i % (D / 4) * 4;
+        if (r >= u.rows) break;
+        const int t = (int)dev::divide(r, k.group);
+        T* o = static_cast<T*>(k.a.o) + ((u.first + t) * k.a.H_q + u.h * G + (r - t * G)) * D + e;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = (T)value;
+    }
+}
+
+// Decode: the span of keys and the tile of `per` rows of workgroup blockIdx.x.  False where there is nothing to
+// attend to: a padding row's outputs are zeros then, those of a row with more keys than max_keys NaN.
+template <typename T, int D>
+__device__ __forceinline__ bool decode_unit(const AttentionKernelArgs& k, int per, int threads, Unit& u) {
+    // the row tiles of one span of keys stand 8 apart: on the same XCD, whose L2 then holds its keys
+    const unsigned id = blockIdx.x, tile = id / 8 % (unsigned)k.row_tiles, at = id / (8 * (unsigned)k.row_tiles) * 8 + id % 8;
+    const unsigned H = (unsigned)k.a.cache.num_heads, by_head = at / H, spans = (unsigned)k.spans;
+    u.h = (int)(at - by_head * H);
+    u.seq = (int)(by_head / spans);
+    u.span = (int)(by_head - (unsigned)u.seq * spans);
+    if (u.seq >= k.a.num_seqs) return false;
+    u.past = k.a.past[u.seq];
+    u.tokens = k.a.tokens_per_row;
+    u.first = (int64_t)u.seq * u.tokens;
+    u.rows = u.tokens * (int)k.group.d;
+    u.row0 = (int)tile * per;
+    const int keys = row_keys(k.a, u.past);
+    if (keys <= 0 || keys > k.a.max_keys) {
+        if (u.span == 0) fill_rows<T, D>(k, u, per, threads, keys > 0 ? NAN : 0.f);
+        return false;
+    }
+    const int span = span_keys(u.rows, keys);
+    u.spans = (keys + span - 1) / span;
+    if (u.span >= u.spans) return false;
+    u.past = u.past < k.a.capacity ? u.past : k.a.capacity;
+    u.lo = u.span * span;
+    u.hi = keys - u.lo < span ? keys : u.lo + span;
+    return true;
+}
+
+// Packed prompts: tile number `tile` of `per` rows.  The first tile of sequence i is number cu[i] G / per + i, so
+// that a tile's sequence is found by bisection and no two share a tile; false for the tiles in between.
+__device__ __forceinline__ bool prompt_unit(const AttentionKernelArgs& k, int per, int tile, int h, Unit& u) {
+    const int G = (int)k.group.d;
+    const int64_t total = k.a.total_tokens;
+    const auto token = [&](int i) {
+        const int64_t c = k.a.cu_seqlens[i];
+        return c < 0 ? 0 : (c > total ? total : c);
+    };
+    int lo = 0, hi = k.a.num_seqs;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (token(mid) * G / per + mid <= tile) lo = mid; else hi = mid;
+    }
+    u.seq = lo;
+    u.h = h;
+    const int64_t b = token(lo), e = token(lo + 1), row0 = (tile - b * G / per - lo) * per;
+    if (row0 < 0 || row0 >= (e - b) * G) return false;
+    u.first = b;
+    u.tokens = (int)(e - b);
+    u.rows = u.tokens * G;
+    u.row0 = (int)row0;
+    const int past = k.a.past ? k.a.past[lo] : 0;
+    u.past = past < 0 ? 0 : (past < k.a.capacity ? past : k.a.capacity);
+    const int last = (u.row0 + per < u.rows ? u.row0 + per : u.rows) - 1;
+    const int64_t keys = (int64_t)u.past + (int)dev::divide(last, k.group) + 1;
+    u.lo = 0;
+    u.hi = (int)(keys < k.a.capacity ? keys : k.a.capacity);
+    u.span = 0;
+    u.spans = 1;
+    return true;
+}
+
+// Where row r of a unit (a query head of a token) stands in q and o, and the keys that it sees.
+__device__ __forceinline__ dev::Sees row_sees(const AttentionKernelArgs& k, const Unit& u, int r) {
+    const int t = (int)dev::divide(r, k.group);
+    if (!k.a.tree_mask) return {u.past + t + 1, 0, 0};
+    const uint64_t all = u.tokens >= 64 ? ~0ull : (1ull << u.tokens) - 1;
+    return {u.past, u.past, (uint64_t)k.a.tree_mask[u.first + t] & all};
+}
+
 }  // namespace gdn

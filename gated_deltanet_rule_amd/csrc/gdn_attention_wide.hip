@@ -1,0 +1,362 @@
+// gdn_attention_wide.hip -- attention of many query rows over a paged cache for gfx950: bf16
+// prompts, and decode rows with large trees.
+//
+// The same sums as gdn_attention.hip, for rows enough to share the keys: four waves of 32 rows
+// take the same tile of 64 keys from LDS, two tiles of which stand there in turn: while one is
+// worked on, the next is loaded into registers and widened, if it holds codes, on its way into
+// the other.  The products are transposed here too, 32 x 32 tiles with a query row to each pair of
+// lanes, so that weights are the second product's operand as they come out of the first.
+#include <hip/hip_runtime.h>
+
+#include "gdn_attention_device.h"
+#include "gdn_layer_internal.h"
+
+namespace gdn {
+namespace {
+
+using dev::bf16x8_t;
+using dev::f32x4_t;
+using dev::f32x16_t;
+using dev::u32x4_t;
+
+constexpr int kThreads = 256, kWaves = 4, kTile = 64, kRows = 128;
+
+__device__ __forceinline__ f32x16_t mma32(bf16x8_t a, bf16x8_t b, f32x16_t acc) { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, acc, 0, 0, 0); }
+
+// One tile of K or V in LDS: rows of D bf16 values, 16-byte chunks exchanged by key, so that neither eight keys'
+// equal chunks (K's operands) nor four keys' neighbouring two (V's transposing loads) meet in a bank.
+template <int D>
+struct Tile {
+    static constexpr int kRow = D * 2, kBytes = kTile * kRow;
+    __device__ static __forceinline__ int chunk(int key, int c) { return key * kRow + ((c ^ (D >= 128 ? (2 * key) & 15 : key & 6)) * 16); }
+};
+
+// LDS of a workgroup: two tiles each of K and V; for each, the keys' factors (score, value) and whether a wave
+// met a value that is not finite where that matters.
+template <int D>
+struct Lds {
+    static constexpr int kTiles = 4 * Tile<D>::kBytes;
+    static constexpr int kFactors = 2 * 2 * kTile * 4;
+    static constexpr int kTotal = kTiles + kFactors + 2 * kWaves * 4;
+};
+
+template <int FORMAT, int D>
+__device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit& u, char* lds) {
+    constexpr bool kCodes = FORMAT != GDN_CACHE_PLAIN;
+    constexpr int kElem = kCodes ? 1 : 2, kRowBytes = D * kElem;
+    constexpr int kPerRow = kRowBytes / 16, kRowsAtOnce = kThreads / kPerRow, kPasses = kTile / kRowsAtOnce;
+    constexpr int kSteps = D / 16, kDims = D / 32;
+    if (u.lo >= u.hi) {        // a table or a cache without rows: no address may be formed
+        fill_rows<__bf16, D>(k, u, kRows, kThreads, 0.f);
+        return;
+    }
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 31, half = lane >> 5, G = (int)k.group.d;
+    const int H = k.a.cache.num_heads;
+    const dev::Pages pages = {k.a.table + (int64_t)u.seq * k.a.table_width, k.a.table_width, k.block, k.a.cache.num_rows};
+    float* const factors = reinterpret_cast<float*>(lds + Lds<D>::kTiles);
+    int* const flags = reinterpret_cast<int*>(lds + Lds<D>::kTiles + Lds<D>::kFactors);
+    // the scale's sign goes into the queries (exactly), so that the largest product is the largest score
+    const float c = k.a.scale == 0.f ? 1.f : fabsf(k.a.scale) * kLog2e, sign = k.a.scale == 0.f ? 0.f : copysignf(1.f, k.a.scale);
+
+    const int r = u.row0 + 32 * wave + col, t = (int)dev::divide(r, k.group);
+    const bool live = r < u.rows;
+    const bool busy = u.row0 + 32 * wave < u.rows;       // whether the wave has any rows
+    bf16x8_t q[kSteps] = {};
+    dev::Sees sees = {0, 0, 0};
+    if (live) {
+        const __bf16* p = static_cast<const __bf16*>(k.a.q) + (u.first + t) * k.a.q_stride + (int64_t)(u.h * G + (r - t * G)) * D + half * 8;
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) q[s] = *reinterpret_cast<const bf16x8_t*>(p + 16 * s);
+        if (sign != 1.f)
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) q[s][i] = (__bf16)((float)q[s][i] * sign);
+        sees = row_sees(k, u, r);
+    }
+    // every row of the workgroup (of the wave) sees the keys below `some` (`mine`), no row of the wave one from `end` on
+    const bool tree = k.a.tree_mask != nullptr;
+    const int some = tree ? u.past : u.past + (int)dev::divide(u.row0, k.group) + 1;
+    const int first_row = u.row0 + 32 * wave, last_row = (first_row + 32 < u.rows ? first_row + 32 : u.rows) - 1;
+    const int mine = tree ? u.past : u.past + (int)dev::divide(first_row, k.group) + 1;
+    const int end = !busy ? 0 : (tree ? u.hi : u.past + (int)dev::divide(last_row, k.group) + 1);
+
+    f32x16_t o[kDims] = {};
+    float m = -INFINITY, l = 0.f;
+
+    // ---- one tile ahead: the keys' rows, then what they hold
+    const auto lookup = [&](int p0) {
+        const int p = p0 + lane;
+        return p < u.hi ? pages.row(p) : (int64_t)-1;
+    };
+    u32x4_t kp[kPasses], vp[kPasses];
+    float ks = 0.f, vs = 0.f;
+    const auto load = [&](int64_t row) {
+        const char* kc = static_cast<const char*>(k.a.cache.k) + threadIdx.x % kPerRow * 16 + (int64_t)u.h * kRowBytes;
+        const char* vc = static_cast<const char*>(k.a.cache.v) + threadIdx.x % kPerRow * 16 + (int64_t)u.h * kRowBytes;
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            const int from = i * kRowsAtOnce + threadIdx.x / kPerRow;
+            const int lo = __shfl((int)(uint64_t)row, from), hi = __shfl((int)((uint64_t)row >> 32), from);
+            int64_t at = (int64_t)((uint64_t)(unsigned)hi << 32 | (unsigned)lo);
+            at = (at < 0 ? 0 : at) * H * kRowBytes;
+            kp[i] = *reinterpret_cast<const u32x4_t*>(kc + at);
+            vp[i] = *reinterpret_cast<const u32x4_t*>(vc + at);
+        }
+        if constexpr (kCodes) {
+            ks = row >= 0 ? k.a.cache.k_scale[row * H + u.h] : 0.f;
+            vs = row >= 0 ? k.a.cache.v_scale[row * H + u.h] : 0.f;
+        }
+    };
+    // Into the tiles of `buf`.  Absent keys' values are zeros: their weights are, and nothing that is not finite may
+    // meet those.  `check`: some rows do not see some of the tile's keys; whether a value of theirs is not finite.
+    const auto store = [&](int buf, uint64_t present, bool check) {
+        char* const kt = lds + buf * 2 * Tile<D>::kBytes;
+        char* const vt = kt + Tile<D>::kBytes;
+        bool fine = true;
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            const int key = i * kRowsAtOnce + threadIdx.x / kPerRow, piece = threadIdx.x % kPerRow;
+            const bool there = present >> key & 1;
+            if constexpr (kCodes) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    *reinterpret_cast<bf16x8_t*>(kt + Tile<D>::chunk(key, 2 * piece + x)) = dev::codes8<__bf16, FORMAT>(kp[i][2 * x], kp[i][2 * x + 1]);
+                    bf16x8_t v = dev::codes8<__bf16, FORMAT>(vp[i][2 * x], vp[i][2 * x + 1]);
+                    if (!there) v = bf16x8_t{};
+                    if (check)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) fine &= dev::finite((float)v[j]);
+                    *reinterpret_cast<bf16x8_t*>(vt + Tile<D>::chunk(key, 2 * piece + x)) = v;
+                }
+            } else {
+                *reinterpret_cast<u32x4_t*>(kt + Tile<D>::chunk(key, piece)) = kp[i];
+                bf16x8_t v = __builtin_bit_cast(bf16x8_t, vp[i]);
+                if (!there) v = bf16x8_t{};
+                if (check)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) fine &= dev::finite((float)v[j]);
+                *reinterpret_cast<bf16x8_t*>(vt + Tile<D>::chunk(key, piece)) = v;
+            }
+        }
+        if constexpr (kCodes) {
+            if (check) fine &= dev::finite(vs);
+            if (wave == 0) {
+                factors[buf * 2 * kTile + lane] = ks * c;
+                factors[buf * 2 * kTile + kTile + lane] = vs;
+            }
+        }
+        const bool bad = __any(!fine);
+        if (lane == 0) flags[buf * kWaves + wave] = bad;
+    };
+
+    int64_t next_row = lookup(u.lo);
+    uint64_t present = __ballot(next_row >= 0);
+    load(next_row);
+    next_row = lookup(u.lo + kTile);
+    store(0, present, present != ~0ull || u.lo + kTile > some);
+    __syncthreads();
+
+    int buf = 0;
+    for (int p0 = u.lo; p0 < u.hi; p0 += kTile, buf ^= 1) {
+        const bool more = p0 + kTile < u.hi;
+        const uint64_t now = present;
+        if (more) {
+            present = __ballot(next_row >= 0);
+            load(next_row);
+            next_row = lookup(p0 + 2 * kTile);
+        }
+        const char* const kt = lds + buf * 2 * Tile<D>::kBytes;
+        const char* const vt = kt + Tile<D>::kBytes;
+        const float* const factor = factors + buf * 2 * kTile;
+        const bool work = p0 < end;
+        const bool partial = now != ~0ull || p0 + kTile > mine;
+        f32x16_t s[2] = {};
+        uint64_t seen = ~0ull;
+        if (work) {
+#pragma unroll
+            for (int x = 0; x < kSteps; ++x)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const bf16x8_t kf = *reinterpret_cast<const bf16x8_t*>(kt + Tile<D>::chunk(32 * b + col, 2 * x + half));
+                    s[b] = mma32(kf, q[x], s[b]);
+                }
+            if constexpr (kCodes)
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const f32x4_t by = *reinterpret_cast<const f32x4_t*>(factor + 32 * b + 8 * i + 4 * half);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) s[b][4 * i + j] *= by[j];
+                    }
+            if (partial) {
+                seen = sees.from(p0) & now;
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const unsigned bits = (unsigned)(seen >> (32 * b)) >> (4 * half);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (!(bits >> (8 * (i / 4) + i % 4) & 1)) s[b][i] = -INFINITY;
+                }
+            }
+            float top = -INFINITY;
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
+            float x, y;
+            dev::pair32(top, x, y);
+            top = fmaxf(x, y);
+            if constexpr (!kCodes) top *= c;
+            const float next = fmaxf(m, top);
+            if (__any(next > m)) {
+                const float keep = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - next);
+                l *= keep;
+#pragma unroll
+                for (int d = 0; d < kDims; ++d)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[d][i] *= keep;
+                m = next;
+            }
+        }
+        // Values that are not finite, where some rows do not see them: added to the rows that do, zeros in the product.
+        int bad = 0;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) bad |= flags[buf * kWaves + w];
+        if (bad) {
+            if (work) {
+                for (int key = 0; key < kTile; ++key) {
+                    if (!(now >> key & 1)) continue;
+                    float by = 1.f;
+                    if constexpr (kCodes) by = factor[kTile + key];
+#pragma unroll
+                    for (int d = 0; d < kDims; ++d)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const int dim = 32 * d + 8 * (i / 4) + 4 * half + i % 4;
+                            float v = (float)*reinterpret_cast<const __bf16*>(vt + Tile<D>::chunk(key, dim / 8) + dim % 8 * 2);
+                            if (!dev::finite(by)) v = NAN;
+                            if (!dev::finite(v) && (seen >> key & 1)) o[d][i] += v;
+                        }
+                }
+            }
+            __syncthreads();
+            for (int i = threadIdx.x; i < kTile * D / 8; i += kThreads) {
+                bf16x8_t* const at = reinterpret_cast<bf16x8_t*>(lds + buf * 2 * Tile<D>::kBytes + Tile<D>::kBytes) + i;
+                bf16x8_t v = *at;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (!dev::finite((float)v[j])) v[j] = (__bf16)0.f;
+                *at = v;
+            }
+            if (kCodes && threadIdx.x < kTile) {
+                float* const at = factors + buf * 2 * kTile + kTile + threadIdx.x;
+                if (!dev::finite(*at)) *at = 0.f;
+            }
+            __syncthreads();
+        }
+        if (work) {
+            const float base = m == -INFINITY ? 0.f : m;
+            bf16x8_t w[4];
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    f32x4_t by = {1.f, 1.f, 1.f, 1.f};
+                    if constexpr (kCodes) by = *reinterpret_cast<const f32x4_t*>(factor + kTile + 32 * b + 8 * i + 4 * half);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float x = __builtin_amdgcn_exp2f(kCodes ? s[b][4 * i + j] - base : fmaf(s[b][4 * i + j], c, -base));
+                        l += x;
+                        w[2 * b + i / 2][4 * (i & 1) + j] = (__bf16)(x * by[j]);
+                    }
+                }
+            typedef __attribute__((address_space(3))) dev::s16x4_t* lds_ptr;
+            const int key = 4 * half + lane % 16 / 4, piece = 2 * (lane >> 4 & 1) + (lane >> 1 & 1);
+#pragma unroll
+            for (int d = 0; d < kDims; ++d)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const auto a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(vt + Tile<D>::chunk(16 * g + key, 4 * d + piece) + (lane & 1) * 8));
+                    const auto b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(vt + Tile<D>::chunk(16 * g + 8 + key, 4 * d + piece) + (lane & 1) * 8));
+                    const dev::bf16x4_t x = __builtin_bit_cast(dev::bf16x4_t, a), y = __builtin_bit_cast(dev::bf16x4_t, b);
+                    o[d] = mma32(__builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7), w[g], o[d]);
+                }
+        }
+        if (more) store(buf ^ 1, present, present != ~0ull || p0 + 2 * kTile > some);
+        __syncthreads();
+    }
+
+    float x, y;
+    dev::pair32(l, x, y);
+    l = x + y;
+    if (!live) return;
+    const int64_t at = (u.first + t) * k.a.H_q + u.h * G + (r - t * G);
+    if (u.spans > 1) {
+        float* const part = k.part + (at * k.spans + u.span) * D + 4 * half;
+#pragma unroll
+        for (int d = 0; d < kDims; ++d)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) *reinterpret_cast<f32x4_t*>(part + 32 * d + 8 * i) = f32x4_t{o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
+        if (half == 0) k.stats[at * k.spans + u.span] = {m, l};
+        return;
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    __bf16* const out = static_cast<__bf16*>(k.a.o) + at * D + 4 * half;
+#pragma unroll
+    for (int d = 0; d < kDims; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            dev::bf16x4_t v;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = (__bf16)(o[d][4 * i + j] * inv);
+            *reinterpret_cast<dev::bf16x4_t*>(out + 32 * d + 8 * i) = v;
+        }
+}
+
+template <int FORMAT, int D>
+__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void wide_decode_kernel(AttentionKernelArgs k) {
+    extern __shared__ __align__(16) char lds[];
+    Unit u;
+    if (decode_unit<__bf16, D>(k, kRows, kThreads, u)) attend<FORMAT, D>(k, u, lds);
+}
+
+// Tiles from the last to the first: those with the most keys start first.
+template <int FORMAT, int D>
+__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void wide_prompt_kernel(AttentionKernelArgs k) {
+    extern __shared__ __align__(16) char lds[];
+    const unsigned H = (unsigned)k.a.cache.num_heads, at = blockIdx.x / H;
+    Unit u;
+    if (prompt_unit(k, kRows, k.row_tiles - 1 - (int)at, (int)(blockIdx.x - at * H), u)) attend<FORMAT, D>(k, u, lds);
+}
+
+template <int FORMAT, int D>
+hipError_t launch(AttentionKernelArgs k, hipStream_t stream) {
+    const int H = k.a.cache.num_heads;
+    const bool decode = k.a.tokens_per_row > 0;
+    const int64_t tiles = decode ? (k.a.tokens_per_row * (int)k.group.d + kRows - 1) / kRows : k.a.total_tokens * (int)k.group.d / kRows + k.a.num_seqs;
+    const int64_t units = decode ? ((int64_t)k.a.num_seqs * k.spans * H + 7) / 8 * 8 : H;
+    if (!grid_fits(tiles * units, kThreads) || k.a.total_tokens * (int64_t)k.group.d > 0x7fffffffLL) return hipErrorInvalidConfiguration;
+    k.row_tiles = (int)tiles;
+    auto* const kernel = decode ? wide_decode_kernel<FORMAT, D> : wide_prompt_kernel<FORMAT, D>;
+    kernel<<<(unsigned)(tiles * units), kThreads, Lds<D>::kTotal, stream>>>(k);
+    return hipGetLastError();
+}
+
+template <int FORMAT>
+hipError_t launch(const AttentionKernelArgs& k, hipStream_t stream) {
+    if (k.a.cache.head_dim == 64) return launch<FORMAT, 64>(k, stream);
+    if (k.a.cache.head_dim == 128) return launch<FORMAT, 128>(k, stream);
+    return launch<FORMAT, 256>(k, stream);
+}
+
+}  // namespace
+
+hipError_t launch_attention_wide(const AttentionKernelArgs& k, hipStream_t stream) {
+    if (k.a.cache.format == GDN_CACHE_PLAIN) return launch<GDN_CACHE_PLAIN>(k, stream);
+    if (k.a.cache.format == GDN_CACHE_E4M3) return launch<GDN_CACHE_E4M3>(k, stream);
+    return launch<GDN_CACHE_INT8>(k, stream);
+}
+
+}  // namespace gdn
