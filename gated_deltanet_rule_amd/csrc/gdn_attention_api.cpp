@@ -66,6 +66,7 @@ gdn_status check_cache(const gdn_kv_cache* c) {
     gdn_status st = check_cache_shape(c);
     if (st != GDN_OK) return st;
     if (c->num_rows < 0) return fail(GDN_ERR_INVALID_ARGUMENT, "num_rows %lld is negative", (long long)c->num_rows);
+    if (c->num_rows > 0x7fffffffLL) return fail(GDN_ERR_UNSUPPORTED, "num_rows %lld exceeds the supported 2^31 - 1", (long long)c->num_rows);
     if (c->num_rows == 0) return GDN_OK;
     st = check_ptrs({{"cache k", c->k, 16}, {"cache v", c->v, 16}});
     if (st != GDN_OK || c->format == GDN_CACHE_PLAIN) return st;

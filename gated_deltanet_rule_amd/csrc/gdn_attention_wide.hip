@@ -23,12 +23,13 @@ constexpr int kThreads = 256, kWaves = 4, kTile = 64, kRows = 128;
 
 __device__ __forceinline__ f32x16_t mma32(bf16x8_t a, bf16x8_t b, f32x16_t acc) { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, acc, 0, 0, 0); }
 
-// One tile of K or V in LDS: rows of D bf16 values, 16-byte chunks exchanged by key, so that neither eight keys'
-// equal chunks (K's operands) nor four keys' neighbouring two (V's transposing loads) meet in a bank.
+// Tiles in LDS: rows of D bf16 values, their 16-byte chunks exchanged by key over the 16 that span all banks.  K's
+// operands take one chunk of 16 keys at a time, V's transposing loads four neighbouring chunks of four keys.
 template <int D>
 struct Tile {
     static constexpr int kRow = D * 2, kBytes = kTile * kRow;
-    __device__ static __forceinline__ int chunk(int key, int c) { return key * kRow + ((c ^ (D >= 128 ? (2 * key) & 15 : key & 6)) * 16); }
+    __device__ static __forceinline__ int k(int key, int c) { return key * kRow + ((c ^ (D >= 128 ? key & 15 : key >> 1 & 7)) * 16); }
+    __device__ static __forceinline__ int v(int key, int c) { return key * kRow + ((c ^ (D >= 128 ? 4 * key & 15 : 2 * key & 4)) * 16); }
 };
 
 // LDS of a workgroup: two tiles each of K and V; for each, the keys' factors (score, value) and whether a wave
@@ -50,7 +51,7 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
         fill_rows<__bf16, D>(k, u, kRows, kThreads, 0.f);
         return;
     }
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 31, half = lane >> 5, G = (int)k.group.d;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 31, half = lane >> 5, G = (int)k.group.d;
     const int H = k.a.cache.num_heads;
     const dev::Pages pages = {k.a.table + (int64_t)u.seq * k.a.table_width, k.a.table_width, k.block, k.a.cache.num_rows};
     float* const factors = reinterpret_cast<float*>(lds + Lds<D>::kTiles);
@@ -87,25 +88,23 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
     // ---- one tile ahead: the keys' rows, then what they hold
     const auto lookup = [&](int p0) {
         const int p = p0 + lane;
-        return p < u.hi ? pages.row(p) : (int64_t)-1;
+        return p < u.hi ? (int)pages.row(p) : -1;
     };
     u32x4_t kp[kPasses], vp[kPasses];
     float ks = 0.f, vs = 0.f;
-    const auto load = [&](int64_t row) {
+    const auto load = [&](int row) {
         const char* kc = static_cast<const char*>(k.a.cache.k) + threadIdx.x % kPerRow * 16 + (int64_t)u.h * kRowBytes;
         const char* vc = static_cast<const char*>(k.a.cache.v) + threadIdx.x % kPerRow * 16 + (int64_t)u.h * kRowBytes;
 #pragma unroll
         for (int i = 0; i < kPasses; ++i) {
-            const int from = i * kRowsAtOnce + threadIdx.x / kPerRow;
-            const int lo = __shfl((int)(uint64_t)row, from), hi = __shfl((int)((uint64_t)row >> 32), from);
-            int64_t at = (int64_t)((uint64_t)(unsigned)hi << 32 | (unsigned)lo);
-            at = (at < 0 ? 0 : at) * H * kRowBytes;
+            const int from = __shfl(row, i * kRowsAtOnce + threadIdx.x / kPerRow);
+            const uint64_t at = (uint64_t)(unsigned)(from < 0 ? 0 : from) * (unsigned)(H * kRowBytes);
             kp[i] = *reinterpret_cast<const u32x4_t*>(kc + at);
             vp[i] = *reinterpret_cast<const u32x4_t*>(vc + at);
         }
         if constexpr (kCodes) {
-            ks = row >= 0 ? k.a.cache.k_scale[row * H + u.h] : 0.f;
-            vs = row >= 0 ? k.a.cache.v_scale[row * H + u.h] : 0.f;
+            ks = row >= 0 ? k.a.cache.k_scale[(int64_t)row * H + u.h] : 0.f;
+            vs = row >= 0 ? k.a.cache.v_scale[(int64_t)row * H + u.h] : 0.f;
         }
     };
     // Into the tiles of `buf`.  Absent keys' values are zeros: their weights are, and nothing that is not finite may
@@ -121,22 +120,22 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
             if constexpr (kCodes) {
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    *reinterpret_cast<bf16x8_t*>(kt + Tile<D>::chunk(key, 2 * piece + x)) = dev::codes8<__bf16, FORMAT>(kp[i][2 * x], kp[i][2 * x + 1]);
+                    *reinterpret_cast<bf16x8_t*>(kt + Tile<D>::k(key, 2 * piece + x)) = dev::codes8<__bf16, FORMAT>(kp[i][2 * x], kp[i][2 * x + 1]);
                     bf16x8_t v = dev::codes8<__bf16, FORMAT>(vp[i][2 * x], vp[i][2 * x + 1]);
-                    if (!there) v = bf16x8_t{};
+                    if (present != ~0ull && !there) v = bf16x8_t{};
                     if (check)
 #pragma unroll
                         for (int j = 0; j < 8; ++j) fine &= dev::finite((float)v[j]);
-                    *reinterpret_cast<bf16x8_t*>(vt + Tile<D>::chunk(key, 2 * piece + x)) = v;
+                    *reinterpret_cast<bf16x8_t*>(vt + Tile<D>::v(key, 2 * piece + x)) = v;
                 }
             } else {
-                *reinterpret_cast<u32x4_t*>(kt + Tile<D>::chunk(key, piece)) = kp[i];
+                *reinterpret_cast<u32x4_t*>(kt + Tile<D>::k(key, piece)) = kp[i];
                 bf16x8_t v = __builtin_bit_cast(bf16x8_t, vp[i]);
-                if (!there) v = bf16x8_t{};
+                if (present != ~0ull && !there) v = bf16x8_t{};
                 if (check)
 #pragma unroll
                     for (int j = 0; j < 8; ++j) fine &= dev::finite((float)v[j]);
-                *reinterpret_cast<bf16x8_t*>(vt + Tile<D>::chunk(key, piece)) = v;
+                *reinterpret_cast<bf16x8_t*>(vt + Tile<D>::v(key, piece)) = v;
             }
         }
         if constexpr (kCodes) {
@@ -150,7 +149,7 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
         if (lane == 0) flags[buf * kWaves + wave] = bad;
     };
 
-    int64_t next_row = lookup(u.lo);
+    int next_row = lookup(u.lo);
     uint64_t present = __ballot(next_row >= 0);
     load(next_row);
     next_row = lookup(u.lo + kTile);
@@ -178,7 +177,7 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
             for (int x = 0; x < kSteps; ++x)
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                    const bf16x8_t kf = *reinterpret_cast<const bf16x8_t*>(kt + Tile<D>::chunk(32 * b + col, 2 * x + half));
+                    const bf16x8_t kf = *reinterpret_cast<const bf16x8_t*>(kt + Tile<D>::k(32 * b + col, 2 * x + half));
                     s[b] = mma32(kf, q[x], s[b]);
                 }
             if constexpr (kCodes)
@@ -209,7 +208,9 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
             dev::pair32(top, x, y);
             top = fmaxf(x, y);
             if constexpr (!kCodes) top *= c;
-            const float next = fmaxf(m, top);
+            // the maximum is kept until it is short by 2^8, which fp32 sums and bf16 weights take as well, so that the sums are
+            // seldom scaled; each row goes by its own
+            const float next = top > m + 8.f ? top : m;
             if (__any(next > m)) {
                 const float keep = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - next);
                 l *= keep;
@@ -235,7 +236,7 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             const int dim = 32 * d + 8 * (i / 4) + 4 * half + i % 4;
-                            float v = (float)*reinterpret_cast<const __bf16*>(vt + Tile<D>::chunk(key, dim / 8) + dim % 8 * 2);
+                            float v = (float)*reinterpret_cast<const __bf16*>(vt + Tile<D>::v(key, dim / 8) + dim % 8 * 2);
                             if (!dev::finite(by)) v = NAN;
                             if (!dev::finite(v) && (seen >> key & 1)) o[d][i] += v;
                         }
@@ -278,8 +279,8 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
             for (int d = 0; d < kDims; ++d)
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    const auto a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(vt + Tile<D>::chunk(16 * g + key, 4 * d + piece) + (lane & 1) * 8));
-                    const auto b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(vt + Tile<D>::chunk(16 * g + 8 + key, 4 * d + piece) + (lane & 1) * 8));
+                    const auto a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(vt + Tile<D>::v(16 * g + key, 4 * d + piece) + (lane & 1) * 8));
+                    const auto b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(vt + Tile<D>::v(16 * g + 8 + key, 4 * d + piece) + (lane & 1) * 8));
                     const dev::bf16x4_t x = __builtin_bit_cast(dev::bf16x4_t, a), y = __builtin_bit_cast(dev::bf16x4_t, b);
                     o[d] = mma32(__builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7), w[g], o[d]);
                 }

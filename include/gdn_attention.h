@@ -51,7 +51,7 @@ typedef enum { GDN_CACHE_PLAIN = 0, GDN_CACHE_E4M3 = 1, GDN_CACHE_INT8 = 2 } gdn
  * k_scale, v_scale device fp32 [num_rows, num_heads] (not read for GDN_CACHE_PLAIN).  Row
  * page * kv_block + i is token i of a page, as in gdn_step_plan's token_kv_slot.  dtype is that
  * of the activations.  head_dim is a multiple of 8 up to 512 (the attention: 64, 128 or 256),
- * num_heads * head_dim at most 2^20. */
+ * num_heads * head_dim at most 2^20, num_rows at most 2^31 - 1. */
 typedef struct {
     int32_t num_heads;
     int32_t head_dim;

@@ -59,6 +59,7 @@ def cache(heads=2, dim=64, dtype=1, form=1, rows=100, k=FAKE, v=FAKE, ks=FAKE, v
 CACHES = [(None, "cache is NULL", INVALID), (cache(heads=0), "num_heads 0", INVALID), (cache(dim=-8), "head_dim -8", INVALID),
           (cache(dim=60), "head_dim 60", UNSUPPORTED), (cache(dim=520), "head_dim 520", UNSUPPORTED), (cache(dtype=7), "dtype 7", UNSUPPORTED),
           (cache(form=3), "format 3", UNSUPPORTED), (cache(heads=1 << 15), "2^20", UNSUPPORTED), (cache(rows=-1), "num_rows -1", INVALID),
+          (cache(rows=1 << 31), "num_rows 2147483648", UNSUPPORTED),
           (cache(k=None), "cache k is NULL", INVALID), (cache(v=FAKE + 8), "cache v", INVALID), (cache(ks=None), "k_scale is NULL", INVALID),
           (cache(vs=FAKE + 2), "v_scale", INVALID)]
 
