@@ -23,29 +23,42 @@ constexpr int kThreads = 256, kWaves = 4, kTile = 64, kRows = 128;
 
 __device__ __forceinline__ f32x16_t mma32(bf16x8_t a, bf16x8_t b, f32x16_t acc) { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, acc, 0, 0, 0); }
 
-// Tiles in LDS: rows of D bf16 values, their 16-byte chunks exchanged by key over the 16 that span all banks.  K's
-// operands take one chunk of 16 keys at a time, V's transposing loads four neighbouring chunks of four keys.
+// Tiles of bf16 values in LDS: blocks of 16 keys by 32 dims, 1 KB each, which one load of a wave fills (16 bytes a
+// lane, in lanes' order).  K's operands take one 16-byte chunk of 16 keys at a time: a block of K holds chunk after
+// chunk.  V's transposing loads take 64 bytes of four keys at a time: a block of V holds key after key.  Neither
+// meets itself in a bank, and all of a tile's operands stand at fixed distances from a lane's first.
 template <int D>
 struct Tile {
-    static constexpr int kRow = D * 2, kBytes = kTile * kRow;
-    __device__ static __forceinline__ int k(int key, int c) { return key * kRow + ((c ^ (D >= 128 ? key & 15 : key >> 1 & 7)) * 16); }
-    __device__ static __forceinline__ int v(int key, int c) { return key * kRow + ((c ^ (D >= 128 ? 4 * key & 15 : 2 * key & 4)) * 16); }
+    static constexpr int kBytes = kTile * D * 2;
+    __device__ static constexpr int block(int key16, int dim32) { return (key16 * (D / 32) + dim32) * 1024; }
+    // chunk c (eight dims) of a key
+    __device__ static constexpr int k(int key, int c) { return block(key / 16, c / 4) + c % 4 * 256 + key % 16 * 16; }
+    __device__ static constexpr int v(int key, int c) { return block(key / 16, c / 4) + key % 16 * 64 + c % 4 * 16; }
 };
 
-// LDS of a workgroup: two tiles each of K and V; for each, the keys' factors (score, value) and whether a wave
-// met a value that is not finite where that matters.
+// 16 bytes a lane from memory into LDS, past the registers: lane l's to dst + 16 l.  In assembly, since the
+// compiler has every transposing load wait for such a load in flight, whatever tile it fills; landed() waits
+// for a wave's own, and a barrier behind that for all.  (m0 holds nothing between instructions: whatever needs it
+// sets it.)
+__device__ __forceinline__ void load_to_lds(const void* src, char* dst) {
+    const unsigned to = __builtin_amdgcn_readfirstlane((unsigned)(uintptr_t)(__attribute__((address_space(3))) char*)dst);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(to), "v"(src) : "memory");
+}
+__device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" : : : "memory"); }
+
+// LDS of a workgroup: two tiles each of K and V; for each, the keys' factors (score, value); whether a wave met a
+// value that is not finite where that matters.
 template <int D>
 struct Lds {
     static constexpr int kTiles = 4 * Tile<D>::kBytes;
     static constexpr int kFactors = 2 * 2 * kTile * 4;
-    static constexpr int kTotal = kTiles + kFactors + 2 * kWaves * 4;
+    static constexpr int kTotal = kTiles + kFactors + kWaves * 4;
 };
 
 template <int FORMAT, int D>
 __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit& u, char* lds) {
     constexpr bool kCodes = FORMAT != GDN_CACHE_PLAIN;
-    constexpr int kElem = kCodes ? 1 : 2, kRowBytes = D * kElem;
-    constexpr int kPerRow = kRowBytes / 16, kRowsAtOnce = kThreads / kPerRow, kPasses = kTile / kRowsAtOnce;
+    constexpr int kRowBytes = D * (kCodes ? 1 : 2), kPieces = kRowBytes / 64;      // 64 bytes of 16 keys to a load of a wave
     constexpr int kSteps = D / 16, kDims = D / 32;
     if (u.lo >= u.hi) {        // a table or a cache without rows: no address may be formed
         fill_rows<__bf16, D>(k, u, kRows, kThreads, 0.f);
@@ -85,75 +98,68 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
     f32x16_t o[kDims] = {};
     float m = -INFINITY, l = 0.f;
 
-    // ---- one tile ahead: the keys' rows, then what they hold
+    // ---- one tile ahead: the keys' rows, then what they hold.  A wave loads 16 of the tile's keys.
+    int entry = -1, key = 0;            // a lane's key two tiles ahead: its page's entry, in flight, and itself
     const auto lookup = [&](int p0) {
-        const int p = p0 + lane;
-        return p < u.hi ? (int)pages.row(p) : -1;
+        key = p0 + lane;
+        const unsigned page = dev::divide((unsigned)key, k.block);
+        entry = pages.table[page < (unsigned)pages.width ? page : (unsigned)pages.width - 1];
     };
-    u32x4_t kp[kPasses], vp[kPasses];
+    const auto row_of = [&]() {
+        const unsigned page = dev::divide((unsigned)key, k.block);
+        const int64_t row = (int64_t)entry * k.block.d + ((unsigned)key - page * k.block.d);
+        return key < u.hi && page < (unsigned)pages.width && entry >= 0 && row < pages.num_rows ? (int)row : -1;
+    };
+    u32x4_t kp[kCodes ? kPieces : 1], vp[kCodes ? kPieces : 1];
     float ks = 0.f, vs = 0.f;
-    const auto load = [&](int row) {
-        const char* kc = static_cast<const char*>(k.a.cache.k) + threadIdx.x % kPerRow * 16 + (int64_t)u.h * kRowBytes;
-        const char* vc = static_cast<const char*>(k.a.cache.v) + threadIdx.x % kPerRow * 16 + (int64_t)u.h * kRowBytes;
+    // Plain values go into `buf` directly, codes into registers.  An absent key's are those of row 0.
+    const auto load = [&](int row, int buf) {
+        const int krow = __shfl(row, 16 * wave + lane % 16), vrow = __shfl(row, 16 * wave + lane / 4);
+        const char* const kc = static_cast<const char*>(k.a.cache.k) + (int64_t)u.h * kRowBytes + lane / 16 * 16 + (uint64_t)(unsigned)(krow < 0 ? 0 : krow) * (unsigned)(H * kRowBytes);
+        const char* const vc = static_cast<const char*>(k.a.cache.v) + (int64_t)u.h * kRowBytes + lane % 4 * 16 + (uint64_t)(unsigned)(vrow < 0 ? 0 : vrow) * (unsigned)(H * kRowBytes);
 #pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
-            const int from = __shfl(row, i * kRowsAtOnce + threadIdx.x / kPerRow);
-            const uint64_t at = (uint64_t)(unsigned)(from < 0 ? 0 : from) * (unsigned)(H * kRowBytes);
-            kp[i] = *reinterpret_cast<const u32x4_t*>(kc + at);
-            vp[i] = *reinterpret_cast<const u32x4_t*>(vc + at);
+        for (int i = 0; i < kPieces; ++i) {
+            if constexpr (kCodes) {
+                kp[i] = *reinterpret_cast<const u32x4_t*>(kc + 64 * i);
+                vp[i] = *reinterpret_cast<const u32x4_t*>(vc + 64 * i);
+            } else {
+                char* const to = lds + buf * 2 * Tile<D>::kBytes + Tile<D>::block(wave, i);
+                load_to_lds(kc + 64 * i, to);
+                load_to_lds(vc + 64 * i, to + Tile<D>::kBytes);
+            }
         }
         if constexpr (kCodes) {
             ks = row >= 0 ? k.a.cache.k_scale[(int64_t)row * H + u.h] : 0.f;
             vs = row >= 0 ? k.a.cache.v_scale[(int64_t)row * H + u.h] : 0.f;
         }
     };
-    // Into the tiles of `buf`.  Absent keys' values are zeros: their weights are, and nothing that is not finite may
-    // meet those.  `check`: some rows do not see some of the tile's keys; whether a value of theirs is not finite.
-    const auto store = [&](int buf, uint64_t present, bool check) {
-        char* const kt = lds + buf * 2 * Tile<D>::kBytes;
-        char* const vt = kt + Tile<D>::kBytes;
-        bool fine = true;
+    // Codes as values into the tiles of `buf`.
+    const auto store = [&](int buf) {
+        if constexpr (kCodes) {
+            char* const kt = lds + buf * 2 * Tile<D>::kBytes;
+            char* const vt = kt + Tile<D>::kBytes;
 #pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
-            const int key = i * kRowsAtOnce + threadIdx.x / kPerRow, piece = threadIdx.x % kPerRow;
-            const bool there = present >> key & 1;
-            if constexpr (kCodes) {
+            for (int i = 0; i < kPieces; ++i)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    *reinterpret_cast<bf16x8_t*>(kt + Tile<D>::k(key, 2 * piece + x)) = dev::codes8<__bf16, FORMAT>(kp[i][2 * x], kp[i][2 * x + 1]);
-                    bf16x8_t v = dev::codes8<__bf16, FORMAT>(vp[i][2 * x], vp[i][2 * x + 1]);
-                    if (present != ~0ull && !there) v = bf16x8_t{};
-                    if (check)
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) fine &= dev::finite((float)v[j]);
-                    *reinterpret_cast<bf16x8_t*>(vt + Tile<D>::v(key, 2 * piece + x)) = v;
+                    const int kchunk = 2 * (4 * i + lane / 16) + x, vchunk = 2 * (4 * i + lane % 4) + x;
+                    *reinterpret_cast<bf16x8_t*>(kt + Tile<D>::k(16 * wave + lane % 16, kchunk)) = dev::codes8<__bf16, FORMAT>(kp[i][2 * x], kp[i][2 * x + 1]);
+                    *reinterpret_cast<bf16x8_t*>(vt + Tile<D>::v(16 * wave + lane / 4, vchunk)) = dev::codes8<__bf16, FORMAT>(vp[i][2 * x], vp[i][2 * x + 1]);
                 }
-            } else {
-                *reinterpret_cast<u32x4_t*>(kt + Tile<D>::k(key, piece)) = kp[i];
-                bf16x8_t v = __builtin_bit_cast(bf16x8_t, vp[i]);
-                if (present != ~0ull && !there) v = bf16x8_t{};
-                if (check)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) fine &= dev::finite((float)v[j]);
-                *reinterpret_cast<bf16x8_t*>(vt + Tile<D>::v(key, piece)) = v;
-            }
-        }
-        if constexpr (kCodes) {
-            if (check) fine &= dev::finite(vs);
             if (wave == 0) {
                 factors[buf * 2 * kTile + lane] = ks * c;
                 factors[buf * 2 * kTile + kTile + lane] = vs;
             }
         }
-        const bool bad = __any(!fine);
-        if (lane == 0) flags[buf * kWaves + wave] = bad;
     };
 
-    int next_row = lookup(u.lo);
-    uint64_t present = __ballot(next_row >= 0);
-    load(next_row);
-    next_row = lookup(u.lo + kTile);
-    store(0, present, present != ~0ull || u.lo + kTile > some);
+    lookup(u.lo);
+    int row = row_of();
+    uint64_t present = __ballot(row >= 0);
+    load(row, 0);
+    lookup(u.lo + kTile);
+    store(0);
+    if (!kCodes) landed();
     __syncthreads();
 
     int buf = 0;
@@ -161,13 +167,14 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
         const bool more = p0 + kTile < u.hi;
         const uint64_t now = present;
         if (more) {
-            present = __ballot(next_row >= 0);
-            load(next_row);
-            next_row = lookup(p0 + 2 * kTile);
+            row = row_of();
+            present = __ballot(row >= 0);
+            load(row, buf ^ 1);
+            lookup(p0 + 2 * kTile);
         }
-        const char* const kt = lds + buf * 2 * Tile<D>::kBytes;
-        const char* const vt = kt + Tile<D>::kBytes;
-        const float* const factor = factors + buf * 2 * kTile;
+        char* const kt = lds + buf * 2 * Tile<D>::kBytes;
+        char* const vt = kt + Tile<D>::kBytes;
+        float* const factor = factors + buf * 2 * kTile;
         const bool work = p0 < end;
         const bool partial = now != ~0ull || p0 + kTile > mine;
         f32x16_t s[2] = {};
@@ -221,41 +228,58 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
                 m = next;
             }
         }
-        // Values that are not finite, where some rows do not see them: added to the rows that do, zeros in the product.
-        int bad = 0;
+        // Where keys are absent, or some rows do not see some, no value that is not finite may meet a weight of zero:
+        // absent keys' values are zeroed; others are added to the rows that see them, and are zeros in the product.
+        if (now != ~0ull || p0 + kTile > some) {
+            constexpr int kChunks = kTile * D / 8;
+            bool fine = true;
+            for (int i = threadIdx.x; i < kChunks; i += kThreads) {
+                const int n = i / (D * 2) * 16 + i % 64 / 4;          // chunks as they lie
+                bf16x8_t* const at = reinterpret_cast<bf16x8_t*>(vt) + i;
+                if (now >> n & 1) {
+                    const bf16x8_t v = *at;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) bad |= flags[buf * kWaves + w];
-        if (bad) {
-            if (work) {
-                for (int key = 0; key < kTile; ++key) {
-                    if (!(now >> key & 1)) continue;
-                    float by = 1.f;
-                    if constexpr (kCodes) by = factor[kTile + key];
-#pragma unroll
-                    for (int d = 0; d < kDims; ++d)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const int dim = 32 * d + 8 * (i / 4) + 4 * half + i % 4;
-                            float v = (float)*reinterpret_cast<const __bf16*>(vt + Tile<D>::v(key, dim / 8) + dim % 8 * 2);
-                            if (!dev::finite(by)) v = NAN;
-                            if (!dev::finite(v) && (seen >> key & 1)) o[d][i] += v;
-                        }
+                    for (int j = 0; j < 8; ++j) fine &= dev::finite((float)v[j]);
+                } else {
+                    *at = bf16x8_t{};
                 }
             }
+            if (kCodes && threadIdx.x < kTile) fine &= dev::finite(factor[kTile + threadIdx.x]);
+            const bool wrong = __any(!fine);
+            if (lane == 0) flags[wave] = wrong;
             __syncthreads();
-            for (int i = threadIdx.x; i < kTile * D / 8; i += kThreads) {
-                bf16x8_t* const at = reinterpret_cast<bf16x8_t*>(lds + buf * 2 * Tile<D>::kBytes + Tile<D>::kBytes) + i;
-                bf16x8_t v = *at;
+            int bad = 0;
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (!dev::finite((float)v[j])) v[j] = (__bf16)0.f;
-                *at = v;
+            for (int w = 0; w < kWaves; ++w) bad |= flags[w];
+            if (bad) {
+                if (work) {
+                    for (int n = 0; n < kTile; ++n) {
+                        if (!(now >> n & 1)) continue;
+                        float by = 1.f;
+                        if constexpr (kCodes) by = factor[kTile + n];
+#pragma unroll
+                        for (int d = 0; d < kDims; ++d)
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const int dim = 32 * d + 8 * (i / 4) + 4 * half + i % 4;
+                                float v = (float)*reinterpret_cast<const __bf16*>(vt + Tile<D>::v(n, dim / 8) + dim % 8 * 2);
+                                if (!dev::finite(by)) v = NAN;
+                                if (!dev::finite(v) && (seen >> n & 1)) o[d][i] += v;
+                            }
+                    }
+                }
+                __syncthreads();
+                for (int i = threadIdx.x; i < kChunks; i += kThreads) {
+                    bf16x8_t* const at = reinterpret_cast<bf16x8_t*>(vt) + i;
+                    bf16x8_t v = *at;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (!dev::finite((float)v[j])) v[j] = (__bf16)0.f;
+                    *at = v;
+                }
+                if (kCodes && threadIdx.x < kTile && !dev::finite(factor[kTile + threadIdx.x])) factor[kTile + threadIdx.x] = 0.f;
+                __syncthreads();
             }
-            if (kCodes && threadIdx.x < kTile) {
-                float* const at = factors + buf * 2 * kTile + kTile + threadIdx.x;
-                if (!dev::finite(*at)) *at = 0.f;
-            }
-            __syncthreads();
         }
         if (work) {
             const float base = m == -INFINITY ? 0.f : m;
@@ -274,18 +298,19 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
                     }
                 }
             typedef __attribute__((address_space(3))) dev::s16x4_t* lds_ptr;
-            const int key = 4 * half + lane % 16 / 4, piece = 2 * (lane >> 4 & 1) + (lane >> 1 & 1);
+            const int vkey = 4 * half + lane % 16 / 4, piece = 2 * (lane >> 4 & 1) + (lane >> 1 & 1);
 #pragma unroll
             for (int d = 0; d < kDims; ++d)
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    const auto a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(vt + Tile<D>::v(16 * g + key, 4 * d + piece) + (lane & 1) * 8));
-                    const auto b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(vt + Tile<D>::v(16 * g + 8 + key, 4 * d + piece) + (lane & 1) * 8));
+                    const auto a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(vt + Tile<D>::v(16 * g + vkey, 4 * d + piece) + (lane & 1) * 8));
+                    const auto b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(vt + Tile<D>::v(16 * g + 8 + vkey, 4 * d + piece) + (lane & 1) * 8));
                     const dev::bf16x4_t x = __builtin_bit_cast(dev::bf16x4_t, a), y = __builtin_bit_cast(dev::bf16x4_t, b);
                     o[d] = mma32(__builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7), w[g], o[d]);
                 }
         }
-        if (more) store(buf ^ 1, present, present != ~0ull || p0 + 2 * kTile > some);
+        if (more) store(buf ^ 1);
+        if (!kCodes) landed();
         __syncthreads();
     }
 
