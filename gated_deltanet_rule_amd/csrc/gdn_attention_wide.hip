@@ -1,14 +1,20 @@
 // gdn_attention_wide.hip -- attention of many query rows over a paged cache for gfx950: bf16
 // prompts, and decode rows with large trees.
 //
-// The same sums as gdn_attention.hip, for rows enough to share the keys: four waves of 32 rows
-// take the same tile of 64 keys from LDS, two tiles of which stand there in turn: while one is
-// worked on, the next is loaded into registers and widened, if it holds codes, on its way into
-// the other.  The products are transposed here too, 32 x 32 tiles with a query row to each pair of
-// lanes, so that weights are the second product's operand as they come out of the first.
+// The same sums as gdn_attention.hip, for rows enough to share the keys: waves of 32 rows each take
+// the same tiles of 64 keys from LDS, where two of K and two of V stand in turn.  Plain values
+// go there past the registers, codes through them, widened.  The products are transposed here
+// too, 32 x 32 tiles with a query row to each pair of lanes, so that weights are the second
+// product's operand as they come out of the first.
+//
+// A tile is two phases to a wave: matrix products (the weights of the tile before times V, then K
+// times the queries) and the softmax, which keeps the vector ALU as long as the products keep the
+// matrix cores.  In a workgroup of eight waves the second four run one phase behind the first: each
+// SIMD holds a wave of either, and one's products run beside the other's softmax.
 #include <hip/hip_runtime.h>
 
 #include "gdn_attention_device.h"
+#include "gdn_device.h"
 #include "gdn_layer_internal.h"
 
 namespace gdn {
@@ -19,56 +25,70 @@ using dev::f32x4_t;
 using dev::f32x16_t;
 using dev::u32x4_t;
 
-constexpr int kThreads = 256, kWaves = 4, kTile = 64, kRows = 128;
+constexpr int kTile = 64;
 
 __device__ __forceinline__ f32x16_t mma32(bf16x8_t a, bf16x8_t b, f32x16_t acc) { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, acc, 0, 0, 0); }
 
-// Tiles of bf16 values in LDS: blocks of 16 keys by 32 dims, 1 KB each, which one load of a wave fills (16 bytes a
-// lane, in lanes' order).  K's operands take one 16-byte chunk of 16 keys at a time: a block of K holds chunk after
-// chunk.  V's transposing loads take 64 bytes of four keys at a time: a block of V holds key after key.  Neither
-// meets itself in a bank, and all of a tile's operands stand at fixed distances from a lane's first.
+template <typename V>
+using lds_ptr = __attribute__((address_space(3))) V*;
+typedef lds_ptr<char> lds_t;
+
+// Tiles of bf16 values in LDS: blocks of 8 keys by 64 dims, 1 KB each, which one load of a wave fills (16 bytes a lane,
+// in lanes' order) from 128 bytes of each key.  K's operands take one 16-byte chunk of 16 keys at a time: a block of K
+// holds chunk after chunk, pairs of chunks exchanged in every other block.  V's transposing loads take 64 bytes of
+// four keys at a time: a block of V holds key after key, their halves exchanged for every other pair of keys.  Neither
+// meets itself in a bank, and a tile's operands stand at fixed distances from a lane's first.
 template <int D>
 struct Tile {
     static constexpr int kBytes = kTile * D * 2;
-    __device__ static constexpr int block(int key16, int dim32) { return (key16 * (D / 32) + dim32) * 1024; }
+    __device__ static constexpr int block(int key8, int dim64) { return (key8 * (D / 64) + dim64) * 1024; }
     // chunk c (eight dims) of a key
-    __device__ static constexpr int k(int key, int c) { return block(key / 16, c / 4) + c % 4 * 256 + key % 16 * 16; }
-    __device__ static constexpr int v(int key, int c) { return block(key / 16, c / 4) + key % 16 * 64 + c % 4 * 16; }
+    __device__ static constexpr int k(int key, int c) { return block(key / 8, c / 8) + (c % 8 ^ (key / 8 & 1)) * 128 + key % 8 * 16; }
+    __device__ static constexpr int v(int key, int c) { return block(key / 8, c / 8) + key % 8 * 128 + (c % 8 ^ (2 * key & 4)) * 16; }
 };
 
 // 16 bytes a lane from memory into LDS, past the registers: lane l's to dst + 16 l.  In assembly, since the
 // compiler has every transposing load wait for such a load in flight, whatever tile it fills; landed() waits
 // for a wave's own, and a barrier behind that for all.  (m0 holds nothing between instructions: whatever needs it
 // sets it.)
-__device__ __forceinline__ void load_to_lds(const void* src, char* dst) {
-    const unsigned to = __builtin_amdgcn_readfirstlane((unsigned)(uintptr_t)(__attribute__((address_space(3))) char*)dst);
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(to), "v"(src) : "memory");
+__device__ __forceinline__ void load_to_lds(const void* src, lds_t dst) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"((unsigned)(uintptr_t)dst), "v"(src) : "memory");
 }
 __device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" : : : "memory"); }
 
-// LDS of a workgroup: two tiles each of K and V; for each, the keys' factors (score, value); whether a wave met a
-// value that is not finite where that matters.
-template <int D>
+// LDS of a workgroup: two tiles of K, two of V; for two tiles the keys' factors (scores, values, values as they are
+// stored); whether a wave met a value that is not finite where that matters.
+template <int D, int WAVES>
 struct Lds {
-    static constexpr int kTiles = 4 * Tile<D>::kBytes;
-    static constexpr int kFactors = 2 * 2 * kTile * 4;
-    static constexpr int kTotal = kTiles + kFactors + kWaves * 4;
+    static constexpr int kFactors = 4 * Tile<D>::kBytes;
+    static constexpr int kFlags = kFactors + 6 * kTile * 4;
+    static constexpr int kTotal = kFlags + WAVES * 4;
 };
 
-template <int FORMAT, int D>
-__device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit& u, char* lds) {
-    constexpr bool kCodes = FORMAT != GDN_CACHE_PLAIN;
-    constexpr int kRowBytes = D * (kCodes ? 1 : 2), kPieces = kRowBytes / 64;      // 64 bytes of 16 keys to a load of a wave
+template <int FORMAT, int D, int WAVES>
+__device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit& u, lds_t lds) {
+    constexpr bool kCodes = FORMAT != GDN_CACHE_PLAIN, kPair = WAVES == 8;
+    constexpr int kThreads = 64 * WAVES;
+    constexpr int kRowBytes = D * (kCodes ? 1 : 2);
+    // A load of a wave takes kRows keys of a tile, 128 bytes (or all) of each; a wave loads kGroups such groups of keys, or,
+    // where there are fewer groups than waves, the first four waves load K and the others V.
+    constexpr int kChunks = kRowBytes < 128 ? kRowBytes / 16 : 8, kRows = 64 / kChunks, kPieces = kRowBytes / (16 * kChunks);
+    constexpr bool kSplit = kTile / kRows < WAVES;
+    constexpr int kGroups = kSplit ? 1 : kTile / kRows / WAVES;
     constexpr int kSteps = D / 16, kDims = D / 32;
     if (u.lo >= u.hi) {        // a table or a cache without rows: no address may be formed
-        fill_rows<__bf16, D>(k, u, kRows, kThreads, 0.f);
+        fill_rows<__bf16, D>(k, u, 32 * WAVES, kThreads, 0.f);
         return;
     }
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 31, half = lane >> 5, G = (int)k.group.d;
     const int H = k.a.cache.num_heads;
     const dev::Pages pages = {k.a.table + (int64_t)u.seq * k.a.table_width, k.a.table_width, k.block, k.a.cache.num_rows};
-    float* const factors = reinterpret_cast<float*>(lds + Lds<D>::kTiles);
-    int* const flags = reinterpret_cast<int*>(lds + Lds<D>::kTiles + Lds<D>::kFactors);
+    const auto ktile = [&](int tile) { return lds + (tile & 1) * Tile<D>::kBytes; };
+    const auto vtile = [&](int tile) { return lds + (2 + (tile & 1)) * Tile<D>::kBytes; };
+    const auto kfactor = [&](int tile) { return (lds_ptr<float>)(lds + Lds<D, WAVES>::kFactors) + (tile & 1) * kTile; };
+    const auto vfactor = [&](int tile) { return (lds_ptr<float>)(lds + Lds<D, WAVES>::kFactors) + (2 + (tile & 1)) * kTile; };
+    const auto vstored = [&](int tile) { return (lds_ptr<float>)(lds + Lds<D, WAVES>::kFactors) + (4 + (tile & 1)) * kTile; };
+    const lds_ptr<int> flags = (lds_ptr<int>)(lds + Lds<D, WAVES>::kFlags);
     // the scale's sign goes into the queries (exactly), so that the largest product is the largest score
     const float c = k.a.scale == 0.f ? 1.f : fabsf(k.a.scale) * kLog2e, sign = k.a.scale == 0.f ? 0.f : copysignf(1.f, k.a.scale);
 
@@ -95,13 +115,17 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
     const int mine = tree ? u.past : u.past + (int)dev::divide(first_row, k.group) + 1;
     const int end = !busy ? 0 : (tree ? u.hi : u.past + (int)dev::divide(last_row, k.group) + 1);
 
+    const bool behind = kPair && wave >= 4;       // one phase behind the others
+    const int tiles = (u.hi - u.lo + kTile - 1) / kTile;
+
     f32x16_t o[kDims] = {};
     float m = -INFINITY, l = 0.f;
 
-    // ---- one tile ahead: the keys' rows, then what they hold.  A wave loads 16 of the tile's keys.
-    int entry = -1, key = 0;            // a lane's key two tiles ahead: its page's entry, in flight, and itself
-    const auto lookup = [&](int p0) {
-        key = p0 + lane;
+    // ---- loads: a lane's key and its page's entry (in flight) two tiles ahead, then the rows, K one tile ahead, V of the tile
+    // itself.  A wave loads 16 of the tile's keys (with eight waves, half of their dims).
+    int entry = -1, key = 0;
+    const auto lookup = [&](int tile) {
+        key = u.lo + tile * kTile + lane;
         const unsigned page = dev::divide((unsigned)key, k.block);
         entry = pages.table[page < (unsigned)pages.width ? page : (unsigned)pages.width - 1];
     };
@@ -110,209 +134,274 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
         const int64_t row = (int64_t)entry * k.block.d + ((unsigned)key - page * k.block.d);
         return key < u.hi && page < (unsigned)pages.width && entry >= 0 && row < pages.num_rows ? (int)row : -1;
     };
-    u32x4_t kp[kCodes ? kPieces : 1], vp[kCodes ? kPieces : 1];
+    const bool loads_k = !kSplit || wave < WAVES / 2, loads_v = !kSplit || wave >= WAVES / 2;
+    const int group0 = kSplit ? wave % (WAVES / 2) : wave * kGroups;
+    u32x4_t kp[kGroups][kPieces], vp[kGroups][kPieces];
     float ks = 0.f, vs = 0.f;
-    // Plain values go into `buf` directly, codes into registers.  An absent key's are those of row 0.
-    const auto load = [&](int row, int buf) {
-        const int krow = __shfl(row, 16 * wave + lane % 16), vrow = __shfl(row, 16 * wave + lane / 4);
-        const char* const kc = static_cast<const char*>(k.a.cache.k) + (int64_t)u.h * kRowBytes + lane / 16 * 16 + (uint64_t)(unsigned)(krow < 0 ? 0 : krow) * (unsigned)(H * kRowBytes);
-        const char* const vc = static_cast<const char*>(k.a.cache.v) + (int64_t)u.h * kRowBytes + lane % 4 * 16 + (uint64_t)(unsigned)(vrow < 0 ? 0 : vrow) * (unsigned)(H * kRowBytes);
+    // Chunk `chunk` of a key's row in the cache; an absent key's values are those of row 0.
+    const auto address = [&](const void* cache, int row, int chunk) {
+        return static_cast<const char*>(cache) + (int64_t)u.h * kRowBytes + chunk * 16 + (uint64_t)(unsigned)(row < 0 ? 0 : row) * (unsigned)(H * kRowBytes);
+    };
+    const auto load_k = [&](int tile, int row) {
+        if (!loads_k) return;
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-            if constexpr (kCodes) {
-                kp[i] = *reinterpret_cast<const u32x4_t*>(kc + 64 * i);
-                vp[i] = *reinterpret_cast<const u32x4_t*>(vc + 64 * i);
-            } else {
-                char* const to = lds + buf * 2 * Tile<D>::kBytes + Tile<D>::block(wave, i);
-                load_to_lds(kc + 64 * i, to);
-                load_to_lds(vc + 64 * i, to + Tile<D>::kBytes);
+        for (int g = 0; g < kGroups; ++g) {
+            const int group = group0 + g, at = lane / kRows;      // (where codes are, chunks stay in order)
+            const char* const from = address(k.a.cache.k, __shfl(row, group * kRows + lane % kRows), kCodes ? at : at ^ (group & 1));
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                if constexpr (kCodes) kp[g][i] = *reinterpret_cast<const u32x4_t*>(from + 128 * i);
+                else load_to_lds(from + 128 * i, ktile(tile) + Tile<D>::block(group, i));
             }
         }
-        if constexpr (kCodes) {
-            ks = row >= 0 ? k.a.cache.k_scale[(int64_t)row * H + u.h] : 0.f;
-            vs = row >= 0 ? k.a.cache.v_scale[(int64_t)row * H + u.h] : 0.f;
-        }
-    };
-    // Codes as values into the tiles of `buf`.
-    const auto store = [&](int buf) {
-        if constexpr (kCodes) {
-            char* const kt = lds + buf * 2 * Tile<D>::kBytes;
-            char* const vt = kt + Tile<D>::kBytes;
-#pragma unroll
-            for (int i = 0; i < kPieces; ++i)
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const int kchunk = 2 * (4 * i + lane / 16) + x, vchunk = 2 * (4 * i + lane % 4) + x;
-                    *reinterpret_cast<bf16x8_t*>(kt + Tile<D>::k(16 * wave + lane % 16, kchunk)) = dev::codes8<__bf16, FORMAT>(kp[i][2 * x], kp[i][2 * x + 1]);
-                    *reinterpret_cast<bf16x8_t*>(vt + Tile<D>::v(16 * wave + lane / 4, vchunk)) = dev::codes8<__bf16, FORMAT>(vp[i][2 * x], vp[i][2 * x + 1]);
-                }
+        if constexpr (kCodes)
             if (wave == 0) {
-                factors[buf * 2 * kTile + lane] = ks * c;
-                factors[buf * 2 * kTile + kTile + lane] = vs;
+                ks = row >= 0 ? k.a.cache.k_scale[(int64_t)row * H + u.h] : 0.f;
+                vs = row >= 0 ? k.a.cache.v_scale[(int64_t)row * H + u.h] : 0.f;
+            }
+    };
+    const auto load_v = [&](int tile, int row) {
+        if (!loads_v) return;
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+            const int group = group0 + g, at = lane % kChunks;
+            const char* const from = address(k.a.cache.v, __shfl(row, group * kRows + lane / kChunks), kCodes ? at : at ^ (lane / kChunks * 2 & 4));
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                if constexpr (kCodes) vp[g][i] = *reinterpret_cast<const u32x4_t*>(from + 128 * i);
+                else load_to_lds(from + 128 * i, vtile(tile) + Tile<D>::block(group, i));
             }
         }
     };
+    // Whether keys of a tile are absent, or some rows of the workgroup do not see some.
+    const auto special = [&](int tile, uint64_t there) { return there != ~0ull || u.lo + (tile + 1) * kTile > some; };
+    // What was loaded, in LDS: codes as values.
+    const auto land_k = [&](int tile, uint64_t there) {
+        if constexpr (kCodes) {
+            if (!loads_k) return;
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+                        *(lds_ptr<bf16x8_t>)(ktile(tile) + Tile<D>::k((group0 + g) * kRows + lane % kRows, 16 * i + 2 * (lane / kRows) + x)) =
+                            dev::codes8<__bf16, FORMAT>(kp[g][i][2 * x], kp[g][i][2 * x + 1]);
+            if (wave == 0) {
+                kfactor(tile)[lane] = ks * c;
+                vfactor(tile)[lane] = special(tile, there) && !dev::finite(vs) ? 0.f : vs;
+                vstored(tile)[lane] = vs;
+            }
+        }
+    };
+    const auto land_v = [&](int tile) {
+        if constexpr (kCodes) {
+            if (!loads_v) return;
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+                        *(lds_ptr<bf16x8_t>)(vtile(tile) + Tile<D>::v((group0 + g) * kRows + lane / kChunks, 16 * i + 2 * (lane % kChunks) + x)) =
+                            dev::codes8<__bf16, FORMAT>(vp[g][i][2 * x], vp[g][i][2 * x + 1]);
+        }
+    };
+    int row;                        // the lane's key of tile `t` after issue(t) began: of tile t + 1 when it is done
+    uint64_t present, ahead;        // which keys of tile t, and t + 1, are there
+    const auto issue = [&](int tile) {
+        // the entry first: what waits for it waits for every load before it
+        const int next = tile + 1 < tiles ? row_of() : -1;
+        present = ahead;
+        ahead = __ballot(next >= 0);
+        load_v(tile, row);
+        if (tile + 1 < tiles) {
+            load_k(tile + 1, next);
+            lookup(tile + 2);
+        }
+        row = next;
+    };
+    const auto land = [&](int tile) {
+        land_v(tile);
+        if (tile + 1 < tiles) land_k(tile + 1, ahead);
+        if (!kCodes) landed();
+    };
 
-    lookup(u.lo);
-    int row = row_of();
-    uint64_t present = __ballot(row >= 0);
-    load(row, 0);
-    lookup(u.lo + kTile);
-    store(0);
-    if (!kCodes) landed();
-    __syncthreads();
-
-    int buf = 0;
-    for (int p0 = u.lo; p0 < u.hi; p0 += kTile, buf ^= 1) {
-        const bool more = p0 + kTile < u.hi;
-        const uint64_t now = present;
-        if (more) {
-            row = row_of();
-            present = __ballot(row >= 0);
-            load(row, buf ^ 1);
-            lookup(p0 + 2 * kTile);
-        }
-        char* const kt = lds + buf * 2 * Tile<D>::kBytes;
-        char* const vt = kt + Tile<D>::kBytes;
-        float* const factor = factors + buf * 2 * kTile;
-        const bool work = p0 < end;
-        const bool partial = now != ~0ull || p0 + kTile > mine;
-        f32x16_t s[2] = {};
-        uint64_t seen = ~0ull;
-        if (work) {
+    // ---- the phases of a tile
+    f32x16_t s[2];
+    bf16x8_t w[4];
+    const auto scores = [&](int tile) {
+        // chunk 2 x + half of key 32 b + col: fixed distances from the lane's first
+        const lds_t kt = ktile(tile) + Tile<D>::k(col, half);
+        s[0] = f32x16_t{};
+        s[1] = f32x16_t{};
 #pragma unroll
-            for (int x = 0; x < kSteps; ++x)
+        for (int x = 0; x < kSteps; ++x)
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const bf16x8_t kf = *reinterpret_cast<const bf16x8_t*>(kt + Tile<D>::k(32 * b + col, 2 * x + half));
-                    s[b] = mma32(kf, q[x], s[b]);
-                }
-            if constexpr (kCodes)
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const f32x4_t by = *reinterpret_cast<const f32x4_t*>(factor + 32 * b + 8 * i + 4 * half);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) s[b][4 * i + j] *= by[j];
-                    }
-            if (partial) {
-                seen = sees.from(p0) & now;
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const unsigned bits = (unsigned)(seen >> (32 * b)) >> (4 * half);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (!(bits >> (8 * (i / 4) + i % 4) & 1)) s[b][i] = -INFINITY;
-                }
-            }
-            float top = -INFINITY;
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
-            float x, y;
-            dev::pair32(top, x, y);
-            top = fmaxf(x, y);
-            if constexpr (!kCodes) top *= c;
-            // the maximum is kept until it is short by 2^8, which fp32 sums and bf16 weights take as well, so that the sums are
-            // seldom scaled; each row goes by its own
-            const float next = top > m + 8.f ? top : m;
-            if (__any(next > m)) {
-                const float keep = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - next);
-                l *= keep;
-#pragma unroll
-                for (int d = 0; d < kDims; ++d)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) o[d][i] *= keep;
-                m = next;
-            }
-        }
-        // Where keys are absent, or some rows do not see some, no value that is not finite may meet a weight of zero:
-        // absent keys' values are zeroed; others are added to the rows that see them, and are zeros in the product.
-        if (now != ~0ull || p0 + kTile > some) {
-            constexpr int kChunks = kTile * D / 8;
-            bool fine = true;
-            for (int i = threadIdx.x; i < kChunks; i += kThreads) {
-                const int n = i / (D * 2) * 16 + i % 64 / 4;          // chunks as they lie
-                bf16x8_t* const at = reinterpret_cast<bf16x8_t*>(vt) + i;
-                if (now >> n & 1) {
-                    const bf16x8_t v = *at;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) fine &= dev::finite((float)v[j]);
-                } else {
-                    *at = bf16x8_t{};
-                }
-            }
-            if (kCodes && threadIdx.x < kTile) fine &= dev::finite(factor[kTile + threadIdx.x]);
-            const bool wrong = __any(!fine);
-            if (lane == 0) flags[wave] = wrong;
-            __syncthreads();
-            int bad = 0;
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w) bad |= flags[w];
-            if (bad) {
-                if (work) {
-                    for (int n = 0; n < kTile; ++n) {
-                        if (!(now >> n & 1)) continue;
-                        float by = 1.f;
-                        if constexpr (kCodes) by = factor[kTile + n];
-#pragma unroll
-                        for (int d = 0; d < kDims; ++d)
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const int dim = 32 * d + 8 * (i / 4) + 4 * half + i % 4;
-                                float v = (float)*reinterpret_cast<const __bf16*>(vt + Tile<D>::v(n, dim / 8) + dim % 8 * 2);
-                                if (!dev::finite(by)) v = NAN;
-                                if (!dev::finite(v) && (seen >> n & 1)) o[d][i] += v;
-                            }
-                    }
-                }
-                __syncthreads();
-                for (int i = threadIdx.x; i < kChunks; i += kThreads) {
-                    bf16x8_t* const at = reinterpret_cast<bf16x8_t*>(vt) + i;
-                    bf16x8_t v = *at;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (!dev::finite((float)v[j])) v[j] = (__bf16)0.f;
-                    *at = v;
-                }
-                if (kCodes && threadIdx.x < kTile && !dev::finite(factor[kTile + threadIdx.x])) factor[kTile + threadIdx.x] = 0.f;
-                __syncthreads();
-            }
-        }
-        if (work) {
-            const float base = m == -INFINITY ? 0.f : m;
-            bf16x8_t w[4];
+            for (int b = 0; b < 2; ++b) s[b] = mma32(*(lds_ptr<bf16x8_t>)(kt + Tile<D>::k(32 * b, 2 * x)), q[x], s[b]);
+    };
+    const auto softmax = [&](int tile, uint64_t now) {
+        const int p0 = u.lo + tile * kTile;
+        if constexpr (kCodes)
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    f32x4_t by = {1.f, 1.f, 1.f, 1.f};
-                    if constexpr (kCodes) by = *reinterpret_cast<const f32x4_t*>(factor + kTile + 32 * b + 8 * i + 4 * half);
+                    const f32x4_t by = *(lds_ptr<f32x4_t>)(kfactor(tile) + 32 * b + 8 * i + 4 * half);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float x = __builtin_amdgcn_exp2f(kCodes ? s[b][4 * i + j] - base : fmaf(s[b][4 * i + j], c, -base));
-                        l += x;
-                        w[2 * b + i / 2][4 * (i & 1) + j] = (__bf16)(x * by[j]);
-                    }
+                    for (int j = 0; j < 4; ++j) s[b][4 * i + j] *= by[j];
                 }
-            typedef __attribute__((address_space(3))) dev::s16x4_t* lds_ptr;
-            const int vkey = 4 * half + lane % 16 / 4, piece = 2 * (lane >> 4 & 1) + (lane >> 1 & 1);
+        if (now != ~0ull || p0 + kTile > mine) {
+            const uint64_t seen = sees.from(p0) & now;
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const unsigned bits = (unsigned)(seen >> (32 * b)) >> (4 * half);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (!(bits >> (8 * (i / 4) + i % 4) & 1)) s[b][i] = -INFINITY;
+            }
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
+        float x, y;
+        dev::pair32(top, x, y);
+        top = fmaxf(x, y);
+        if constexpr (!kCodes) top *= c;
+        // the maximum is kept until it is short by 2^8, which fp32 sums and bf16 weights take as well, so that the sums are
+        // seldom scaled; each row goes by its own
+        const float next = top > m + 8.f ? top : m;
+        if (__any(next > m)) {
+            const float keep = m == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - next);      // (no sums yet)
+            l *= keep;
 #pragma unroll
             for (int d = 0; d < kDims; ++d)
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const auto a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(vt + Tile<D>::v(16 * g + vkey, 4 * d + piece) + (lane & 1) * 8));
-                    const auto b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(vt + Tile<D>::v(16 * g + 8 + vkey, 4 * d + piece) + (lane & 1) * 8));
-                    const dev::bf16x4_t x = __builtin_bit_cast(dev::bf16x4_t, a), y = __builtin_bit_cast(dev::bf16x4_t, b);
-                    o[d] = mma32(__builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7), w[g], o[d]);
-                }
+                for (int i = 0; i < 16; ++i) o[d][i] *= keep;
+            m = next;
         }
-        if (more) store(buf ^ 1);
-        if (!kCodes) landed();
-        __syncthreads();
+        const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f32x4_t by = {1.f, 1.f, 1.f, 1.f};
+                if constexpr (kCodes) by = *(lds_ptr<f32x4_t>)(vfactor(tile) + 32 * b + 8 * i + 4 * half);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float e = __builtin_amdgcn_exp2f(kCodes ? s[b][4 * i + j] - base : fmaf(s[b][4 * i + j], c, -base));
+                    l += e;
+                    w[2 * b + i / 2][4 * (i & 1) + j] = (__bf16)(e * by[j]);
+                }
+            }
+    };
+    const auto sums = [&](int tile) {
+        // chunk 4 d + piece of four keys: fixed distances too, from one first for the even d and one for the odd
+        const int vkey = 4 * half + lane % 16 / 4, piece = 2 * (lane >> 4 & 1) + (lane >> 1 & 1);
+        const lds_t vt[2] = {vtile(tile) + Tile<D>::v(vkey, piece) + (lane & 1) * 8, vtile(tile) + Tile<D>::v(vkey, 4 + piece) + (lane & 1) * 8};
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int d = 0; d < kDims; ++d) {
+                const auto a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr<dev::s16x4_t>)(vt[d & 1] + Tile<D>::block(2 * g, d / 2)));
+                const auto b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr<dev::s16x4_t>)(vt[d & 1] + Tile<D>::block(2 * g + 1, d / 2)));
+                const dev::bf16x4_t x = __builtin_bit_cast(dev::bf16x4_t, a), y = __builtin_bit_cast(dev::bf16x4_t, b);
+                o[d] = mma32(__builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7), w[g], o[d]);
+            }
+    };
+    // Where keys are absent, or some rows do not see some, no value that is not finite may meet a weight of zero: absent
+    // keys' values are zeroed; others are added to the rows that see them, and are zeros in the product.  All waves
+    // come here together, between the landing of the tile's V and its sums.
+    const auto mend = [&](int tile, uint64_t now) {
+        const int p0 = u.lo + tile * kTile;
+        if (!special(tile, now)) return;
+        constexpr int kAll = kTile * D / 8;
+        const lds_t vt = vtile(tile);
+        bool fine = true;
+        for (int i = threadIdx.x; i < kAll; i += kThreads) {
+            const int n = i / D * 8 + i % 64 / 8;                 // chunks as they lie: D to eight keys
+            const lds_ptr<bf16x8_t> at = (lds_ptr<bf16x8_t>)vt + i;
+            if (now >> n & 1) {
+                const bf16x8_t v = *at;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) fine &= dev::finite((float)v[j]);
+            } else {
+                *at = bf16x8_t{};
+            }
+        }
+        if (kCodes && threadIdx.x < kTile) fine &= dev::finite(vstored(tile)[threadIdx.x]);
+        const bool wrong = __any(!fine);
+        if (lane == 0) flags[wave] = wrong;
+        dev::lds_barrier();
+        int bad = 0;
+#pragma unroll
+        for (int i = 0; i < WAVES; ++i) bad |= flags[i];
+        if (bad) {
+            if (p0 < end) {
+                const uint64_t seen = sees.from(p0) & now;
+                for (int n = 0; n < kTile; ++n) {
+                    if (!(now >> n & 1)) continue;
+                    float by = 1.f;
+                    if constexpr (kCodes) by = vstored(tile)[n];
+#pragma unroll
+                    for (int d = 0; d < kDims; ++d)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const int dim = 32 * d + 8 * (i / 4) + 4 * half + i % 4;
+                            float v = (float)*(lds_ptr<__bf16>)(vt + Tile<D>::v(n, dim / 8) + dim % 8 * 2);
+                            if (!dev::finite(by)) v = NAN;
+                            if (!dev::finite(v) && (seen >> n & 1)) o[d][i] += v;
+                        }
+                }
+            }
+            dev::lds_barrier();
+            for (int i = threadIdx.x; i < kAll; i += kThreads) {
+                const lds_ptr<bf16x8_t> at = (lds_ptr<bf16x8_t>)vt + i;
+                bf16x8_t v = *at;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (!dev::finite((float)v[j])) v[j] = (__bf16)0.f;
+                *at = v;
+            }
+        }
+        dev::lds_barrier();
+    };
+
+    // ---- slot 2 t: issue(t), the first waves' products of tile t (their sums of t - 1); slot 2 t + 1: their softmax, and what was
+    // issued lands.  The waves behind do the same one slot later, and issue and land in the same slots as the first.  A tile's
+    // buffers are free when it is issued: K of t - 1 and V of t - 2 were last read in slot 2 t - 1.
+    lookup(0);
+    row = row_of();
+    ahead = __ballot(row >= 0);
+    load_k(0, row);
+    lookup(1);
+    land_k(0, ahead);
+    if (!kCodes) landed();
+    dev::lds_barrier();
+    if (behind) {
+        issue(0);
+        dev::lds_barrier();
     }
+    for (int t = 0; t < tiles; ++t) {
+        const bool work = u.lo + t * kTile < end;
+        if (!behind) issue(t);
+        const uint64_t now = present;
+        if (t > 0 && u.lo + (t - 1) * kTile < end) sums(t - 1);
+        if (work) scores(t);
+        if (behind) land(t);
+        if (kPair) dev::lds_barrier();
+        if (behind) {
+            mend(t, now);
+            if (t + 1 < tiles) issue(t + 1);
+        }
+        if (work) softmax(t, now);
+        if (!behind) land(t);
+        if (!behind || t + 1 < tiles) dev::lds_barrier();
+        if (!behind) mend(t, now);
+    }
+    if (u.lo + (tiles - 1) * kTile < end) sums(tiles - 1);
 
     float x, y;
     dev::pair32(l, x, y);
@@ -341,33 +430,42 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
         }
 }
 
-template <int FORMAT, int D>
-__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void wide_decode_kernel(AttentionKernelArgs k) {
+// Eight waves of 256 registers, or four of 512: a head of 256 dims has sums of 128 registers a wave.
+template <int FORMAT, int D, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void wide_decode_kernel(AttentionKernelArgs k) {
     extern __shared__ __align__(16) char lds[];
     Unit u;
-    if (decode_unit<__bf16, D>(k, kRows, kThreads, u)) attend<FORMAT, D>(k, u, lds);
+    if (decode_unit<__bf16, D>(k, 32 * WAVES, 64 * WAVES, u)) attend<FORMAT, D, WAVES>(k, u, (lds_t)lds);
 }
 
 // Tiles from the last to the first: those with the most keys start first.
-template <int FORMAT, int D>
-__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void wide_prompt_kernel(AttentionKernelArgs k) {
+template <int FORMAT, int D, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, D == 256 ? 1 : 2) void wide_prompt_kernel(AttentionKernelArgs k) {
     extern __shared__ __align__(16) char lds[];
     const unsigned H = (unsigned)k.a.cache.num_heads, at = blockIdx.x / H;
     Unit u;
-    if (prompt_unit(k, kRows, k.row_tiles - 1 - (int)at, (int)(blockIdx.x - at * H), u)) attend<FORMAT, D>(k, u, lds);
+    if (prompt_unit(k, 32 * WAVES, k.row_tiles - 1 - (int)at, (int)(blockIdx.x - at * H), u)) attend<FORMAT, D, WAVES>(k, u, (lds_t)lds);
 }
 
-template <int FORMAT, int D>
+template <int FORMAT, int D, int WAVES>
 hipError_t launch(AttentionKernelArgs k, hipStream_t stream) {
+    constexpr int kThreads = 64 * WAVES, kRows = 32 * WAVES;
     const int H = k.a.cache.num_heads;
     const bool decode = k.a.tokens_per_row > 0;
     const int64_t tiles = decode ? (k.a.tokens_per_row * (int)k.group.d + kRows - 1) / kRows : k.a.total_tokens * (int)k.group.d / kRows + k.a.num_seqs;
     const int64_t units = decode ? ((int64_t)k.a.num_seqs * k.spans * H + 7) / 8 * 8 : H;
     if (!grid_fits(tiles * units, kThreads) || k.a.total_tokens * (int64_t)k.group.d > 0x7fffffffLL) return hipErrorInvalidConfiguration;
     k.row_tiles = (int)tiles;
-    auto* const kernel = decode ? wide_decode_kernel<FORMAT, D> : wide_prompt_kernel<FORMAT, D>;
-    kernel<<<(unsigned)(tiles * units), kThreads, Lds<D>::kTotal, stream>>>(k);
+    auto* const kernel = decode ? wide_decode_kernel<FORMAT, D, WAVES> : wide_prompt_kernel<FORMAT, D, WAVES>;
+    kernel<<<(unsigned)(tiles * units), kThreads, Lds<D, WAVES>::kTotal, stream>>>(k);
     return hipGetLastError();
+}
+
+template <int FORMAT, int D>
+hipError_t launch(const AttentionKernelArgs& k, hipStream_t stream) {
+    if constexpr (D < 256)
+        if (k.a.tokens_per_row == 0 || k.a.tokens_per_row * (int)k.group.d > 128) return launch<FORMAT, D, 8>(k, stream);
+    return launch<FORMAT, D, 4>(k, stream);
 }
 
 template <int FORMAT>
