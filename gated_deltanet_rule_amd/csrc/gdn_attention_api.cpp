@@ -90,9 +90,10 @@ gdn_status check_table(int32_t width, int32_t kv_block) {
     return GDN_OK;
 }
 
+// Keys that a table holds.  The kernels look up to 512 positions past the last key.
 int table_capacity(int32_t width, int32_t kv_block) {
-    const int64_t keys = (int64_t)width * kv_block;
-    return (int)(keys < kMaxTokens ? keys : kMaxTokens);
+    const int64_t keys = (int64_t)width * kv_block, most = 0x7fffffffLL - 1024;
+    return (int)(keys < most ? keys : most);
 }
 
 gdn::AttentionArgs attention_args(const gdn_kv_cache* cache, int32_t num_q_heads, float scale, int32_t num_seqs, int64_t total_tokens,

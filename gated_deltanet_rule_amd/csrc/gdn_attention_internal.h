@@ -61,7 +61,7 @@ struct AttentionArgs {
     int64_t q_stride;
     const int32_t* table;
     int table_width, kv_block;
-    int capacity;           // keys that the table holds, at most 2^31 - 129
+    int capacity;           // keys that the table holds, at most 2^31 - 1025
     int max_keys;           // decode: the launch's bound, at most capacity
     void* o;
     void* workspace;

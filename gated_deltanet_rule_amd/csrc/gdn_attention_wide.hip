@@ -2,10 +2,15 @@
 // prompts, and decode rows with large trees.
 //
 // The same sums as gdn_attention.hip, for rows enough to share the keys: waves of 32 rows each take
-// the same tiles of 64 keys from LDS, where two of K and two of V stand in turn.  Plain values
-// go there past the registers, codes through them, widened.  The products are transposed here
-// too, 32 x 32 tiles with a query row to each pair of lanes, so that weights are the second
-// product's operand as they come out of the first.
+// the same tiles of keys from LDS.  The products are transposed here too, 32 x 32 tiles with a
+// query row to each pair of lanes, so that weights are the second product's operand as they
+// come out of the first.
+//
+// Everything comes from memory into LDS past the registers, three tiles ahead: the pages' entries, then K
+// and V.  That is what it takes: the waves of all workgroups that share keys run along them together, so
+// every tile is new to the cache when the first of them asks for it, and a tile is worked off in less
+// time than memory takes to answer.  Codes wait in LDS as they are stored, each wave's own, and become
+// bf16 tiles just before they are needed.
 //
 // A tile is two phases to a wave: matrix products (the weights of the tile before times V, then K
 // times the queries) and the softmax, which keeps the vector ALU as long as the products keep the
@@ -25,7 +30,9 @@ using dev::f32x4_t;
 using dev::f32x16_t;
 using dev::u32x4_t;
 
-constexpr int kTile = 64;
+// Keys of a tile: where LDS has to hold two workgroups, or heads of 256 dims, half of them.
+template <int WAVES>
+constexpr int kKeys = WAVES == 8 ? 64 : 32;
 
 __device__ __forceinline__ f32x16_t mma32(bf16x8_t a, bf16x8_t b, f32x16_t acc) { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, acc, 0, 0, 0); }
 
@@ -40,55 +47,72 @@ typedef lds_ptr<char> lds_t;
 // meets itself in a bank, and a tile's operands stand at fixed distances from a lane's first.
 template <int D>
 struct Tile {
-    static constexpr int kBytes = kTile * D * 2;
     __device__ static constexpr int block(int key8, int dim64) { return (key8 * (D / 64) + dim64) * 1024; }
     // chunk c (eight dims) of a key
     __device__ static constexpr int k(int key, int c) { return block(key / 8, c / 8) + (c % 8 ^ (key / 8 & 1)) * 128 + key % 8 * 16; }
     __device__ static constexpr int v(int key, int c) { return block(key / 8, c / 8) + key % 8 * 128 + (c % 8 ^ (2 * key & 4)) * 16; }
 };
 
-// 16 bytes a lane from memory into LDS, past the registers: lane l's to dst + 16 l.  In assembly, since the
-// compiler has every transposing load wait for such a load in flight, whatever tile it fills; landed() waits
-// for a wave's own, and a barrier behind that for all.  (m0 holds nothing between instructions: whatever needs it
-// sets it.)
+// From memory into LDS, past the registers: lane l's 16 (4) bytes to dst + 16 l (4 l).  In assembly, since the compiler
+// has every transposing load wait for all such loads in flight.  landed<N>() waits for a wave's own but the last N, and
+// a barrier behind that for all.  (m0 holds nothing between instructions: whatever needs it sets it.)
 __device__ __forceinline__ void load_to_lds(const void* src, lds_t dst) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"((unsigned)(uintptr_t)dst), "v"(src) : "memory");
 }
-__device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" : : : "memory"); }
+__device__ __forceinline__ void load_word_to_lds(const void* src, lds_t dst) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" : : "s"((unsigned)(uintptr_t)dst), "v"(src) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void landed() {
+    asm volatile("s_waitcnt vmcnt(%0)" : : "i"(N) : "memory");
+}
 
-// LDS of a workgroup: two tiles of K, two of V; for two tiles the keys' factors (scores, values, values as they are
-// stored); whether a wave met a value that is not finite where that matters.
-template <int D, int WAVES>
-struct Lds {
-    static constexpr int kFactors = 4 * Tile<D>::kBytes;
-    static constexpr int kFlags = kFactors + 6 * kTile * 4;
-    static constexpr int kTotal = kFlags + WAVES * 4;
+// How a workgroup's waves load a tile.  A load of a wave takes kRows keys, 128 bytes (or all) of each.  Every wave takes
+// kRows keys of K and of V, or, where a load takes twice as many, the first half of the waves K and the others V.
+template <int FORMAT, int D, int WAVES>
+struct Plan {
+    static constexpr bool kCodes = FORMAT != GDN_CACHE_PLAIN;
+    static constexpr int kTile = kKeys<WAVES>;
+    static constexpr int kRowBytes = D * (kCodes ? 1 : 2);
+    static constexpr int kChunks = kRowBytes < 128 ? kRowBytes / 16 : 8, kRows = 64 / kChunks, kPieces = kRowBytes / (16 * kChunks);
+    static constexpr bool kSplit = kTile / kRows < WAVES;
+    static_assert(kTile / kRows == (kSplit ? WAVES / 2 : WAVES), "one group of keys to a wave");
+    static constexpr int kLoads = kPieces * (kSplit ? 1 : 2) + 1;      // a wave's, a tile; wave 0 of codes loads two scales more
+    // LDS: tiles of K, of V; codes on their way; the waves' page entries; scales on their way, factors of the keys (scores,
+    // values, values as they are stored); whether a wave met a value that is not finite where that matters
+    static constexpr int kRing = kCodes ? 2 : 4, kWaiting = 3, kEntries = 4;
+    static constexpr int kTileBytes = kTile * D * 2;
+    static constexpr int kV = kRing * kTileBytes, kRaw = 2 * kV, kRawWave = kPieces * 1024 * 2;
+    static constexpr int kEntry = kRaw + (kCodes ? kWaiting * WAVES * kRawWave : 0);
+    static constexpr int kScales = kEntry + WAVES * kEntries * 256, kFactors = kScales + (kCodes ? kWaiting * 2 * 256 : 0);
+    static constexpr int kFlags = kFactors + (kCodes ? 6 * kTile * 4 : 0), kTotal = kFlags + WAVES * 4;
+    static_assert(kTotal <= 160 * 1024, "LDS of a compute unit");
 };
 
 template <int FORMAT, int D, int WAVES>
 __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit& u, lds_t lds) {
-    constexpr bool kCodes = FORMAT != GDN_CACHE_PLAIN, kPair = WAVES == 8;
-    constexpr int kThreads = 64 * WAVES;
-    constexpr int kRowBytes = D * (kCodes ? 1 : 2);
-    // A load of a wave takes kRows keys of a tile, 128 bytes (or all) of each; a wave loads kGroups such groups of keys, or,
-    // where there are fewer groups than waves, the first four waves load K and the others V.
-    constexpr int kChunks = kRowBytes < 128 ? kRowBytes / 16 : 8, kRows = 64 / kChunks, kPieces = kRowBytes / (16 * kChunks);
-    constexpr bool kSplit = kTile / kRows < WAVES;
-    constexpr int kGroups = kSplit ? 1 : kTile / kRows / WAVES;
+    using P = Plan<FORMAT, D, WAVES>;
+    constexpr bool kCodes = P::kCodes, kPair = WAVES == 8;
+    constexpr int kThreads = 64 * WAVES, kTile = P::kTile, kBlocks = kTile / 32, kRows = P::kRows, kChunks = P::kChunks, kPieces = P::kPieces;
     constexpr int kSteps = D / 16, kDims = D / 32;
+    constexpr uint64_t kAll = kTile == 64 ? ~0ull : (1ull << kTile) - 1;
     if (u.lo >= u.hi) {        // a table or a cache without rows: no address may be formed
         fill_rows<__bf16, D>(k, u, 32 * WAVES, kThreads, 0.f);
         return;
     }
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 31, half = lane >> 5, G = (int)k.group.d;
     const int H = k.a.cache.num_heads;
-    const dev::Pages pages = {k.a.table + (int64_t)u.seq * k.a.table_width, k.a.table_width, k.block, k.a.cache.num_rows};
-    const auto ktile = [&](int tile) { return lds + (tile & 1) * Tile<D>::kBytes; };
-    const auto vtile = [&](int tile) { return lds + (2 + (tile & 1)) * Tile<D>::kBytes; };
-    const auto kfactor = [&](int tile) { return (lds_ptr<float>)(lds + Lds<D, WAVES>::kFactors) + (tile & 1) * kTile; };
-    const auto vfactor = [&](int tile) { return (lds_ptr<float>)(lds + Lds<D, WAVES>::kFactors) + (2 + (tile & 1)) * kTile; };
-    const auto vstored = [&](int tile) { return (lds_ptr<float>)(lds + Lds<D, WAVES>::kFactors) + (4 + (tile & 1)) * kTile; };
-    const lds_ptr<int> flags = (lds_ptr<int>)(lds + Lds<D, WAVES>::kFlags);
+    const int32_t* const table = k.a.table + (int64_t)u.seq * k.a.table_width;
+    // tile numbers from -3 on; 12 is a multiple of every ring's length
+    const auto ktile = [&](int t) { return lds + (unsigned)(t + 12) % P::kRing * P::kTileBytes; };
+    const auto vtile = [&](int t) { return lds + P::kV + (unsigned)(t + 12) % P::kRing * P::kTileBytes; };
+    const auto raw = [&](int t) { return lds + P::kRaw + ((unsigned)(t + 12) % P::kWaiting * WAVES + wave) * P::kRawWave; };
+    const auto entries = [&](int t) { return lds + P::kEntry + (wave * P::kEntries + (unsigned)(t + 12) % P::kEntries) * 256; };
+    const auto scales = [&](int t) { return lds + P::kScales + (unsigned)(t + 12) % P::kWaiting * 512; };
+    const auto kfactor = [&](int t) { return (lds_ptr<float>)(lds + P::kFactors) + (t & 1) * kTile; };
+    const auto vfactor = [&](int t) { return (lds_ptr<float>)(lds + P::kFactors) + (2 + (t & 1)) * kTile; };
+    const auto vstored = [&](int t) { return (lds_ptr<float>)(lds + P::kFactors) + (4 + (t & 1)) * kTile; };
+    const lds_ptr<int> flags = (lds_ptr<int>)(lds + P::kFlags);
     // the scale's sign goes into the queries (exactly), so that the largest product is the largest score
     const float c = k.a.scale == 0.f ? 1.f : fabsf(k.a.scale) * kLog2e, sign = k.a.scale == 0.f ? 0.f : copysignf(1.f, k.a.scale);
 
@@ -121,140 +145,114 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
     f32x16_t o[kDims] = {};
     float m = -INFINITY, l = 0.f;
 
-    // ---- loads: a lane's key and its page's entry (in flight) two tiles ahead, then the rows, K one tile ahead, V of the tile
-    // itself.  A wave loads 16 of the tile's keys (with eight waves, half of their dims).
-    int entry = -1, key = 0;
-    const auto lookup = [&](int tile) {
-        key = u.lo + tile * kTile + lane;
-        const unsigned page = dev::divide((unsigned)key, k.block);
-        entry = pages.table[page < (unsigned)pages.width ? page : (unsigned)pages.width - 1];
-    };
-    const auto row_of = [&]() {
-        const unsigned page = dev::divide((unsigned)key, k.block);
-        const int64_t row = (int64_t)entry * k.block.d + ((unsigned)key - page * k.block.d);
-        return key < u.hi && page < (unsigned)pages.width && entry >= 0 && row < pages.num_rows ? (int)row : -1;
-    };
-    const bool loads_k = !kSplit || wave < WAVES / 2, loads_v = !kSplit || wave >= WAVES / 2;
-    const int group0 = kSplit ? wave % (WAVES / 2) : wave * kGroups;
-    u32x4_t kp[kGroups][kPieces], vp[kGroups][kPieces];
-    float ks = 0.f, vs = 0.f;
+    // ---- loads
+    const bool loads_k = !P::kSplit || wave < WAVES / 2, loads_v = !P::kSplit || wave >= WAVES / 2;
+    const int group = P::kSplit ? wave % (WAVES / 2) : wave;      // of kRows keys
     // Chunk `chunk` of a key's row in the cache; an absent key's values are those of row 0.
     const auto address = [&](const void* cache, int row, int chunk) {
-        return static_cast<const char*>(cache) + (int64_t)u.h * kRowBytes + chunk * 16 + (uint64_t)(unsigned)(row < 0 ? 0 : row) * (unsigned)(H * kRowBytes);
+        return static_cast<const char*>(cache) + (int64_t)u.h * P::kRowBytes + chunk * 16 + (uint64_t)(unsigned)(row < 0 ? 0 : row) * (unsigned)(H * P::kRowBytes);
     };
-    const auto load_k = [&](int tile, int row) {
-        if (!loads_k) return;
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-            const int group = group0 + g, at = lane / kRows;      // (where codes are, chunks stay in order)
-            const char* const from = address(k.a.cache.k, __shfl(row, group * kRows + lane % kRows), kCodes ? at : at ^ (group & 1));
-#pragma unroll
-            for (int i = 0; i < kPieces; ++i) {
-                if constexpr (kCodes) kp[g][i] = *reinterpret_cast<const u32x4_t*>(from + 128 * i);
-                else load_to_lds(from + 128 * i, ktile(tile) + Tile<D>::block(group, i));
-            }
-        }
-        if constexpr (kCodes)
-            if (wave == 0) {
-                ks = row >= 0 ? k.a.cache.k_scale[(int64_t)row * H + u.h] : 0.f;
-                vs = row >= 0 ? k.a.cache.v_scale[(int64_t)row * H + u.h] : 0.f;
-            }
+    const auto load_entries = [&](int t) {
+        const unsigned page = dev::divide((unsigned)(u.lo + t * kTile + lane), k.block);
+        load_word_to_lds(table + (page < (unsigned)k.a.table_width ? page : (unsigned)k.a.table_width - 1), entries(t));
     };
-    const auto load_v = [&](int tile, int row) {
-        if (!loads_v) return;
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-            const int group = group0 + g, at = lane % kChunks;
-            const char* const from = address(k.a.cache.v, __shfl(row, group * kRows + lane / kChunks), kCodes ? at : at ^ (lane / kChunks * 2 & 4));
-#pragma unroll
-            for (int i = 0; i < kPieces; ++i) {
-                if constexpr (kCodes) vp[g][i] = *reinterpret_cast<const u32x4_t*>(from + 128 * i);
-                else load_to_lds(from + 128 * i, vtile(tile) + Tile<D>::block(group, i));
-            }
-        }
+    const auto row_of = [&](int t) {      // the cache row of the lane's key of tile t, or -1
+        const int key = u.lo + t * kTile + lane, entry = ((lds_ptr<int>)entries(t))[lane];
+        const unsigned page = dev::divide((unsigned)key, k.block);
+        const int64_t at = (int64_t)entry * k.block.d + ((unsigned)key - page * k.block.d);
+        return (kTile == 64 || lane < kTile) && key < u.hi && page < (unsigned)k.a.table_width && entry >= 0 && at < k.a.cache.num_rows ? (int)at : -1;
     };
-    // Whether keys of a tile are absent, or some rows of the workgroup do not see some.
-    const auto special = [&](int tile, uint64_t there) { return there != ~0ull || u.lo + (tile + 1) * kTile > some; };
-    // What was loaded, in LDS: codes as values.
-    const auto land_k = [&](int tile, uint64_t there) {
-        if constexpr (kCodes) {
-            if (!loads_k) return;
+    int row = -1;                       // of the lane's key of tile t + 2 before issue(t)
+    uint64_t there[4] = {0, 0, 0, 0};   // which keys of tiles t .. t + 3 are there, after issue(t)
+    // What is issued with tile t: the entries six tiles ahead, K (and the scales) three, V two.
+    const auto issue = [&](int t) {
+        const int next = row_of(t + 3);
+        there[0] = there[1];
+        there[1] = there[2];
+        there[2] = there[3];
+        there[3] = __ballot(next >= 0);
+        if (loads_v) {
+            const int at = lane % kChunks, key = lane / kChunks;
+            const char* const from = address(k.a.cache.v, __shfl(row, group * kRows + key), kCodes ? at : at ^ (2 * key & 4));
 #pragma unroll
-            for (int g = 0; g < kGroups; ++g)
-#pragma unroll
-                for (int i = 0; i < kPieces; ++i)
-#pragma unroll
-                    for (int x = 0; x < 2; ++x)
-                        *(lds_ptr<bf16x8_t>)(ktile(tile) + Tile<D>::k((group0 + g) * kRows + lane % kRows, 16 * i + 2 * (lane / kRows) + x)) =
-                            dev::codes8<__bf16, FORMAT>(kp[g][i][2 * x], kp[g][i][2 * x + 1]);
-            if (wave == 0) {
-                kfactor(tile)[lane] = ks * c;
-                vfactor(tile)[lane] = special(tile, there) && !dev::finite(vs) ? 0.f : vs;
-                vstored(tile)[lane] = vs;
-            }
+            for (int i = 0; i < kPieces; ++i) load_to_lds(from + 128 * i, kCodes ? raw(t + 2) + (kPieces + i) * 1024 : vtile(t + 2) + Tile<D>::block(group, i));
         }
-    };
-    const auto land_v = [&](int tile) {
-        if constexpr (kCodes) {
-            if (!loads_v) return;
+        if (loads_k) {
+            const int at = lane / kRows;
+            const char* const from = address(k.a.cache.k, __shfl(next, group * kRows + lane % kRows), kCodes ? at : at ^ (group & 1));
 #pragma unroll
-            for (int g = 0; g < kGroups; ++g)
-#pragma unroll
-                for (int i = 0; i < kPieces; ++i)
-#pragma unroll
-                    for (int x = 0; x < 2; ++x)
-                        *(lds_ptr<bf16x8_t>)(vtile(tile) + Tile<D>::v((group0 + g) * kRows + lane / kChunks, 16 * i + 2 * (lane % kChunks) + x)) =
-                            dev::codes8<__bf16, FORMAT>(vp[g][i][2 * x], vp[g][i][2 * x + 1]);
+            for (int i = 0; i < kPieces; ++i) load_to_lds(from + 128 * i, kCodes ? raw(t + 3) + i * 1024 : ktile(t + 3) + Tile<D>::block(group, i));
         }
-    };
-    int row;                        // the lane's key of tile `t` after issue(t) began: of tile t + 1 when it is done
-    uint64_t present, ahead;        // which keys of tile t, and t + 1, are there
-    const auto issue = [&](int tile) {
-        // the entry first: what waits for it waits for every load before it
-        const int next = tile + 1 < tiles ? row_of() : -1;
-        present = ahead;
-        ahead = __ballot(next >= 0);
-        load_v(tile, row);
-        if (tile + 1 < tiles) {
-            load_k(tile + 1, next);
-            lookup(tile + 2);
+        if (kCodes && wave == 0) {
+            const int64_t at = (int64_t)(next < 0 ? 0 : next) * H + u.h;
+            load_word_to_lds(k.a.cache.k_scale + at, scales(t + 3));
+            load_word_to_lds(k.a.cache.v_scale + at, scales(t + 3) + 256);
         }
+        load_entries(t + 6);
         row = next;
     };
-    const auto land = [&](int tile) {
-        land_v(tile);
-        if (tile + 1 < tiles) land_k(tile + 1, ahead);
-        if (!kCodes) landed();
+    // Whether keys of a tile are absent, or some rows of the workgroup do not see some.
+    const auto special = [&](int t, uint64_t now) { return now != kAll || u.lo + (t + 1) * kTile > some; };
+    // K of the next tile and V of tile t (the loads of issue(t - 2)) are there; codes as values.
+    const auto land = [&](int t) {
+        if (kCodes && wave == 0) landed<2 * (P::kLoads + 2)>();
+        else landed<2 * P::kLoads>();
+        if constexpr (kCodes) {
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                if (loads_k) {
+                    const u32x4_t w = *(lds_ptr<u32x4_t>)(raw(t + 1) + i * 1024 + lane * 16);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+                        *(lds_ptr<bf16x8_t>)(ktile(t + 1) + Tile<D>::k(group * kRows + lane % kRows, 16 * i + 2 * (lane / kRows) + x)) =
+                            dev::codes8<__bf16, FORMAT>(w[2 * x], w[2 * x + 1]);
+                }
+                if (loads_v) {
+                    const u32x4_t w = *(lds_ptr<u32x4_t>)(raw(t) + (kPieces + i) * 1024 + lane * 16);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+                        *(lds_ptr<bf16x8_t>)(vtile(t) + Tile<D>::v(group * kRows + lane / kChunks, 16 * i + 2 * (lane % kChunks) + x)) =
+                            dev::codes8<__bf16, FORMAT>(w[2 * x], w[2 * x + 1]);
+                }
+            }
+            if (wave == 0 && (kTile == 64 || lane < kTile)) {
+                const float ks = ((lds_ptr<float>)scales(t + 1))[lane], vs = ((lds_ptr<float>)(scales(t + 1) + 256))[lane];
+                const bool here = there[1] >> lane & 1;
+                kfactor(t + 1)[lane] = here ? ks * c : 0.f;
+                vfactor(t + 1)[lane] = !here || (special(t + 1, there[1]) && !dev::finite(vs)) ? 0.f : vs;
+                vstored(t + 1)[lane] = here ? vs : 0.f;
+            }
+        }
     };
 
     // ---- the phases of a tile
-    f32x16_t s[2];
-    bf16x8_t w[4];
-    const auto scores = [&](int tile) {
+    f32x16_t s[kBlocks];
+    bf16x8_t w[2 * kBlocks];
+    const auto scores = [&](int t) {
         // chunk 2 x + half of key 32 b + col: fixed distances from the lane's first
-        const lds_t kt = ktile(tile) + Tile<D>::k(col, half);
-        s[0] = f32x16_t{};
-        s[1] = f32x16_t{};
+        const lds_t kt = ktile(t) + Tile<D>::k(col, half);
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) s[b] = f32x16_t{};
 #pragma unroll
         for (int x = 0; x < kSteps; ++x)
 #pragma unroll
-            for (int b = 0; b < 2; ++b) s[b] = mma32(*(lds_ptr<bf16x8_t>)(kt + Tile<D>::k(32 * b, 2 * x)), q[x], s[b]);
+            for (int b = 0; b < kBlocks; ++b) s[b] = mma32(*(lds_ptr<bf16x8_t>)(kt + Tile<D>::k(32 * b, 2 * x)), q[x], s[b]);
     };
-    const auto softmax = [&](int tile, uint64_t now) {
-        const int p0 = u.lo + tile * kTile;
+    const auto softmax = [&](int t, uint64_t now) {
+        const int p0 = u.lo + t * kTile;
         if constexpr (kCodes)
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+            for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const f32x4_t by = *(lds_ptr<f32x4_t>)(kfactor(tile) + 32 * b + 8 * i + 4 * half);
+                    const f32x4_t by = *(lds_ptr<f32x4_t>)(kfactor(t) + 32 * b + 8 * i + 4 * half);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) s[b][4 * i + j] *= by[j];
                 }
-        if (now != ~0ull || p0 + kTile > mine) {
+        if (now != kAll || p0 + kTile > mine) {
             const uint64_t seen = sees.from(p0) & now;
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
+            for (int b = 0; b < kBlocks; ++b) {
                 const unsigned bits = (unsigned)(seen >> (32 * b)) >> (4 * half);
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
@@ -263,7 +261,7 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
         }
         float top = -INFINITY;
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
             for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
         float x, y;
@@ -284,11 +282,11 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
         }
         const float base = m == -INFINITY ? 0.f : m;
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 f32x4_t by = {1.f, 1.f, 1.f, 1.f};
-                if constexpr (kCodes) by = *(lds_ptr<f32x4_t>)(vfactor(tile) + 32 * b + 8 * i + 4 * half);
+                if constexpr (kCodes) by = *(lds_ptr<f32x4_t>)(vfactor(t) + 32 * b + 8 * i + 4 * half);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float e = __builtin_amdgcn_exp2f(kCodes ? s[b][4 * i + j] - base : fmaf(s[b][4 * i + j], c, -base));
@@ -297,12 +295,12 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
                 }
             }
     };
-    const auto sums = [&](int tile) {
+    const auto sums = [&](int t) {
         // chunk 4 d + piece of four keys: fixed distances too, from one first for the even d and one for the odd
         const int vkey = 4 * half + lane % 16 / 4, piece = 2 * (lane >> 4 & 1) + (lane >> 1 & 1);
-        const lds_t vt[2] = {vtile(tile) + Tile<D>::v(vkey, piece) + (lane & 1) * 8, vtile(tile) + Tile<D>::v(vkey, 4 + piece) + (lane & 1) * 8};
+        const lds_t vt[2] = {vtile(t) + Tile<D>::v(vkey, piece) + (lane & 1) * 8, vtile(t) + Tile<D>::v(vkey, 4 + piece) + (lane & 1) * 8};
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
+        for (int g = 0; g < 2 * kBlocks; ++g)
 #pragma unroll
             for (int d = 0; d < kDims; ++d) {
                 const auto a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr<dev::s16x4_t>)(vt[d & 1] + Tile<D>::block(2 * g, d / 2)));
@@ -314,13 +312,13 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
     // Where keys are absent, or some rows do not see some, no value that is not finite may meet a weight of zero: absent
     // keys' values are zeroed; others are added to the rows that see them, and are zeros in the product.  All waves
     // come here together, between the landing of the tile's V and its sums.
-    const auto mend = [&](int tile, uint64_t now) {
-        const int p0 = u.lo + tile * kTile;
-        if (!special(tile, now)) return;
-        constexpr int kAll = kTile * D / 8;
-        const lds_t vt = vtile(tile);
+    const auto mend = [&](int t, uint64_t now) {
+        const int p0 = u.lo + t * kTile;
+        if (!special(t, now)) return;
+        constexpr int kCount = kTile * D / 8;
+        const lds_t vt = vtile(t);
         bool fine = true;
-        for (int i = threadIdx.x; i < kAll; i += kThreads) {
+        for (int i = threadIdx.x; i < kCount; i += kThreads) {
             const int n = i / D * 8 + i % 64 / 8;                 // chunks as they lie: D to eight keys
             const lds_ptr<bf16x8_t> at = (lds_ptr<bf16x8_t>)vt + i;
             if (now >> n & 1) {
@@ -331,7 +329,7 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
                 *at = bf16x8_t{};
             }
         }
-        if (kCodes && threadIdx.x < kTile) fine &= dev::finite(vstored(tile)[threadIdx.x]);
+        if (kCodes && threadIdx.x < kTile) fine &= dev::finite(vstored(t)[threadIdx.x]);
         const bool wrong = __any(!fine);
         if (lane == 0) flags[wave] = wrong;
         dev::lds_barrier();
@@ -344,7 +342,7 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
                 for (int n = 0; n < kTile; ++n) {
                     if (!(now >> n & 1)) continue;
                     float by = 1.f;
-                    if constexpr (kCodes) by = vstored(tile)[n];
+                    if constexpr (kCodes) by = vstored(t)[n];
 #pragma unroll
                     for (int d = 0; d < kDims; ++d)
 #pragma unroll
@@ -357,7 +355,7 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
                 }
             }
             dev::lds_barrier();
-            for (int i = threadIdx.x; i < kAll; i += kThreads) {
+            for (int i = threadIdx.x; i < kCount; i += kThreads) {
                 const lds_ptr<bf16x8_t> at = (lds_ptr<bf16x8_t>)vt + i;
                 bf16x8_t v = *at;
 #pragma unroll
@@ -369,16 +367,15 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
         dev::lds_barrier();
     };
 
-    // ---- slot 2 t: issue(t), the first waves' products of tile t (their sums of t - 1); slot 2 t + 1: their softmax, and what was
-    // issued lands.  The waves behind do the same one slot later, and issue and land in the same slots as the first.  A tile's
-    // buffers are free when it is issued: K of t - 1 and V of t - 2 were last read in slot 2 t - 1.
-    lookup(0);
-    row = row_of();
-    ahead = __ballot(row >= 0);
-    load_k(0, row);
-    lookup(1);
-    land_k(0, ahead);
-    if (!kCodes) landed();
+    // ---- slot 2 t: issue(t), the first waves' products of tile t (their sums of t - 1); slot 2 t + 1: their softmax, and land(t).
+    // The waves behind do the same one slot later, but issue and land in the same slots as the first.  K of tile t is read in
+    // slots 2 t and 2 t + 1, V in 2 t + 2 and 2 t + 3; K of t + 3 and V of t + 2, issued in slot 2 t, take the places of t - 1 and
+    // t - 2, last read in slot 2 t - 1; so do codes' tiles, K of t + 1 and V of t made in slot 2 t + 1.  A wave reads its entries of t + 3
+    // in slot 2 t, three landings after they were issued.
+    for (int t = 0; t < 3; ++t) load_entries(t);
+    landed<0>();
+    for (int t = -3; t < 0; ++t) issue(t);
+    land(-1);
     dev::lds_barrier();
     if (behind) {
         issue(0);
@@ -387,7 +384,7 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
     for (int t = 0; t < tiles; ++t) {
         const bool work = u.lo + t * kTile < end;
         if (!behind) issue(t);
-        const uint64_t now = present;
+        const uint64_t now = there[0];
         if (t > 0 && u.lo + (t - 1) * kTile < end) sums(t - 1);
         if (work) scores(t);
         if (behind) land(t);
@@ -402,6 +399,7 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
         if (!behind) mend(t, now);
     }
     if (u.lo + (tiles - 1) * kTile < end) sums(tiles - 1);
+    landed<0>();               // nothing may be on its way into LDS that is another workgroup's by then
 
     float x, y;
     dev::pair32(l, x, y);
@@ -457,7 +455,7 @@ hipError_t launch(AttentionKernelArgs k, hipStream_t stream) {
     if (!grid_fits(tiles * units, kThreads) || k.a.total_tokens * (int64_t)k.group.d > 0x7fffffffLL) return hipErrorInvalidConfiguration;
     k.row_tiles = (int)tiles;
     auto* const kernel = decode ? wide_decode_kernel<FORMAT, D, WAVES> : wide_prompt_kernel<FORMAT, D, WAVES>;
-    kernel<<<(unsigned)(tiles * units), kThreads, Lds<D, WAVES>::kTotal, stream>>>(k);
+    kernel<<<(unsigned)(tiles * units), kThreads, (Plan<FORMAT, D, WAVES>::kTotal), stream>>>(k);
     return hipGetLastError();
 }
 
