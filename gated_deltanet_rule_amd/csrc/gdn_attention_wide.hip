@@ -132,6 +132,11 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
                 for (int i = 0; i < 8; ++i) q[s][i] = (__bf16)((float)q[s][i] * sign);
         sees = row_sees(k, u, r);
     }
+    // The compiler's own loads are waited for here: it does not see the waits in assembly below, and would otherwise place its
+    // own where the queries are first used, in the loop, for whatever is on its way there.
+#pragma unroll
+    for (int x = 0; x < kSteps; ++x) asm volatile("" : "+v"(q[x]));
+    asm volatile("" : "+v"(sees.all), "+v"(sees.first), "+v"(sees.mask));
     // every row of the workgroup (of the wave) sees the keys below `some` (`mine`), no row of the wave one from `end` on
     const bool tree = k.a.tree_mask != nullptr;
     const int some = tree ? u.past : u.past + (int)dev::divide(u.row0, k.group) + 1;
