@@ -40,17 +40,18 @@ template <typename V>
 using lds_ptr = __attribute__((address_space(3))) V*;
 typedef lds_ptr<char> lds_t;
 
-// Tiles of bf16 values in LDS: blocks of 8 keys by 64 dims, 1 KB each, which one load of a wave fills (16 bytes a lane,
-// in lanes' order) from 128 bytes of each key.  K's operands take one 16-byte chunk of 16 keys at a time: a block of K
-// holds chunk after chunk, pairs of chunks exchanged in every other block.  V's transposing loads take 64 bytes of
-// four keys at a time: a block of V holds key after key, their halves exchanged for every other pair of keys.  Neither
-// meets itself in a bank, and a tile's operands stand at fixed distances from a lane's first.
+// Tiles of bf16 values in LDS: blocks of 8 keys by 64 dims, 1 KB each, key after key, which one load of a wave fills (16
+// bytes a lane, in lanes' order) from 128 bytes of each key: four neighbouring lanes have to stand in the same 64 bytes of
+// memory, or a load takes the memory path up to four times as long.  The 16-byte chunks of a key are exchanged: K's operands
+// take one chunk of 16 keys at a time, V's transposing loads 64 bytes of four, and neither meets itself in a bank.
 template <int D>
 struct Tile {
     __device__ static constexpr int block(int key8, int dim64) { return (key8 * (D / 64) + dim64) * 1024; }
-    // chunk c (eight dims) of a key
-    __device__ static constexpr int k(int key, int c) { return block(key / 8, c / 8) + (c % 8 ^ (key / 8 & 1)) * 128 + key % 8 * 16; }
-    __device__ static constexpr int v(int key, int c) { return block(key / 8, c / 8) + key % 8 * 128 + (c % 8 ^ (2 * key & 4)) * 16; }
+    // where chunk c (eight dims) of a key stands
+    __device__ static constexpr int kswap(int key) { return key >> 1 & 7; }
+    __device__ static constexpr int vswap(int key) { return 2 * key & 4; }
+    __device__ static constexpr int k(int key, int c) { return block(key / 8, c / 8) + key % 8 * 128 + (c % 8 ^ kswap(key)) * 16; }
+    __device__ static constexpr int v(int key, int c) { return block(key / 8, c / 8) + key % 8 * 128 + (c % 8 ^ vswap(key)) * 16; }
 };
 
 // From memory into LDS, past the registers: lane l's 16 (4) bytes to dst + 16 l (4 l).  In assembly, since the compiler
@@ -176,22 +177,21 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
         there[1] = there[2];
         there[2] = there[3];
         there[3] = __ballot(next >= 0);
+        const int at = lane % kChunks, key = group * kRows + lane / kChunks;
         if (loads_v) {
-            const int at = lane % kChunks, key = lane / kChunks;
-            const char* const from = address(k.a.cache.v, __shfl(row, group * kRows + key), kCodes ? at : at ^ (2 * key & 4));
+            const char* const from = address(k.a.cache.v, __shfl(row, key), kCodes ? at : at ^ Tile<D>::vswap(key));
 #pragma unroll
             for (int i = 0; i < kPieces; ++i) load_to_lds(from + 128 * i, kCodes ? raw(t + 2) + (kPieces + i) * 1024 : vtile(t + 2) + Tile<D>::block(group, i));
         }
         if (loads_k) {
-            const int at = lane / kRows;
-            const char* const from = address(k.a.cache.k, __shfl(next, group * kRows + lane % kRows), kCodes ? at : at ^ (group & 1));
+            const char* const from = address(k.a.cache.k, __shfl(next, key), kCodes ? at : at ^ Tile<D>::kswap(key));
 #pragma unroll
             for (int i = 0; i < kPieces; ++i) load_to_lds(from + 128 * i, kCodes ? raw(t + 3) + i * 1024 : ktile(t + 3) + Tile<D>::block(group, i));
         }
         if (kCodes && wave == 0) {
-            const int64_t at = (int64_t)(next < 0 ? 0 : next) * H + u.h;
-            load_word_to_lds(k.a.cache.k_scale + at, scales(t + 3));
-            load_word_to_lds(k.a.cache.v_scale + at, scales(t + 3) + 256);
+            const int64_t head = (int64_t)(next < 0 ? 0 : next) * H + u.h;
+            load_word_to_lds(k.a.cache.k_scale + head, scales(t + 3));
+            load_word_to_lds(k.a.cache.v_scale + head, scales(t + 3) + 256);
         }
         load_entries(t + 6);
         row = next;
@@ -209,7 +209,7 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
                     const u32x4_t w = *(lds_ptr<u32x4_t>)(raw(t + 1) + i * 1024 + lane * 16);
 #pragma unroll
                     for (int x = 0; x < 2; ++x)
-                        *(lds_ptr<bf16x8_t>)(ktile(t + 1) + Tile<D>::k(group * kRows + lane % kRows, 16 * i + 2 * (lane / kRows) + x)) =
+                        *(lds_ptr<bf16x8_t>)(ktile(t + 1) + Tile<D>::k(group * kRows + lane / kChunks, 16 * i + 2 * (lane % kChunks) + x)) =
                             dev::codes8<__bf16, FORMAT>(w[2 * x], w[2 * x + 1]);
                 }
                 if (loads_v) {
@@ -234,14 +234,16 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
     f32x16_t s[kBlocks];
     bf16x8_t w[2 * kBlocks];
     const auto scores = [&](int t) {
-        // chunk 2 x + half of key 32 b + col: fixed distances from the lane's first
-        const lds_t kt = ktile(t) + Tile<D>::k(col, half);
+        // chunk 2 x + half of key 32 b + col: fixed distances from the lane's first four
+        lds_t kt[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) kt[x] = ktile(t) + Tile<D>::k(col, 2 * x + half);
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b) s[b] = f32x16_t{};
 #pragma unroll
         for (int x = 0; x < kSteps; ++x)
 #pragma unroll
-            for (int b = 0; b < kBlocks; ++b) s[b] = mma32(*(lds_ptr<bf16x8_t>)(kt + Tile<D>::k(32 * b, 2 * x)), q[x], s[b]);
+            for (int b = 0; b < kBlocks; ++b) s[b] = mma32(*(lds_ptr<bf16x8_t>)(kt[x & 3] + Tile<D>::block(4 * b, x / 4)), q[x], s[b]);
     };
     const auto softmax = [&](int t, uint64_t now) {
         const int p0 = u.lo + t * kTile;
