@@ -214,10 +214,14 @@ __device__ __forceinline__ bool prompt_unit(const AttentionKernelArgs& k, int pe
         const int64_t c = k.a.cu_seqlens[i];
         return c < 0 ? 0 : (c > total ? total : c);
     };
-    int lo = 0, hi = k.a.num_seqs;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (token(mid) * G / per + mid <= tile) lo = mid; else hi = mid;
+    // 64 sequences at a time, a lane each: the last whose first tile is not behind this one
+    const int lane = threadIdx.x & 63;
+    int lo = 0, step = 1;
+    while ((int64_t)step * 64 < k.a.num_seqs) step *= 64;
+    for (; step > 0; step /= 64) {
+        const int64_t i = lo + (int64_t)lane * step;
+        const bool reached = i < k.a.num_seqs && token((int)i) * G / per + i <= tile;
+        lo += step * (63 - __builtin_clzll(__ballot(reached) | 1));
     }
     u.seq = lo;
     u.h = h;

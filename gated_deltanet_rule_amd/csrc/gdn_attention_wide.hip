@@ -117,6 +117,12 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
     // the scale's sign goes into the queries (exactly), so that the largest product is the largest score
     const float c = k.a.scale == 0.f ? 1.f : fabsf(k.a.scale) * kLog2e, sign = k.a.scale == 0.f ? 0.f : copysignf(1.f, k.a.scale);
 
+    const auto load_entries = [&](int t) {
+        const unsigned page = dev::divide((unsigned)(u.lo + t * kTile + lane), k.block);
+        load_word_to_lds(table + (page < (unsigned)k.a.table_width ? page : (unsigned)k.a.table_width - 1), entries(t));
+    };
+    for (int t = 0; t < 3; ++t) load_entries(t);
+
     const int r = u.row0 + 32 * wave + col, t = (int)dev::divide(r, k.group);
     const bool live = r < u.rows;
     const bool busy = u.row0 + 32 * wave < u.rows;       // whether the wave has any rows
@@ -157,10 +163,6 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
     // Chunk `chunk` of a key's row in the cache; an absent key's values are those of row 0.
     const auto address = [&](const void* cache, int row, int chunk) {
         return static_cast<const char*>(cache) + (int64_t)u.h * P::kRowBytes + chunk * 16 + (uint64_t)(unsigned)(row < 0 ? 0 : row) * (unsigned)(H * P::kRowBytes);
-    };
-    const auto load_entries = [&](int t) {
-        const unsigned page = dev::divide((unsigned)(u.lo + t * kTile + lane), k.block);
-        load_word_to_lds(table + (page < (unsigned)k.a.table_width ? page : (unsigned)k.a.table_width - 1), entries(t));
     };
     const auto row_of = [&](int t) {      // the cache row of the lane's key of tile t, or -1
         const int key = u.lo + t * kTile + lane, entry = ((lds_ptr<int>)entries(t))[lane];
@@ -374,13 +376,13 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
         dev::lds_barrier();
     };
 
-    // ---- slot 2 t: issue(t), the first waves' products of tile t (their sums of t - 1); slot 2 t + 1: their softmax, and land(t).
-    // The waves behind do the same one slot later, but issue and land in the same slots as the first.  K of tile t is read in
-    // slots 2 t and 2 t + 1, V in 2 t + 2 and 2 t + 3; K of t + 3 and V of t + 2, issued in slot 2 t, take the places of t - 1 and
-    // t - 2, last read in slot 2 t - 1; so do codes' tiles, K of t + 1 and V of t made in slot 2 t + 1.  A wave reads its entries of t + 3
-    // in slot 2 t, three landings after they were issued.
-    for (int t = 0; t < 3; ++t) load_entries(t);
-    landed<0>();
+    // ---- slot 2 t: the first waves' products of tile t (their sums of t - 1); slot 2 t + 1: their softmax.  The waves behind do the
+    // same one slot later.  A wave issues behind its softmax, where it has time to wait for the memory path: the first waves
+    // issue(t) in slot 2 t + 1, the others in slot 2 t; all land(t) in slot 2 t + 1, where issue(t - 2) is behind any of them.  K of tile t
+    // is read in slots 2 t and 2 t + 1, V in 2 t + 2 and 2 t + 3; K of t + 3 and V of t + 2 take the places of t - 1 and t - 2, last read in
+    // slot 2 t - 1; so do codes' tiles, K of t + 1 and V of t made in slot 2 t + 1.  A wave reads its entries of t + 3 in issue(t), behind
+    // land(t - 1), to which those of issue(t - 3) have come.
+    landed<0>();               // the first three tiles' entries (and the queries)
     for (int t = -3; t < 0; ++t) issue(t);
     land(-1);
     dev::lds_barrier();
@@ -390,17 +392,14 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
     }
     for (int t = 0; t < tiles; ++t) {
         const bool work = u.lo + t * kTile < end;
-        if (!behind) issue(t);
-        const uint64_t now = there[0];
+        const uint64_t now = behind ? there[0] : there[1];
         if (t > 0 && u.lo + (t - 1) * kTile < end) sums(t - 1);
         if (work) scores(t);
         if (behind) land(t);
         if (kPair) dev::lds_barrier();
-        if (behind) {
-            mend(t, now);
-            if (t + 1 < tiles) issue(t + 1);
-        }
+        if (behind) mend(t, now);
         if (work) softmax(t, now);
+        if (!behind || t + 1 < tiles) issue(behind ? t + 1 : t);
         if (!behind) land(t);
         if (!behind || t + 1 < tiles) dev::lds_barrier();
         if (!behind) mend(t, now);
