@@ -154,6 +154,15 @@ struct Unit {
 // gdn_attention_wide.hip: bf16 prompts, and decode rows (without the join of their spans).
 hipError_t launch_attention_wide(const AttentionKernelArgs& k, hipStream_t stream);
 
+// A unit is its workgroup's: its fields go into scalar registers, which the compiler does not see where they come out of memory,
+// so that the branches and addresses made of them are scalar too.
+__device__ __forceinline__ void make_uniform(Unit& u) {
+    const auto one = [](int& x) { x = __builtin_amdgcn_readfirstlane(x); };
+    one(u.seq); one(u.h); one(u.tokens); one(u.past); one(u.row0); one(u.rows); one(u.lo); one(u.hi); one(u.span); one(u.spans);
+    const unsigned lo = __builtin_amdgcn_readfirstlane((unsigned)u.first), hi = __builtin_amdgcn_readfirstlane((unsigned)((uint64_t)u.first >> 32));
+    u.first = (int64_t)((uint64_t)hi << 32 | lo);
+}
+
 // Keys of a decode row, all of its tokens' among them, as far as its table goes; < 0 for a padding row.
 __device__ __forceinline__ int row_keys(const AttentionArgs& a, int past) {
     if (past < 0) return -1;
@@ -202,6 +211,7 @@ __device__ __forceinline__ bool decode_unit(const AttentionKernelArgs& k, int pe
     u.past = u.past < k.a.capacity ? u.past : k.a.capacity;
     u.lo = u.span * span;
     u.hi = keys - u.lo < span ? keys : u.lo + span;
+    make_uniform(u);
     return true;
 }
 
@@ -239,6 +249,7 @@ __device__ __forceinline__ bool prompt_unit(const AttentionKernelArgs& k, int pe
     u.hi = (int)(keys < k.a.capacity ? keys : k.a.capacity);
     u.span = 0;
     u.spans = 1;
+    make_uniform(u);
     return true;
 }
 

@@ -96,7 +96,7 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
     constexpr bool kCodes = P::kCodes, kPair = WAVES == 8;
     constexpr int kThreads = 64 * WAVES, kTile = P::kTile, kBlocks = kTile / 32, kRows = P::kRows, kChunks = P::kChunks, kPieces = P::kPieces;
     constexpr int kSteps = D / 16, kDims = D / 32;
-    constexpr uint64_t kAll = kTile == 64 ? ~0ull : (1ull << kTile) - 1;
+    constexpr uint64_t kAll = ~0ull >> (64 - kTile);
     if (u.lo >= u.hi) {        // a table or a cache without rows: no address may be formed
         fill_rows<__bf16, D>(k, u, 32 * WAVES, kThreads, 0.f);
         return;
@@ -121,7 +121,7 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
         const unsigned page = dev::divide((unsigned)(u.lo + t * kTile + lane), k.block);
         load_word_to_lds(table + (page < (unsigned)k.a.table_width ? page : (unsigned)k.a.table_width - 1), entries(t));
     };
-    for (int t = 0; t < 3; ++t) load_entries(t);
+    for (int t = 0; t < 4; ++t) load_entries(t);
 
     const int r = u.row0 + 32 * wave + col, t = (int)dev::divide(r, k.group);
     const bool live = r < u.rows;
@@ -170,33 +170,36 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
         const int64_t at = (int64_t)entry * k.block.d + ((unsigned)key - page * k.block.d);
         return (kTile == 64 || lane < kTile) && key < u.hi && page < (unsigned)k.a.table_width && entry >= 0 && at < k.a.cache.num_rows ? (int)at : -1;
     };
-    int row = -1;                       // of the lane's key of tile t + 2 before issue(t)
-    uint64_t there[4] = {0, 0, 0, 0};   // which keys of tiles t .. t + 3 are there, after issue(t)
-    // What is issued with tile t: the entries six tiles ahead, K (and the scales) three, V two.
+    // What is issued with tile t: the entries seven tiles ahead, K (and the scales) three, V two.  Where they come from is worked out
+    // one issue earlier (prepare(t)), in the shadow of the loads before.
+    int next = -1;                          // the cache row of the lane's key of tile t + 3, from prepare(t) on
+    uint64_t there[5] = {0, 0, 0, 0, 0};    // which keys of tiles t .. t + 4 are there, after issue(t)
+    const char *kfrom = nullptr, *vfrom = nullptr;
+    const int chunk = lane % kChunks, mykey = group * kRows + lane / kChunks;
+    const auto prepare = [&](int t) {
+        if (loads_v) vfrom = address(k.a.cache.v, __shfl(next, mykey), kCodes ? chunk : chunk ^ Tile<D>::vswap(mykey));
+        next = row_of(t + 3);
+        there[4] = __ballot(next >= 0);
+        if (loads_k) kfrom = address(k.a.cache.k, __shfl(next, mykey), kCodes ? chunk : chunk ^ Tile<D>::kswap(mykey));
+    };
     const auto issue = [&](int t) {
-        const int next = row_of(t + 3);
         there[0] = there[1];
         there[1] = there[2];
         there[2] = there[3];
-        there[3] = __ballot(next >= 0);
-        const int at = lane % kChunks, key = group * kRows + lane / kChunks;
-        if (loads_v) {
-            const char* const from = address(k.a.cache.v, __shfl(row, key), kCodes ? at : at ^ Tile<D>::vswap(key));
+        there[3] = there[4];
+        if (loads_v)
 #pragma unroll
-            for (int i = 0; i < kPieces; ++i) load_to_lds(from + 128 * i, kCodes ? raw(t + 2) + (kPieces + i) * 1024 : vtile(t + 2) + Tile<D>::block(group, i));
-        }
-        if (loads_k) {
-            const char* const from = address(k.a.cache.k, __shfl(next, key), kCodes ? at : at ^ Tile<D>::kswap(key));
+            for (int i = 0; i < kPieces; ++i) load_to_lds(vfrom + 128 * i, kCodes ? raw(t + 2) + (kPieces + i) * 1024 : vtile(t + 2) + Tile<D>::block(group, i));
+        if (loads_k)
 #pragma unroll
-            for (int i = 0; i < kPieces; ++i) load_to_lds(from + 128 * i, kCodes ? raw(t + 3) + i * 1024 : ktile(t + 3) + Tile<D>::block(group, i));
-        }
+            for (int i = 0; i < kPieces; ++i) load_to_lds(kfrom + 128 * i, kCodes ? raw(t + 3) + i * 1024 : ktile(t + 3) + Tile<D>::block(group, i));
         if (kCodes && wave == 0) {
             const int64_t head = (int64_t)(next < 0 ? 0 : next) * H + u.h;
             load_word_to_lds(k.a.cache.k_scale + head, scales(t + 3));
             load_word_to_lds(k.a.cache.v_scale + head, scales(t + 3) + 256);
         }
-        load_entries(t + 6);
-        row = next;
+        load_entries(t + 7);
+        prepare(t + 1);
     };
     // Whether keys of a tile are absent, or some rows of the workgroup do not see some.
     const auto special = [&](int t, uint64_t now) { return now != kAll || u.lo + (t + 1) * kTile > some; };
@@ -380,9 +383,10 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
     // same one slot later.  A wave issues behind its softmax, where it has time to wait for the memory path: the first waves
     // issue(t) in slot 2 t + 1, the others in slot 2 t; all land(t) in slot 2 t + 1, where issue(t - 2) is behind any of them.  K of tile t
     // is read in slots 2 t and 2 t + 1, V in 2 t + 2 and 2 t + 3; K of t + 3 and V of t + 2 take the places of t - 1 and t - 2, last read in
-    // slot 2 t - 1; so do codes' tiles, K of t + 1 and V of t made in slot 2 t + 1.  A wave reads its entries of t + 3 in issue(t), behind
+    // slot 2 t - 1; so do codes' tiles, K of t + 1 and V of t made in slot 2 t + 1.  A wave reads its entries of t + 4 in issue(t), behind
     // land(t - 1), to which those of issue(t - 3) have come.
-    landed<0>();               // the first three tiles' entries (and the queries)
+    landed<0>();               // the first four tiles' entries (and the queries)
+    prepare(-3);
     for (int t = -3; t < 0; ++t) issue(t);
     land(-1);
     dev::lds_barrier();
