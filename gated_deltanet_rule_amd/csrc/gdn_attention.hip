@@ -27,27 +27,40 @@ namespace {
 using dev::f32x4_t;
 using dev::u32x4_t;
 
-constexpr int kThreads = 256, kWaves = 4, kTile = 32;
+constexpr int kJoinThreads = 256, kTile = 32;
 
-// V's rows in LDS: bf16 rows are D values, their 16-byte chunks exchanged by key so that neither the
-// stores (16 keys, one chunk) nor the transposing loads (4 keys, two chunks to a group of 16 lanes)
-// meet in a bank; fp32 rows are padded by four.
+// A tile of a wave in LDS, as values of T, in 16-byte chunks.  Chunks of a key are exchanged by the key, so that operands
+// (K: one chunk of 16 keys; V: two chunks of four keys to a group of 16 lanes) do not meet in a bank; V's rows are
+// padded instead where the elements are single words.
 template <typename T, int D>
-struct VTile {
-    static constexpr int kRow = sizeof(T) == 2 ? D * 2 : (D + 4) * 4;      // bytes
-    static constexpr int kBytes = kTile * kRow;
-    __device__ static __forceinline__ int chunk(int key, int c) {
-        if constexpr (sizeof(T) == 4) return key * kRow + c * 16;
-        else if constexpr (D >= 128) return key * kRow + ((c ^ ((2 * key) & 15)) * 16);
-        else return key * kRow + ((c ^ (key & 6)) * 16);
+struct Tile {
+    static constexpr int kRow = D * (int)sizeof(T), kChunks = kRow / 16;                     // of K
+    static constexpr int kVRow = sizeof(T) == 2 ? kRow : kRow + 16;
+    static constexpr int kV = kTile * kRow, kBytes = kV + kTile * kVRow;
+    __device__ static __forceinline__ int k(int key, int c) { return key * kRow + (c ^ (kChunks >= 16 ? key & 15 : key >> 1 & 7)) * 16; }
+    __device__ static __forceinline__ int v(int key, int c) {
+        if constexpr (sizeof(T) == 4) return kV + key * kVRow + c * 16;
+        else if constexpr (D >= 128) return kV + key * kVRow + ((c ^ ((2 * key) & 15)) * 16);
+        else return kV + key * kVRow + ((c ^ (key & 6)) * 16);
+    }
+    // first of the lane's eight dims of operand f of the scores; the last four of fp32 stand 16 further
+    __device__ static __forceinline__ int dim(int f, int lane) { return f * 32 + lane / 16 * (16 / (int)sizeof(T)); }
+    __device__ static __forceinline__ dev::frag_t<T> query(const T* q, int f, int lane) {
+        if constexpr (sizeof(T) == 2) return *reinterpret_cast<const dev::bf16x8_t*>(q + dim(f, lane));
+        else return __builtin_shufflevector(*reinterpret_cast<const f32x4_t*>(q + dim(f, lane)), *reinterpret_cast<const f32x4_t*>(q + dim(f, lane) + 16), 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+    __device__ static __forceinline__ dev::frag_t<T> load_k(const char* lds, int key, int f, int lane) {
+        if constexpr (sizeof(T) == 2) return *reinterpret_cast<const dev::bf16x8_t*>(lds + k(key, 4 * f + lane / 16));
+        else return __builtin_shufflevector(*reinterpret_cast<const f32x4_t*>(lds + k(key, 8 * f + lane / 16)),
+                                            *reinterpret_cast<const f32x4_t*>(lds + k(key, 8 * f + 4 + lane / 16)), 0, 1, 2, 3, 4, 5, 6, 7);
     }
     // V^T for dims 16 t .. 16 t + 15: lane % 16 is the dim, the eight keys 4 (lane / 16) + 0..3 of both halves of the tile
-    __device__ static __forceinline__ dev::frag_t<T> load(const char* lds, int t, int lane) {
+    __device__ static __forceinline__ dev::frag_t<T> load_v(const char* lds, int t, int lane) {
         if constexpr (sizeof(T) == 2) {
             const int key = 4 * (lane / 16) + lane % 16 / 4, c = 2 * t + (lane & 3) / 2;
             typedef __attribute__((address_space(3))) dev::s16x4_t* lds_ptr;
-            const auto a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(lds + chunk(key, c) + (lane & 1) * 8));
-            const auto b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(lds + chunk(key + 16, c) + (lane & 1) * 8));
+            const auto a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(lds + v(key, c) + (lane & 1) * 8));
+            const auto b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(lds + v(key + 16, c) + (lane & 1) * 8));
             const dev::bf16x4_t x = __builtin_bit_cast(dev::bf16x4_t, a), y = __builtin_bit_cast(dev::bf16x4_t, b);
             return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
         } else {
@@ -55,181 +68,175 @@ struct VTile {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int key = 16 * (j / 4) + 4 * (lane / 16) + j % 4;
-                f[j] = *reinterpret_cast<const float*>(lds + key * kRow + (16 * t + lane % 16) * 4);
+                f[j] = *reinterpret_cast<const float*>(lds + kV + key * kVRow + (16 * t + lane % 16) * 4);
             }
             return f;
         }
     }
-    __device__ static __forceinline__ float at(const char* lds, int key, int dim) {
-        return (float)*reinterpret_cast<const T*>(lds + chunk(key, dim * (int)sizeof(T) / 16) + dim * (int)sizeof(T) % 16);
+    __device__ static __forceinline__ T& v_at(char* lds, int key, int dim) {
+        return *reinterpret_cast<T*>(lds + v(key, dim * (int)sizeof(T) / 16) + dim * (int)sizeof(T) % 16);
     }
 };
 
-// What a lane holds of one key for one tile: its 16-byte pieces of the stored row and the operands they make.
-// Piece i of lane l is bytes 64 i + 16 (l / 16) of the head's row.
-template <typename T, int FORMAT, int D>
-struct Stored {
-    static constexpr bool kCodes = FORMAT != GDN_CACHE_PLAIN;
-    static constexpr int kElem = kCodes ? 1 : (int)sizeof(T);
-    static constexpr int kPieces = D * kElem / 64;
-    static constexpr int kFrags = D / 32;
-    // operand f of the contraction over dims: eight dims for each lane
-    __device__ static __forceinline__ int dim(int f, int lane) {
-        if constexpr (kCodes) return f / 2 * 64 + lane / 16 * 16 + f % 2 * 8;
-        else if constexpr (sizeof(T) == 2) return f * 32 + lane / 16 * 8;
-        else return f * 32 + lane / 16 * 4;         // two pieces, 16 dims apart
-    }
-    __device__ static __forceinline__ dev::frag_t<T> frag(const u32x4_t (&p)[kPieces], int f) {
-        if constexpr (kCodes) return dev::codes8<T, FORMAT>(p[f / 2][f % 2 * 2], p[f / 2][f % 2 * 2 + 1]);
-        else if constexpr (sizeof(T) == 2) return __builtin_bit_cast(dev::bf16x8_t, p[f]);
-        else {
-            const f32x4_t x = __builtin_bit_cast(f32x4_t, p[2 * f]), y = __builtin_bit_cast(f32x4_t, p[2 * f + 1]);
-            return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
-        }
-    }
-    // the query's operand f: the same dims
-    __device__ static __forceinline__ dev::frag_t<T> query(const T* q, int f, int lane) {
-        if constexpr (sizeof(T) == 2) return *reinterpret_cast<const dev::bf16x8_t*>(q + dim(f, lane));
-        else {
-            const int second = kCodes ? 4 : 16;
-            const f32x4_t x = *reinterpret_cast<const f32x4_t*>(q + dim(f, lane)), y = *reinterpret_cast<const f32x4_t*>(q + dim(f, lane) + second);
-            return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
-        }
-    }
-};
-
-template <typename T, int FORMAT, int D>
-__device__ __forceinline__ void load_pieces(const void* cache, int64_t head, int lane, u32x4_t (&p)[Stored<T, FORMAT, D>::kPieces]) {
-    using S = Stored<T, FORMAT, D>;
-    const char* at = static_cast<const char*>(cache) + head * (D * S::kElem) + lane / 16 * 16;
-#pragma unroll
-    for (int i = 0; i < S::kPieces; ++i) p[i] = *reinterpret_cast<const u32x4_t*>(at + 64 * i);
-}
-
-// A piece's values into V's tile in LDS; with `clean`, what is not finite as zero.  Returns whether all were finite.
-template <typename T, int FORMAT, int D>
-__device__ __forceinline__ bool stage(char* lds, int key, int lane, const u32x4_t (&p)[Stored<T, FORMAT, D>::kPieces], bool present, bool clean) {
-    using S = Stored<T, FORMAT, D>;
-    bool fine = true;
-#pragma unroll
-    for (int i = 0; i < S::kPieces; ++i) {
-        if constexpr (S::kCodes) {
-            T v[16];
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                T c[4];
-                dev::codes4<T, FORMAT>(p[i][w], c);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v[4 * w + j] = c[j];
-            }
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const bool ok = dev::finite((float)v[j]);
-                fine &= ok || !present;
-                if (!present || (clean && !ok)) v[j] = (T)0.f;
-            }
-            constexpr int N = 16 / (int)sizeof(T);
-            const int first = (64 * i + lane / 16 * 16) * (int)sizeof(T) / 16;
-#pragma unroll
-            for (int c = 0; c < (int)sizeof(T); ++c) {
-                u32x4_t w;
-                __builtin_memcpy(&w, v + c * N, 16);
-                *reinterpret_cast<u32x4_t*>(lds + VTile<T, D>::chunk(key, first + c)) = w;
-            }
-        } else {
-            constexpr int N = 16 / (int)sizeof(T);
-            T v[N];
-            __builtin_memcpy(v, &p[i], 16);
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                const bool ok = dev::finite((float)v[j]);
-                fine &= ok || !present;
-                if (!present || (clean && !ok)) v[j] = (T)0.f;
-            }
-            u32x4_t w;
-            __builtin_memcpy(&w, v, 16);
-            *reinterpret_cast<u32x4_t*>(lds + VTile<T, D>::chunk(key, 4 * i + lane / 16)) = w;
-        }
-    }
-    return fine;
-}
-
-// LDS of a workgroup: V's tiles of the four waves, which the waves' sums share at the end; then the
-// waves' scales and statistics.
+// LDS of a workgroup: a tile of each wave, which the waves' sums share at the end; then the waves' scales and statistics.
 template <typename T, int D>
 struct Lds {
-    static constexpr int kSum = 16 * (D + 4) * 4;              // 16 rows of a wave's sums
-    static constexpr int kWave = VTile<T, D>::kBytes > kSum ? VTile<T, D>::kBytes : kSum;
+    static constexpr int kWaves = sizeof(T) == 4 && D == 256 ? 2 : 4, kThreads = 64 * kWaves;      // (66 KB to a wave there)
+    static constexpr int kWave = Tile<T, D>::kBytes;
     static constexpr int kScales = kWaves * 2 * kTile * 4;
     static constexpr int kTotal = kWaves * kWave + kScales + kWaves * 16 * 8;
 };
 
 template <typename T, int FORMAT, int D, int NT>
 __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit& u, char* lds) {
-    using S = Stored<T, FORMAT, D>;
-    constexpr int kDims = D / 16;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane % 16, quad = lane / 16, G = (int)k.group.d;
-    char* const vt = lds + wave * Lds<T, D>::kWave;
+    using Tl = Tile<T, D>;
+    constexpr int kWaves = Lds<T, D>::kWaves, kThreads = Lds<T, D>::kThreads;
+    constexpr bool kCodes = FORMAT != GDN_CACHE_PLAIN;
+    constexpr int kRowBytes = D * (kCodes ? 1 : (int)sizeof(T));
+    constexpr int kPieces = kRowBytes / 16, kKeys = 64 / kPieces, kLoads = kTile / kKeys;        // a load of a wave takes kKeys whole rows
+    constexpr int kDims = D / 16, kFrags = D / 32;
+    if (u.lo >= u.hi) {        // a table or a cache without rows: no address may be formed
+        fill_rows<T, D>(k, u, 16 * NT, kThreads, 0.f);
+        return;
+    }
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane % 16, quad = lane / 16, G = (int)k.group.d;
+    char* const tile = lds + wave * Lds<T, D>::kWave;
     float* const scales = reinterpret_cast<float*>(lds + kWaves * Lds<T, D>::kWave) + wave * 2 * kTile;
     float2* const stats = reinterpret_cast<float2*>(lds + kWaves * Lds<T, D>::kWave + Lds<T, D>::kScales);
     const dev::Pages pages = {k.a.table + (int64_t)u.seq * k.a.table_width, k.a.table_width, k.block, k.a.cache.num_rows};
     const int H = k.a.cache.num_heads;
     const float c = k.a.scale * kLog2e;
 
-    dev::frag_t<T> q[NT][S::kFrags];
+    // ---- loads: the lane's key and its page's entry (in flight) two tiles ahead, values one.  Lanes l and l + 32 hold the same key.
+    int entry = -1, key = 0, row = -1;
+    const auto lookup = [&](int p0) {
+        key = p0 + (lane & 31);
+        const unsigned page = dev::divide((unsigned)key, k.block);
+        entry = pages.table[page < (unsigned)pages.width ? page : (unsigned)pages.width - 1];
+    };
+    const auto row_of = [&]() {
+        const unsigned page = dev::divide((unsigned)key, k.block);
+        const int64_t at = (int64_t)entry * k.block.d + ((unsigned)key - page * k.block.d);
+        return key < u.hi && page < (unsigned)pages.width && entry >= 0 && at < pages.num_rows ? (int)at : -1;
+    };
+    u32x4_t kp[kLoads], vp[kLoads];
+    float scale = 0.f;                                  // of the lane's key: K's in the lower half of the wave, V's in the upper
+    const auto load = [&]() {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int r = __shfl(row, i * kKeys + lane / kPieces);
+            const uint64_t at = (uint64_t)(unsigned)(r < 0 ? 0 : r) * (unsigned)(H * kRowBytes) + (unsigned)(u.h * kRowBytes + lane % kPieces * 16);
+            kp[i] = *reinterpret_cast<const u32x4_t*>(static_cast<const char*>(k.a.cache.k) + at);
+            vp[i] = *reinterpret_cast<const u32x4_t*>(static_cast<const char*>(k.a.cache.v) + at);
+        }
+        if constexpr (kCodes) scale = row >= 0 ? (lane < 32 ? k.a.cache.k_scale : k.a.cache.v_scale)[(int64_t)row * H + u.h] : 0.f;
+    };
+    // What was loaded, in LDS as values; keys that are absent as zeros.
+    const auto stage = [&](uint32_t present) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int n = i * kKeys + lane / kPieces, first = lane % kPieces;
+            u32x4_t v = vp[i];
+            if (present != 0xffffffffu && !(present >> n & 1)) v = u32x4_t{};
+            if constexpr (!kCodes) {
+                *reinterpret_cast<u32x4_t*>(tile + Tl::k(n, first)) = kp[i];
+                *reinterpret_cast<u32x4_t*>(tile + Tl::v(n, first)) = v;
+            } else {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const dev::frag_t<T> a = dev::codes8<T, FORMAT>(kp[i][2 * x], kp[i][2 * x + 1]), b = dev::codes8<T, FORMAT>(v[2 * x], v[2 * x + 1]);
+                    if constexpr (sizeof(T) == 2) {
+                        *reinterpret_cast<dev::bf16x8_t*>(tile + Tl::k(n, 2 * first + x)) = a;
+                        *reinterpret_cast<dev::bf16x8_t*>(tile + Tl::v(n, 2 * first + x)) = b;
+                    } else {
+                        *reinterpret_cast<f32x4_t*>(tile + Tl::k(n, 4 * first + 2 * x)) = __builtin_shufflevector(a, a, 0, 1, 2, 3);
+                        *reinterpret_cast<f32x4_t*>(tile + Tl::k(n, 4 * first + 2 * x + 1)) = __builtin_shufflevector(a, a, 4, 5, 6, 7);
+                        *reinterpret_cast<f32x4_t*>(tile + Tl::v(n, 4 * first + 2 * x)) = __builtin_shufflevector(b, b, 0, 1, 2, 3);
+                        *reinterpret_cast<f32x4_t*>(tile + Tl::v(n, 4 * first + 2 * x + 1)) = __builtin_shufflevector(b, b, 4, 5, 6, 7);
+                    }
+                }
+            }
+        }
+        if constexpr (kCodes) scales[lane] = lane < 32 ? scale * c : scale;
+    };
+    int p0 = u.lo + wave * kTile;
+    const bool any = p0 < u.hi;
+    if (any) {
+        lookup(p0);
+        row = row_of();
+        load();
+    }
+    uint32_t present = (uint32_t)__ballot(row >= 0);
+    lookup(p0 + kWaves * kTile);
+
+    dev::frag_t<T> q[NT][kFrags];
     dev::Sees sees[NT];
-    int some = 0x7fffffff;                     // every row sees the keys below this
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         const int r = u.row0 + 16 * n + col, t = (int)dev::divide(r, k.group);
-        const bool live = r < u.rows;
         sees[n] = {0, 0, 0};
-        if (live) {
+        if (r < u.rows) {
             const T* p = static_cast<const T*>(k.a.q) + (u.first + t) * k.a.q_stride + (int64_t)(u.h * G + (r - t * G)) * D;
 #pragma unroll
-            for (int f = 0; f < S::kFrags; ++f) q[n][f] = S::query(p, f, lane);
+            for (int f = 0; f < kFrags; ++f) q[n][f] = Tl::query(p, f, lane);
             sees[n] = row_sees(k, u, r);
         } else {
 #pragma unroll
-            for (int f = 0; f < S::kFrags; ++f) q[n][f] = dev::frag_t<T>{};
+            for (int f = 0; f < kFrags; ++f) q[n][f] = dev::frag_t<T>{};
         }
+        // waited for here: in the loop the wait would be for the tile on its way as well
+#pragma unroll
+        for (int f = 0; f < kFrags; ++f) asm volatile("" : "+v"(q[n][f]));
+        asm volatile("" : "+v"(sees[n].all), "+v"(sees[n].first), "+v"(sees[n].mask));
     }
-    some = k.a.tree_mask ? u.past : u.past + (int)dev::divide(u.row0, k.group) + 1;
+    const int some = k.a.tree_mask ? u.past : u.past + (int)dev::divide(u.row0, k.group) + 1;        // every row sees the keys below
 
     f32x4_t o[NT][kDims] = {};
     float m[NT], l[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) { m[n] = -INFINITY; l[n] = 0.f; }
 
-    for (int p0 = u.lo + wave * kTile; p0 < u.hi; p0 += kWaves * kTile) {
-        // the lane's two keys
-        int64_t row[2];
+    for (; p0 < u.hi; p0 += kWaves * kTile) {
+        const bool partial = present != 0xffffffffu || p0 + kTile > some;
+        stage(present);
+        uint32_t seen[NT];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            const int p = p0 + 16 * b + col;
-            row[b] = p < u.hi ? pages.row(p) : -1;
-        }
-        const bool there[2] = {row[0] >= 0, row[1] >= 0};
-        u32x4_t kp[2][S::kPieces], vp[2][S::kPieces];
+        for (int n = 0; n < NT; ++n) seen[n] = partial ? (uint32_t)sees[n].from(p0) & present : 0xffffffffu;
+        // Where some rows do not see some keys, no value that is not finite may meet a weight of zero: it is added to the
+        // rows that see it, and stands as zero in the product.
+        if (partial) {
+            constexpr int kOfChunk = 16 / (int)sizeof(T);
+            bool fine = !kCodes || dev::finite(scale);
+            for (int i = lane; i < kTile * Tl::kChunks; i += 64) {
+                const T* const v = &Tl::v_at(tile, i / Tl::kChunks, i % Tl::kChunks * kOfChunk);
 #pragma unroll
-        for (int b = 0; b < 2; ++b) load_pieces<T, FORMAT, D>(k.a.cache.k, (there[b] ? row[b] : 0) * H + u.h, lane, kp[b]);
+                for (int j = 0; j < kOfChunk; ++j) fine &= dev::finite((float)v[j]);
+            }
+            if (__any(!fine)) {
+                for (int n = 0; n < kTile; ++n) {
+                    if (!(present >> n & 1)) continue;
+                    const bool no = kCodes && !dev::finite(scales[kTile + n]);
 #pragma unroll
-        for (int b = 0; b < 2; ++b) load_pieces<T, FORMAT, D>(k.a.cache.v, (there[b] ? row[b] : 0) * H + u.h, lane, vp[b]);
-        float vscale[2] = {1.f, 1.f};
-        if constexpr (S::kCodes) {
+                    for (int t = 0; t < kDims; ++t)
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const float ks = there[b] ? k.a.cache.k_scale[row[b] * H + u.h] : 0.f;
-                vscale[b] = there[b] ? k.a.cache.v_scale[row[b] * H + u.h] : 0.f;
-                if (quad == 0) {
-                    scales[16 * b + col] = ks * c;
-                    scales[kTile + 16 * b + col] = vscale[b];
+                        for (int i = 0; i < 4; ++i) {
+                            const float v = no ? NAN : (float)Tl::v_at(tile, n, 16 * t + 4 * quad + i);
+#pragma unroll
+                            for (int x = 0; x < NT; ++x)
+                                if (!dev::finite(v) && (seen[x] >> n & 1)) o[x][t][i] += v;
+                        }
                 }
+                for (int i = lane; i < kTile * D; i += 64)
+                    if (!dev::finite((float)Tl::v_at(tile, i / D, i % D))) Tl::v_at(tile, i / D, i % D) = (T)0.f;
+                if (kCodes && lane >= 32 && !dev::finite(scale)) scales[lane] = 0.f;
             }
         }
-        // keys that are there, as bits
-        const uint32_t present = (uint32_t)(__ballot(there[0]) & 0xffff) | (uint32_t)(__ballot(there[1]) & 0xffff) << 16;
-        const bool partial = present != 0xffffffffu || p0 + kTile > some;
+        if (p0 + kWaves * kTile < u.hi) {
+            row = row_of();
+            present = (uint32_t)__ballot(row >= 0);
+            load();
+            lookup(p0 + 2 * kWaves * kTile);
+        }
 
         f32x4_t s[NT][2];
 #pragma unroll
@@ -237,23 +244,21 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
 #pragma unroll
             for (int b = 0; b < 2; ++b) s[n][b] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int f = 0; f < S::kFrags; ++f)
+        for (int f = 0; f < kFrags; ++f)
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                const dev::frag_t<T> kf = S::frag(kp[b], f);
+                const dev::frag_t<T> kf = Tl::load_k(tile, 16 * b + col, f, lane);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) s[n][b] = dev::mma16(kf, q[n][f], s[n][b]);
             }
-        uint32_t seen[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) seen[n] = partial ? (uint32_t)sees[n].from(p0) & present : 0xffffffffu;
+        dev::frag_t<T> w[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             float top = -INFINITY;
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 f32x4_t by = {c, c, c, c};
-                if constexpr (S::kCodes) by = *reinterpret_cast<const f32x4_t*>(scales + 16 * b + 4 * quad);
+                if constexpr (kCodes) by = *reinterpret_cast<const f32x4_t*>(scales + 16 * b + 4 * quad);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     s[n][b][i] *= by[i];
@@ -262,9 +267,10 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
                 }
             }
             top = dev::across_max(top);
-            const float next = fmaxf(m[n], top);
+            // kept until it is short by 2^8, which sums and weights take as well: the sums are seldom scaled
+            const float next = top > m[n] + 8.f ? top : m[n];
             if (__any(next > m[n])) {
-                const float keep = m[n] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[n] - next);
+                const float keep = m[n] == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m[n] - next);        // (no sums yet)
                 l[n] *= keep;
 #pragma unroll
                 for (int t = 0; t < kDims; ++t)
@@ -272,48 +278,11 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
                     for (int i = 0; i < 4; ++i) o[n][t][i] *= keep;
                 m[n] = next;
             }
-        }
-        // V: through the wave's LDS.  Where some rows do not see some keys, what is not finite must not meet a weight of zero:
-        // it is added to the rows that see it, and stands as zero in the product.
-        bool fine = true;
-#pragma unroll
-        for (int b = 0; b < 2; ++b) fine &= stage<T, FORMAT, D>(vt, 16 * b + col, lane, vp[b], there[b], false);
-        if (partial) {
-            fine &= dev::finite(vscale[0]) && dev::finite(vscale[1]);
-            uint64_t bad = __ballot(!fine);
-            if (bad) {
-                bad |= bad >> 32;
-                bad |= bad >> 16;
-                for (int key = 0; key < kTile; ++key) {
-                    if (!(bad >> (key % 16) & 1)) continue;
-                    float vs = 1.f;
-                    if constexpr (S::kCodes) vs = scales[kTile + key];
-#pragma unroll
-                    for (int t = 0; t < kDims; ++t)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            float v = VTile<T, D>::at(vt, key, 16 * t + 4 * quad + i);
-                            if (!dev::finite(vs)) v = NAN;
-#pragma unroll
-                            for (int n = 0; n < NT; ++n)
-                                if (!dev::finite(v) && (seen[n] >> key & 1)) o[n][t][i] += v;
-                        }
-                }
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    stage<T, FORMAT, D>(vt, 16 * b + col, lane, vp[b], there[b], true);
-                    if (S::kCodes && quad == 0 && !dev::finite(vscale[b])) scales[kTile + 16 * b + col] = 0.f;
-                }
-            }
-        }
-        dev::frag_t<T> w[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
             const float base = m[n] == -INFINITY ? 0.f : m[n];
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 f32x4_t by = {1.f, 1.f, 1.f, 1.f};
-                if constexpr (S::kCodes) by = *reinterpret_cast<const f32x4_t*>(scales + kTile + 16 * b + 4 * quad);
+                if constexpr (kCodes) by = *reinterpret_cast<const f32x4_t*>(scales + kTile + 16 * b + 4 * quad);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float x = __builtin_amdgcn_exp2f(s[n][b][i] - base);
@@ -324,32 +293,34 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
         }
 #pragma unroll
         for (int t = 0; t < kDims; ++t) {
-            const dev::frag_t<T> vf = VTile<T, D>::load(vt, t, lane);
+            const dev::frag_t<T> vf = Tl::load_v(tile, t, lane);
 #pragma unroll
             for (int n = 0; n < NT; ++n) o[n][t] = dev::mma16(vf, w[n], o[n][t]);
         }
     }
 
-    // the four waves' sums, 16 rows at a time
+    // the waves' sums, 16 rows at a time
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         l[n] = dev::across_sum(l[n]);
         __syncthreads();
-        float* const mine = reinterpret_cast<float*>(vt);
+        float* const mine = reinterpret_cast<float*>(tile);
 #pragma unroll
         for (int t = 0; t < kDims; ++t) *reinterpret_cast<f32x4_t*>(mine + col * (D + 4) + 16 * t + 4 * quad) = o[n][t];
         if (quad == 0) stats[wave * 16 + col] = {m[n], l[n]};
         __syncthreads();
-        const int r = threadIdx.x / 16, row = u.row0 + 16 * n + r;
-        float top = -INFINITY, sum = 0.f, by[kWaves];
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) top = fmaxf(top, stats[w * 16 + r].x);
+        for (int r = threadIdx.x / 16; r < 16; r += kThreads / 16) {
+            const int row = u.row0 + 16 * n + r;
+            if (row >= u.rows) break;
+            float top = -INFINITY, sum = 0.f, by[kWaves];
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            by[w] = top == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(stats[w * 16 + r].x - top);
-            sum += by[w] * stats[w * 16 + r].y;
-        }
-        if (row < u.rows) {
+            for (int w = 0; w < kWaves; ++w) top = fmaxf(top, stats[w * 16 + r].x);
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                by[w] = top == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(stats[w * 16 + r].x - top);
+                sum += by[w] * stats[w * 16 + r].y;
+            }
             const int t = (int)dev::divide(row, k.group);
             const int64_t at = (u.first + t) * k.a.H_q + u.h * G + (row - t * G);
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -359,7 +330,6 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
                 f32x4_t x = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int w = 0; w < kWaves; ++w) {
-                    // a wave without keys holds zeros: nothing of it is taken
                     const f32x4_t v = *reinterpret_cast<const f32x4_t*>(reinterpret_cast<const float*>(lds + w * Lds<T, D>::kWave) + r * (D + 4) + dim);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) x[i] += by[w] * v[i];
@@ -377,15 +347,19 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
     }
 }
 
+// Workgroups (as waves to a SIMD) of a compute unit: two if LDS holds them and 256 registers a wave's sums, queries and tile.
+template <typename T, int D, int NT>
+constexpr int workgroups() { return 2 * Lds<T, D>::kTotal <= 160 * 1024 && NT * D <= 256 ? 2 : 1; }
+
 template <typename T, int FORMAT, int D, int NT>
-__global__ __launch_bounds__(kThreads) void decode_kernel(AttentionKernelArgs k) {
+__global__ __launch_bounds__((Lds<T, D>::kThreads), (workgroups<T, D, NT>())) void decode_kernel(AttentionKernelArgs k) {
     extern __shared__ __align__(16) char lds[];
     Unit u;
-    if (decode_unit<T, D>(k, 16 * NT, kThreads, u)) attend<T, FORMAT, D, NT>(k, u, lds);
+    if (decode_unit<T, D>(k, 16 * NT, Lds<T, D>::kThreads, u)) attend<T, FORMAT, D, NT>(k, u, lds);
 }
 
 template <typename T, int FORMAT, int D, int NT>
-__global__ __launch_bounds__(kThreads) void prompt_kernel(AttentionKernelArgs k) {
+__global__ __launch_bounds__((Lds<T, D>::kThreads), (workgroups<T, D, NT>())) void prompt_kernel(AttentionKernelArgs k) {
     extern __shared__ __align__(16) char lds[];
     const unsigned H = (unsigned)k.a.cache.num_heads, tile = blockIdx.x / H;
     Unit u;
@@ -394,8 +368,8 @@ __global__ __launch_bounds__(kThreads) void prompt_kernel(AttentionKernelArgs k)
 
 // A row's spans joined: one wave for each query head of a token.
 template <typename T, int D>
-__global__ __launch_bounds__(kThreads) void join_kernel(AttentionKernelArgs k) {
-    const int64_t at = (int64_t)blockIdx.x * (kThreads / 64) + threadIdx.x / 64;
+__global__ __launch_bounds__(kJoinThreads) void join_kernel(AttentionKernelArgs k) {
+    const int64_t at = (int64_t)blockIdx.x * (kJoinThreads / 64) + threadIdx.x / 64;
     const int lane = threadIdx.x & 63;
     if (at >= k.a.total_tokens * k.a.H_q) return;
     const int64_t token = at / k.a.H_q;
@@ -447,8 +421,8 @@ hipError_t launch_rows(AttentionKernelArgs k, hipStream_t stream) {
     const int rows = k.a.tokens_per_row * (int)k.group.d;
     k.row_tiles = (rows + 16 * NT - 1) / (16 * NT);
     const int64_t blocks = ((int64_t)k.a.num_seqs * k.spans * k.a.cache.num_heads + 7) / 8 * 8 * k.row_tiles;
-    if (!grid_fits(blocks, kThreads)) return hipErrorInvalidConfiguration;
-    decode_kernel<T, FORMAT, D, NT><<<(unsigned)blocks, kThreads, Lds<T, D>::kTotal, stream>>>(k);
+    if (!grid_fits(blocks, Lds<T, D>::kThreads)) return hipErrorInvalidConfiguration;
+    decode_kernel<T, FORMAT, D, NT><<<(unsigned)blocks, Lds<T, D>::kThreads, Lds<T, D>::kTotal, stream>>>(k);
     return hipGetLastError();
 }
 
@@ -458,8 +432,8 @@ hipError_t launch_decode(const AttentionArgs& a, hipStream_t stream) {
     const int rows = a.tokens_per_row * (int)k.group.d;
     k.rows = Divisor((uint32_t)a.tokens_per_row);
     k.spans = most_spans(rows, k.a.max_keys);
-    const int64_t heads = a.total_tokens * a.H_q, joins = (heads + kThreads / 64 - 1) / (kThreads / 64);
-    if (!grid_fits(joins, kThreads)) return hipErrorInvalidConfiguration;
+    const int64_t heads = a.total_tokens * a.H_q, joins = (heads + kJoinThreads / 64 - 1) / (kJoinThreads / 64);
+    if (!grid_fits(joins, kJoinThreads)) return hipErrorInvalidConfiguration;
     k.part = static_cast<float*>(a.workspace);
     k.stats = reinterpret_cast<float2*>(k.part + (k.spans > 1 ? heads * k.spans * D : 0));
     // as many row tiles to a wave as the rows fill and the registers hold
@@ -470,7 +444,7 @@ hipError_t launch_decode(const AttentionArgs& a, hipStream_t stream) {
     else if (rows <= 32 || most == 2) e = launch_rows<T, FORMAT, D, (most > 1 ? 2 : 1)>(k, stream);
     else e = launch_rows<T, FORMAT, D, (most > 2 ? 4 : 1)>(k, stream);
     if (e != hipSuccess || k.spans == 1) return e;
-    join_kernel<T, D><<<(unsigned)joins, kThreads, 0, stream>>>(k);
+    join_kernel<T, D><<<(unsigned)joins, kJoinThreads, 0, stream>>>(k);
     return hipGetLastError();
 }
 
@@ -479,8 +453,8 @@ hipError_t launch_prompt(const AttentionArgs& a, hipStream_t stream) {
     constexpr int NT = D <= 64 ? 4 : (D <= 128 ? 2 : 1);
     const AttentionKernelArgs k = kernel_args(a);
     const int64_t tiles = a.total_tokens * (int)k.group.d / (16 * NT) + a.num_seqs, blocks = tiles * a.cache.num_heads;
-    if (!grid_fits(blocks, kThreads) || a.total_tokens * (int64_t)k.group.d > 0x7fffffffLL) return hipErrorInvalidConfiguration;
-    prompt_kernel<float, FORMAT, D, NT><<<(unsigned)blocks, kThreads, Lds<float, D>::kTotal, stream>>>(k);
+    if (!grid_fits(blocks, Lds<float, D>::kThreads) || a.total_tokens * (int64_t)k.group.d > 0x7fffffffLL) return hipErrorInvalidConfiguration;
+    prompt_kernel<float, FORMAT, D, NT><<<(unsigned)blocks, Lds<float, D>::kThreads, Lds<float, D>::kTotal, stream>>>(k);
     return hipGetLastError();
 }
 
