@@ -366,35 +366,46 @@ __global__ __launch_bounds__((Lds<T, D>::kThreads), (workgroups<T, D, NT>())) vo
     if (prompt_unit(k, 16 * NT, (int)tile, (int)(blockIdx.x - tile * H), u)) attend<T, FORMAT, D, NT>(k, u, lds);
 }
 
-// A row's spans joined: one wave for each query head of a token.
+// A row's spans joined: a workgroup for each query head of a token, whose four waves take every fourth span.
 template <typename T, int D>
 __global__ __launch_bounds__(kJoinThreads) void join_kernel(AttentionKernelArgs k) {
-    const int64_t at = (int64_t)blockIdx.x * (kJoinThreads / 64) + threadIdx.x / 64;
-    const int lane = threadIdx.x & 63;
-    if (at >= k.a.total_tokens * k.a.H_q) return;
-    const int64_t token = at / k.a.H_q;
-    const int keys = row_keys(k.a, k.a.past[dev::divide((unsigned)token, k.rows)]);
+    constexpr int N = D / 64, kWaves = kJoinThreads / 64, kMost = kMaxSpans / kWaves;
+    __shared__ float sums[kWaves][D];
+    const unsigned at = blockIdx.x;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const unsigned token = at / (unsigned)k.a.H_q;
+    const int keys = row_keys(k.a, k.a.past[dev::divide(token, k.rows)]);
     if (keys <= 0 || keys > k.a.max_keys) return;
     const int span = span_keys(k.a.tokens_per_row * (int)k.group.d, keys), spans = (keys + span - 1) / span;
     if (spans == 1) return;
-    const float2 mine = lane < spans ? k.stats[at * k.spans + lane] : float2{-INFINITY, 0.f};
+    const float2 mine = lane < spans ? k.stats[(int64_t)at * k.spans + lane] : float2{-INFINITY, 0.f};
+    float x[N] = {}, v[kMost][N];
+    const float* p = k.part + (int64_t)at * k.spans * D + lane * N;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i)
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[i][j] = i * kWaves + wave < spans ? p[(i * kWaves + wave) * D + j] : 0.f;
     float top = mine.x;
 #pragma unroll
     for (int i = 1; i < 64; i *= 2) top = fmaxf(top, __shfl_xor(top, i));
     const float by = top == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mine.x - top);
     const float sum = dev::group_sum(by * mine.y, 64);
-    constexpr int N = D / 64;
-    float x[N] = {};
-    const float* p = k.part + at * k.spans * D + lane * N;
-    for (int s = 0; s < spans; ++s) {
-        const float f = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, by), s));
 #pragma unroll
-        for (int i = 0; i < N; ++i) x[i] += f * p[s * D + i];
+    for (int i = 0; i < kMost; ++i) {
+        const float f = __shfl(by, i * kWaves + wave);
+#pragma unroll
+        for (int j = 0; j < N; ++j) x[j] += f * v[i][j];
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    T* o = static_cast<T*>(k.a.o) + at * D + lane * N;
 #pragma unroll
-    for (int i = 0; i < N; ++i) o[i] = (T)(x[i] * inv);
+    for (int j = 0; j < N; ++j) sums[wave][lane * N + j] = x[j];
+    __syncthreads();
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    if ((int)threadIdx.x < D) {
+        float o = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) o += sums[w][threadIdx.x];
+        static_cast<T*>(k.a.o)[(int64_t)at * D + threadIdx.x] = (T)(o * inv);
+    }
 }
 
 // ---------------------------------------------------------------- launches
@@ -420,7 +431,7 @@ template <typename T, int FORMAT, int D, int NT>
 hipError_t launch_rows(AttentionKernelArgs k, hipStream_t stream) {
     const int rows = k.a.tokens_per_row * (int)k.group.d;
     k.row_tiles = (rows + 16 * NT - 1) / (16 * NT);
-    const int64_t blocks = ((int64_t)k.a.num_seqs * k.spans * k.a.cache.num_heads + 7) / 8 * 8 * k.row_tiles;
+    const int64_t blocks = ((int64_t)k.a.num_seqs * k.spans + 7) / 8 * 8 * k.a.cache.num_heads * k.row_tiles;
     if (!grid_fits(blocks, Lds<T, D>::kThreads)) return hipErrorInvalidConfiguration;
     decode_kernel<T, FORMAT, D, NT><<<(unsigned)blocks, Lds<T, D>::kThreads, Lds<T, D>::kTotal, stream>>>(k);
     return hipGetLastError();
@@ -432,8 +443,8 @@ hipError_t launch_decode(const AttentionArgs& a, hipStream_t stream) {
     const int rows = a.tokens_per_row * (int)k.group.d;
     k.rows = Divisor((uint32_t)a.tokens_per_row);
     k.spans = most_spans(rows, k.a.max_keys);
-    const int64_t heads = a.total_tokens * a.H_q, joins = (heads + kJoinThreads / 64 - 1) / (kJoinThreads / 64);
-    if (!grid_fits(joins, kJoinThreads)) return hipErrorInvalidConfiguration;
+    const int64_t heads = a.total_tokens * a.H_q;
+    if (!grid_fits(heads, kJoinThreads)) return hipErrorInvalidConfiguration;
     k.part = static_cast<float*>(a.workspace);
     k.stats = reinterpret_cast<float2*>(k.part + (k.spans > 1 ? heads * k.spans * D : 0));
     // as many row tiles to a wave as the rows fill and the registers hold
@@ -444,7 +455,7 @@ hipError_t launch_decode(const AttentionArgs& a, hipStream_t stream) {
     else if (rows <= 32 || most == 2) e = launch_rows<T, FORMAT, D, (most > 1 ? 2 : 1)>(k, stream);
     else e = launch_rows<T, FORMAT, D, (most > 2 ? 4 : 1)>(k, stream);
     if (e != hipSuccess || k.spans == 1) return e;
-    join_kernel<T, D><<<(unsigned)joins, kJoinThreads, 0, stream>>>(k);
+    join_kernel<T, D><<<(unsigned)heads, kJoinThreads, 0, stream>>>(k);
     return hipGetLastError();
 }
 

@@ -121,9 +121,11 @@ __device__ __forceinline__ bool finite(float x) { return fabsf(x) < INFINITY; }
 
 }  // namespace dev
 
-// Keys of a span of a long context: at least this many for so many rows of a head, doubled until kMaxSpans suffice.
+// Keys of a span of a long context: at least this many for so many rows of a head, doubled until kMaxSpans suffice.  Short
+// spans keep more of the chip busy for few requests, long ones start and join less often (16 rows of 128 dims in bf16 at
+// 256 / 512 / 1024 keys: one request of 1024 keys 9.5 / 12 / 17 us, 64 requests of up to 8192 keys 266 / 245 / 235 us).
 constexpr int kMaxSpans = 64;
-__host__ __device__ inline int least_span(int rows) { return rows <= 16 ? 256 : (rows <= 64 ? 512 : 1024); }
+__host__ __device__ inline int least_span(int rows) { return rows <= 16 ? 512 : (rows <= 64 ? 512 : 1024); }
 __host__ __device__ inline int span_keys(int rows, int keys) {
     int span = least_span(rows);
     while (keys > kMaxSpans * (int64_t)span) span *= 2;
@@ -188,10 +190,11 @@ __device__ __forceinline__ void fill_rows(const AttentionKernelArgs& k, const Un
 // attend to: a padding row's outputs are zeros then, those of a row with more keys than max_keys NaN.
 template <typename T, int D>
 __device__ __forceinline__ bool decode_unit(const AttentionKernelArgs& k, int per, int threads, Unit& u) {
-    // the row tiles of one span of keys stand 8 apart: on the same XCD, whose L2 then holds its keys
+    // The row tiles of one span of keys stand 8 apart: on the same XCD, whose L2 then holds its keys.  So do its heads, whose
+    // rows lie side by side: 58.4 -> 57.6 us for one request of 131072 keys in 8 bits, 240 -> 233 us for 64 in bf16.
     const unsigned id = blockIdx.x, tile = id / 8 % (unsigned)k.row_tiles, at = id / (8 * (unsigned)k.row_tiles) * 8 + id % 8;
-    const unsigned H = (unsigned)k.a.cache.num_heads, by_head = at / H, spans = (unsigned)k.spans;
-    u.h = (int)(at - by_head * H);
+    const unsigned H = (unsigned)k.a.cache.num_heads, group8 = at / (8 * H), by_head = group8 * 8 + at % 8, spans = (unsigned)k.spans;
+    u.h = (int)((at - group8 * 8 * H) / 8);
     u.seq = (int)(by_head / spans);
     u.span = (int)(by_head - (unsigned)u.seq * spans);
     if (u.seq >= k.a.num_seqs) return false;
