@@ -347,19 +347,23 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
     }
 }
 
-// Workgroups (as waves to a SIMD) of a compute unit: two if LDS holds them and 256 registers a wave's sums, queries and tile.
-template <typename T, int D, int NT>
-constexpr int workgroups() { return 2 * Lds<T, D>::kTotal <= 160 * 1024 && NT * D <= 256 ? 2 : 1; }
+// Most tiles of 16 rows to a wave: more spill.
+template <typename T, int D>
+constexpr int row_tiles() { return D == 256 ? 1 : (D == 128 || sizeof(T) == 4 ? 2 : 4); }
+
+// Workgroups (as waves to a SIMD) of a compute unit: two, with 256 registers, or one, with 512.
+template <typename T, int D>
+constexpr int workgroups() { return 2 * Lds<T, D>::kTotal <= 160 * 1024 ? 2 : 1; }
 
 template <typename T, int FORMAT, int D, int NT>
-__global__ __launch_bounds__((Lds<T, D>::kThreads), (workgroups<T, D, NT>())) void decode_kernel(AttentionKernelArgs k) {
+__global__ __launch_bounds__((Lds<T, D>::kThreads), (workgroups<T, D>())) void decode_kernel(AttentionKernelArgs k) {
     extern __shared__ __align__(16) char lds[];
     Unit u;
     if (decode_unit<T, D>(k, 16 * NT, Lds<T, D>::kThreads, u)) attend<T, FORMAT, D, NT>(k, u, lds);
 }
 
 template <typename T, int FORMAT, int D, int NT>
-__global__ __launch_bounds__((Lds<T, D>::kThreads), (workgroups<T, D, NT>())) void prompt_kernel(AttentionKernelArgs k) {
+__global__ __launch_bounds__((Lds<T, D>::kThreads), (workgroups<T, D>())) void prompt_kernel(AttentionKernelArgs k) {
     extern __shared__ __align__(16) char lds[];
     const unsigned H = (unsigned)k.a.cache.num_heads, tile = blockIdx.x / H;
     Unit u;
@@ -447,10 +451,11 @@ hipError_t launch_decode(const AttentionArgs& a, hipStream_t stream) {
     if (!grid_fits(heads, kJoinThreads)) return hipErrorInvalidConfiguration;
     k.part = static_cast<float*>(a.workspace);
     k.stats = reinterpret_cast<float2*>(k.part + (k.spans > 1 ? heads * k.spans * D : 0));
-    // as many row tiles to a wave as the rows fill and the registers hold
-    constexpr int most = (sizeof(T) == 2 ? 512 : 256) / D;
+    // as many row tiles to a wave as the rows fill and the registers hold; more rows share the keys in gdn_attention_wide.hip (two
+    // heads of 16 requests with 4096 keys, 48 / 64 rows here and 96 there: 61 / 64 and 36 us at 128 dims, where four tiles spill)
+    constexpr int most = row_tiles<T, D>();
     hipError_t e;
-    if (sizeof(T) == 2 && rows > 64) e = launch_attention_wide(k, stream);
+    if (sizeof(T) == 2 && rows > 16 * most) e = launch_attention_wide(k, stream);
     else if (rows <= 16 || most == 1) e = launch_rows<T, FORMAT, D, 1>(k, stream);
     else if (rows <= 32 || most == 2) e = launch_rows<T, FORMAT, D, (most > 1 ? 2 : 1)>(k, stream);
     else e = launch_rows<T, FORMAT, D, (most > 2 ? 4 : 1)>(k, stream);
@@ -459,14 +464,21 @@ hipError_t launch_decode(const AttentionArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-template <int FORMAT, int D>
-hipError_t launch_prompt(const AttentionArgs& a, hipStream_t stream) {
-    constexpr int NT = D <= 64 ? 4 : (D <= 128 ? 2 : 1);
-    const AttentionKernelArgs k = kernel_args(a);
-    const int64_t tiles = a.total_tokens * (int)k.group.d / (16 * NT) + a.num_seqs, blocks = tiles * a.cache.num_heads;
-    if (!grid_fits(blocks, Lds<float, D>::kThreads) || a.total_tokens * (int64_t)k.group.d > 0x7fffffffLL) return hipErrorInvalidConfiguration;
+template <int FORMAT, int D, int NT>
+hipError_t launch_prompt(const AttentionKernelArgs& k, hipStream_t stream) {
+    const int64_t tiles = k.a.total_tokens * (int)k.group.d / (16 * NT) + k.a.num_seqs, blocks = tiles * k.a.cache.num_heads;
+    if (!grid_fits(blocks, Lds<float, D>::kThreads) || k.a.total_tokens * (int64_t)k.group.d > 0x7fffffffLL) return hipErrorInvalidConfiguration;
     prompt_kernel<float, FORMAT, D, NT><<<(unsigned)blocks, Lds<float, D>::kThreads, Lds<float, D>::kTotal, stream>>>(k);
     return hipGetLastError();
+}
+
+// One row tile to a wave where two would leave compute units without work.
+template <int FORMAT, int D>
+hipError_t launch_prompt(const AttentionArgs& a, hipStream_t stream) {
+    constexpr int most = row_tiles<float, D>();
+    const AttentionKernelArgs k = kernel_args(a);
+    if (most == 1 || a.total_tokens * a.H_q <= 16 * most * 256) return launch_prompt<FORMAT, D, 1>(k, stream);
+    return launch_prompt<FORMAT, D, most>(k, stream);
 }
 
 template <typename T, int FORMAT, int D>
