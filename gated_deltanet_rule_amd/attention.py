@@ -142,10 +142,13 @@ def tree_masks(parents: Sequence[Sequence[int]], device=None) -> Tuple[torch.Ten
 
 # ---------------------------------------------------------------- rotary positions
 
-def _head_rows(t, name, dtype, device, tokens):
-    if t.dim() != 3:
-        raise ValueError("%s must have 3 dims, got shape %s" % (name, tuple(t.shape)))
-    return _rows(t, name, dtype, device, tokens, t.shape[1], t.shape[2])
+def _head_rows(t, name, dtype, device, tokens, heads, dim):
+    """layer._rows of [tokens, heads, dim], in one condition where the heads are dense."""
+    if t.dtype is dtype and t.get_device() == device.index and t.shape == (tokens, heads, dim):
+        row, head, one = t.stride()
+        if one == 1 and head == dim and tokens > 1:
+            return t.data_ptr(), row
+    return _rows(t, name, dtype, device, tokens, heads, dim)
 
 
 def gdn_rotary(q, k, positions, inv_freq, *, q_out=None, k_out=None, interleaved: bool = False, attention_factor: float = 1.0,
@@ -155,28 +158,33 @@ def gdn_rotary(q, k, positions, inv_freq, *, q_out=None, k_out=None, interleaved
     first = k if q is None else q
     if first is None:
         raise ValueError("q or k is required")
-    dev, dtype = _device(first, "k" if q is None else "q"), first.dtype
-    if first.dim() != 3:
-        raise ValueError("q and k must have 3 dims, got shape %s" % (tuple(first.shape),))
-    tokens, head_dim = first.shape[0], first.shape[2]
-    args, heads = [], []
-    for name, x, out in (("q", q, q_out), ("k", k, k_out)):
-        if x is None:
-            if out is not None:
-                raise ValueError("%s_out is given without %s" % (name, name))
-            args.append((None, 0, None, 0))
-            heads.append(0)
-            continue
-        if x.dim() != 3 or x.shape[2] != head_dim:
-            raise ValueError("q and k must be [T, heads, %d], %s is %s" % (head_dim, name, tuple(x.shape)))
-        p, stride = _rows(x, name, dtype, dev, tokens, x.shape[1], head_dim)
-        args.append((p, stride) + ((p, stride) if out is None else _rows(out, name + "_out", dtype, dev, tokens, x.shape[1], head_dim)))
-        heads.append(x.shape[1])
+    dev, dtype, size = _device(first, "k" if q is None else "q"), first.dtype, first.shape
+    if len(size) != 3:
+        raise ValueError("q and k must have 3 dims, got shape %s" % (tuple(size),))
+    tokens, q_heads, head_dim = size
+    pq = sq = oq = soq = pk = sk = ok = sok = None
+    k_heads = 0
+    if q is not None:
+        pq, sq = _head_rows(q, "q", dtype, dev, tokens, q_heads, head_dim)
+        oq, soq = (pq, sq) if q_out is None else _head_rows(q_out, "q_out", dtype, dev, tokens, q_heads, head_dim)
+    else:
+        q_heads = sq = soq = 0
+        if q_out is not None:
+            raise ValueError("q_out is given without q")
+    if k is not None:
+        if k.dim() != 3 or k.shape[2] != head_dim:
+            raise ValueError("q and k must be [T, heads, %d], k is %s" % (head_dim, tuple(k.shape)))
+        k_heads = k.shape[1]
+        pk, sk = _head_rows(k, "k", dtype, dev, tokens, k_heads, head_dim)
+        ok, sok = (pk, sk) if k_out is None else _head_rows(k_out, "k_out", dtype, dev, tokens, k_heads, head_dim)
+    else:
+        sk = sok = 0
+        if k_out is not None:
+            raise ValueError("k_out is given without k")
     if inv_freq.dim() != 1:
         raise ValueError("inv_freq must have 1 dim, got shape %s" % (tuple(inv_freq.shape),))
-    shape = GdnRotaryShape(heads[0], heads[1], head_dim, 2 * inv_freq.shape[0], _code(first, "q and k"), 1 if interleaved else 0,
+    shape = GdnRotaryShape(q_heads, k_heads, head_dim, 2 * inv_freq.shape[0], _code(first, "q and k"), 1 if interleaved else 0,
                            attention_factor)
-    (pq, sq, oq, soq), (pk, sk, ok, sok) = args
     _enqueue("gdn_rotary", dev, stream, shape, tokens, _dense(positions, "positions", torch.int32, dev, tokens),
              _dense(inv_freq, "inv_freq", torch.float32, dev, inv_freq.shape[0]), pq, sq, pk, sk, oq, soq, ok, sok)
 
@@ -197,9 +205,10 @@ def alloc_kv_cache(num_rows: int, num_heads: int, head_dim: int, dtype: torch.dt
 
 def _cache(k_cache, v_cache, k_scale, v_scale, like, device):
     """The C description of a cache for activations like `like`."""
-    if k_cache.dim() != 3:
-        raise ValueError("k_cache must have 3 dims, got shape %s" % (tuple(k_cache.shape),))
-    rows, heads, head_dim = k_cache.shape
+    size = k_cache.shape
+    if len(size) != 3:
+        raise ValueError("k_cache must have 3 dims, got shape %s" % (tuple(size),))
+    rows, heads, head_dim = size
     stored, dtype = k_cache.dtype, _code(like, "activations")
     form = GDN_CACHE_PLAIN if stored is like.dtype else _FORMAT_CODES.get(stored)
     if form is None:
@@ -222,8 +231,8 @@ def gdn_kv_cache_write(k, v, slots, k_cache, v_cache, *, k_scale=None, v_scale=N
     cache = _cache(k_cache, v_cache, k_scale, v_scale, k, dev)
     tokens = k.shape[0]
     shape = (tokens, cache.num_heads, cache.head_dim)
-    pk, sk = _rows(k, "k", k.dtype, dev, *shape)
-    pv, sv = _rows(v, "v", k.dtype, dev, *shape)
+    pk, sk = _head_rows(k, "k", k.dtype, dev, *shape)
+    pv, sv = _head_rows(v, "v", k.dtype, dev, *shape)
     _enqueue("gdn_kv_cache_write", dev, stream, cache, tokens, pk, sk, pv, sv, _dense(slots, "slots", torch.int64, dev, tokens))
 
 
@@ -241,14 +250,15 @@ def gdn_kv_cache_read(slots, k_cache, v_cache, k_out, v_out, *, k_scale=None, v_
 def _attention(q, k_cache, v_cache, k_scale, v_scale, o, kv_table, sequences):
     dev = _device(q, "q")
     cache = _cache(k_cache, v_cache, k_scale, v_scale, q, dev)
-    if q.dim() != 3 or q.shape[2] != cache.head_dim:
-        raise ValueError("q must be [T, heads, %d], got shape %s" % (cache.head_dim, tuple(q.shape)))
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != cache.head_dim:
+        raise ValueError("q must be [T, heads, %d], got shape %s" % (cache.head_dim, tuple(shape)))
     if kv_table.dim() != 2:
         raise ValueError("kv_table must have 2 dims, got shape %s" % (tuple(kv_table.shape),))
-    pq, sq = _rows(q, "q", q.dtype, dev, *q.shape)
+    pq, sq = _head_rows(q, "q", q.dtype, dev, *shape)
     width = kv_table.shape[1]
     return dev, cache, pq, sq, _dense(kv_table, "kv_table", torch.int32, dev, sequences, width), width, \
-        _dense(o, "o", q.dtype, dev, *q.shape)
+        _dense(o, "o", q.dtype, dev, *shape)
 
 
 def gdn_attention_prefill(q, k_cache, v_cache, o, cu_seqlens, start_pos, kv_table, *, kv_block: int, scale: float, k_scale=None,

@@ -27,16 +27,21 @@ namespace {
 using dev::f32x4_t;
 using dev::u32x4_t;
 
-constexpr int kJoinThreads = 256, kTile = 32;
+constexpr int kThreads = 256, kWaves = 4, kTile = 32;
 
-// A tile of a wave in LDS, as values of T, in 16-byte chunks.  Chunks of a key are exchanged by the key, so that operands
+// A wave's tiles of K and V in LDS, as values of T, in 16-byte chunks.  Chunks of a key are exchanged by the key, so that operands
 // (K: one chunk of 16 keys; V: two chunks of four keys to a group of 16 lanes) do not meet in a bank; V's rows are
 // padded instead where the elements are single words.
 template <typename T, int D>
 struct Tile {
     static constexpr int kRow = D * (int)sizeof(T), kChunks = kRow / 16;                     // of K
     static constexpr int kVRow = sizeof(T) == 2 ? kRow : kRow + 16;
-    static constexpr int kV = kTile * kRow, kBytes = kV + kTile * kVRow;
+    static constexpr int kSum = 16 * (D + 4) * 4;                                           // 16 rows of a wave's sums
+    // Where two tiles fit twice into LDS, V has a place of its own and is loaded and staged beside K, else it takes K's after
+    // the scores: 57.6 us beside and 65 after (131072 keys of 128 dims in 8 bits); but 44.5 and 42.1 (16 x 4096 keys of 256
+    // dims in bf16), 608 and 352 (a prompt of 2048 tokens, 256 dims in fp32, whose two tiles leave room for two waves).
+    static constexpr bool kBeside = kRow <= 256;
+    static constexpr int kV = kBeside ? kTile * kRow : 0, kUsed = kV + kTile * kVRow, kBytes = kUsed > kSum ? kUsed : kSum;
     __device__ static __forceinline__ int k(int key, int c) { return key * kRow + (c ^ (kChunks >= 16 ? key & 15 : key >> 1 & 7)) * 16; }
     __device__ static __forceinline__ int v(int key, int c) {
         if constexpr (sizeof(T) == 4) return kV + key * kVRow + c * 16;
@@ -81,7 +86,6 @@ struct Tile {
 // LDS of a workgroup: a tile of each wave, which the waves' sums share at the end; then the waves' scales and statistics.
 template <typename T, int D>
 struct Lds {
-    static constexpr int kWaves = sizeof(T) == 4 && D == 256 ? 2 : 4, kThreads = 64 * kWaves;      // (66 KB to a wave there)
     static constexpr int kWave = Tile<T, D>::kBytes;
     static constexpr int kScales = kWaves * 2 * kTile * 4;
     static constexpr int kTotal = kWaves * kWave + kScales + kWaves * 16 * 8;
@@ -90,7 +94,6 @@ struct Lds {
 template <typename T, int FORMAT, int D, int NT>
 __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit& u, char* lds) {
     using Tl = Tile<T, D>;
-    constexpr int kWaves = Lds<T, D>::kWaves, kThreads = Lds<T, D>::kThreads;
     constexpr bool kCodes = FORMAT != GDN_CACHE_PLAIN;
     constexpr int kRowBytes = D * (kCodes ? 1 : (int)sizeof(T));
     constexpr int kPieces = kRowBytes / 16, kKeys = 64 / kPieces, kLoads = kTile / kKeys;        // a load of a wave takes kKeys whole rows
@@ -121,53 +124,54 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
     };
     u32x4_t kp[kLoads], vp[kLoads];
     float scale = 0.f;                                  // of the lane's key: K's in the lower half of the wave, V's in the upper
-    const auto load = [&]() {
+    const auto load = [&](const void* cache, u32x4_t (&p)[kLoads]) {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             const int r = __shfl(row, i * kKeys + lane / kPieces);
             const uint64_t at = (uint64_t)(unsigned)(r < 0 ? 0 : r) * (unsigned)(H * kRowBytes) + (unsigned)(u.h * kRowBytes + lane % kPieces * 16);
-            kp[i] = *reinterpret_cast<const u32x4_t*>(static_cast<const char*>(k.a.cache.k) + at);
-            vp[i] = *reinterpret_cast<const u32x4_t*>(static_cast<const char*>(k.a.cache.v) + at);
+            p[i] = *reinterpret_cast<const u32x4_t*>(static_cast<const char*>(cache) + at);
         }
+    };
+    const auto load_scales = [&]() {
         if constexpr (kCodes) scale = row >= 0 ? (lane < 32 ? k.a.cache.k_scale : k.a.cache.v_scale)[(int64_t)row * H + u.h] : 0.f;
     };
-    // What was loaded, in LDS as values; keys that are absent as zeros.
-    const auto stage = [&](uint32_t present) {
+    // What was loaded, in LDS as values; with `there`, keys that are absent as zeros.
+    const auto stage = [&](const u32x4_t (&p)[kLoads], auto place, uint32_t there) {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             const int n = i * kKeys + lane / kPieces, first = lane % kPieces;
-            u32x4_t v = vp[i];
-            if (present != 0xffffffffu && !(present >> n & 1)) v = u32x4_t{};
+            u32x4_t v = p[i];
+            if (there != 0xffffffffu && !(there >> n & 1)) v = u32x4_t{};
             if constexpr (!kCodes) {
-                *reinterpret_cast<u32x4_t*>(tile + Tl::k(n, first)) = kp[i];
-                *reinterpret_cast<u32x4_t*>(tile + Tl::v(n, first)) = v;
+                *reinterpret_cast<u32x4_t*>(tile + place(n, first)) = v;
             } else {
+                asm volatile("" : "+v"(v));                // (else integers are taken apart where they are loaded, a tile ahead)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    const dev::frag_t<T> a = dev::codes8<T, FORMAT>(kp[i][2 * x], kp[i][2 * x + 1]), b = dev::codes8<T, FORMAT>(v[2 * x], v[2 * x + 1]);
+                    const dev::frag_t<T> f = dev::codes8<T, FORMAT>(v[2 * x], v[2 * x + 1]);
                     if constexpr (sizeof(T) == 2) {
-                        *reinterpret_cast<dev::bf16x8_t*>(tile + Tl::k(n, 2 * first + x)) = a;
-                        *reinterpret_cast<dev::bf16x8_t*>(tile + Tl::v(n, 2 * first + x)) = b;
+                        *reinterpret_cast<dev::bf16x8_t*>(tile + place(n, 2 * first + x)) = f;
                     } else {
-                        *reinterpret_cast<f32x4_t*>(tile + Tl::k(n, 4 * first + 2 * x)) = __builtin_shufflevector(a, a, 0, 1, 2, 3);
-                        *reinterpret_cast<f32x4_t*>(tile + Tl::k(n, 4 * first + 2 * x + 1)) = __builtin_shufflevector(a, a, 4, 5, 6, 7);
-                        *reinterpret_cast<f32x4_t*>(tile + Tl::v(n, 4 * first + 2 * x)) = __builtin_shufflevector(b, b, 0, 1, 2, 3);
-                        *reinterpret_cast<f32x4_t*>(tile + Tl::v(n, 4 * first + 2 * x + 1)) = __builtin_shufflevector(b, b, 4, 5, 6, 7);
+                        *reinterpret_cast<f32x4_t*>(tile + place(n, 4 * first + 2 * x)) = __builtin_shufflevector(f, f, 0, 1, 2, 3);
+                        *reinterpret_cast<f32x4_t*>(tile + place(n, 4 * first + 2 * x + 1)) = __builtin_shufflevector(f, f, 4, 5, 6, 7);
                     }
                 }
             }
         }
-        if constexpr (kCodes) scales[lane] = lane < 32 ? scale * c : scale;
     };
+    const auto place_k = [](int n, int c) { return Tl::k(n, c); };
+    const auto place_v = [](int n, int c) { return Tl::v(n, c); };
     int p0 = u.lo + wave * kTile;
     const bool any = p0 < u.hi;
     if (any) {
         lookup(p0);
         row = row_of();
-        load();
+        load_scales();
+        load(k.a.cache.k, kp);
+        lookup(p0 + kWaves * kTile);
+        load(k.a.cache.v, vp);
     }
     uint32_t present = (uint32_t)__ballot(row >= 0);
-    lookup(p0 + kWaves * kTile);
 
     dev::frag_t<T> q[NT][kFrags];
     dev::Sees sees[NT];
@@ -197,46 +201,22 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
     for (int n = 0; n < NT; ++n) { m[n] = -INFINITY; l[n] = 0.f; }
 
     for (; p0 < u.hi; p0 += kWaves * kTile) {
-        const bool partial = present != 0xffffffffu || p0 + kTile > some;
-        stage(present);
-        uint32_t seen[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) seen[n] = partial ? (uint32_t)sees[n].from(p0) & present : 0xffffffffu;
-        // Where some rows do not see some keys, no value that is not finite may meet a weight of zero: it is added to the
-        // rows that see it, and stands as zero in the product.
-        if (partial) {
-            constexpr int kOfChunk = 16 / (int)sizeof(T);
-            bool fine = !kCodes || dev::finite(scale);
-            for (int i = lane; i < kTile * Tl::kChunks; i += 64) {
-                const T* const v = &Tl::v_at(tile, i / Tl::kChunks, i % Tl::kChunks * kOfChunk);
-#pragma unroll
-                for (int j = 0; j < kOfChunk; ++j) fine &= dev::finite((float)v[j]);
-            }
-            if (__any(!fine)) {
-                for (int n = 0; n < kTile; ++n) {
-                    if (!(present >> n & 1)) continue;
-                    const bool no = kCodes && !dev::finite(scales[kTile + n]);
-#pragma unroll
-                    for (int t = 0; t < kDims; ++t)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float v = no ? NAN : (float)Tl::v_at(tile, n, 16 * t + 4 * quad + i);
-#pragma unroll
-                            for (int x = 0; x < NT; ++x)
-                                if (!dev::finite(v) && (seen[x] >> n & 1)) o[x][t][i] += v;
-                        }
-                }
-                for (int i = lane; i < kTile * D; i += 64)
-                    if (!dev::finite((float)Tl::v_at(tile, i / D, i % D))) Tl::v_at(tile, i / D, i % D) = (T)0.f;
-                if (kCodes && lane >= 32 && !dev::finite(scale)) scales[lane] = 0.f;
-            }
-        }
-        if (p0 + kWaves * kTile < u.hi) {
+        const uint32_t there = present;
+        const bool partial = there != 0xffffffffu || p0 + kTile > some, more = p0 + kWaves * kTile < u.hi;
+        stage(kp, place_k, 0xffffffffu);
+        if constexpr (kCodes) scales[lane] = lane < 32 ? scale * c : scale;
+        if (Tl::kBeside) stage(vp, place_v, there);
+        if (more) {
             row = row_of();
             present = (uint32_t)__ballot(row >= 0);
-            load();
-            lookup(p0 + 2 * kWaves * kTile);
+            load_scales();
+            load(k.a.cache.k, kp);
+            if (Tl::kBeside) load(k.a.cache.v, vp);
+            lookup(p0 + 2 * kWaves * kTile);         // (before V: what waits for it waits for every load before it)
         }
+        uint32_t seen[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) seen[n] = partial ? (uint32_t)sees[n].from(p0) & there : 0xffffffffu;
 
         f32x4_t s[NT][2];
 #pragma unroll
@@ -278,6 +258,42 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
                     for (int i = 0; i < 4; ++i) o[n][t][i] *= keep;
                 m[n] = next;
             }
+        }
+        if (!Tl::kBeside) {
+            stage(vp, place_v, there);
+            if (more) load(k.a.cache.v, vp);
+        }
+        // Where some rows do not see some keys, no value that is not finite may meet a weight of zero: it is added to the
+        // rows that see it, and stands as zero in the product.
+        if (partial) {
+            constexpr int kOfChunk = 16 / (int)sizeof(T);
+            bool fine = !kCodes || dev::finite(scales[kTile + (lane & 31)]);
+            for (int i = lane; i < kTile * Tl::kChunks; i += 64) {
+                const T* const v = &Tl::v_at(tile, i / Tl::kChunks, i % Tl::kChunks * kOfChunk);
+#pragma unroll
+                for (int j = 0; j < kOfChunk; ++j) fine &= dev::finite((float)v[j]);
+            }
+            if (__any(!fine)) {
+                for (int n = 0; n < kTile; ++n) {
+                    if (!(there >> n & 1)) continue;
+                    const bool no = kCodes && !dev::finite(scales[kTile + n]);
+#pragma unroll
+                    for (int t = 0; t < kDims; ++t)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float v = no ? NAN : (float)Tl::v_at(tile, n, 16 * t + 4 * quad + i);
+#pragma unroll
+                            for (int x = 0; x < NT; ++x)
+                                if (!dev::finite(v) && (seen[x] >> n & 1)) o[x][t][i] += v;
+                        }
+                }
+                for (int i = lane; i < kTile * D; i += 64)
+                    if (!dev::finite((float)Tl::v_at(tile, i / D, i % D))) Tl::v_at(tile, i / D, i % D) = (T)0.f;
+                if (kCodes && lane >= 32 && !dev::finite(scales[lane])) scales[lane] = 0.f;
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
             const float base = m[n] == -INFINITY ? 0.f : m[n];
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
@@ -351,64 +367,73 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
 template <typename T, int D>
 constexpr int row_tiles() { return D == 256 ? 1 : (D == 128 || sizeof(T) == 4 ? 2 : 4); }
 
-// Workgroups (as waves to a SIMD) of a compute unit: two, with 256 registers, or one, with 512.
+// Workgroups of a compute unit, as waves to a SIMD, by the registers that a wave's tile, sums and queries take.
 template <typename T, int D>
-constexpr int workgroups() { return 2 * Lds<T, D>::kTotal <= 160 * 1024 ? 2 : 1; }
+constexpr int workgroups() { return Tile<T, D>::kBeside ? 2 : 1; }
 
 template <typename T, int FORMAT, int D, int NT>
-__global__ __launch_bounds__((Lds<T, D>::kThreads), (workgroups<T, D>())) void decode_kernel(AttentionKernelArgs k) {
+__global__ __launch_bounds__(kThreads, (workgroups<T, D>())) void decode_kernel(AttentionKernelArgs k) {
     extern __shared__ __align__(16) char lds[];
     Unit u;
-    if (decode_unit<T, D>(k, 16 * NT, Lds<T, D>::kThreads, u)) attend<T, FORMAT, D, NT>(k, u, lds);
+    if (decode_unit<T, D>(k, 16 * NT, kThreads, u)) attend<T, FORMAT, D, NT>(k, u, lds);
 }
 
 template <typename T, int FORMAT, int D, int NT>
-__global__ __launch_bounds__((Lds<T, D>::kThreads), (workgroups<T, D>())) void prompt_kernel(AttentionKernelArgs k) {
+__global__ __launch_bounds__(kThreads, (workgroups<T, D>())) void prompt_kernel(AttentionKernelArgs k) {
     extern __shared__ __align__(16) char lds[];
     const unsigned H = (unsigned)k.a.cache.num_heads, tile = blockIdx.x / H;
     Unit u;
     if (prompt_unit(k, 16 * NT, (int)tile, (int)(blockIdx.x - tile * H), u)) attend<T, FORMAT, D, NT>(k, u, lds);
 }
 
-// A row's spans joined: a workgroup for each query head of a token, whose four waves take every fourth span.
-template <typename T, int D>
-__global__ __launch_bounds__(kJoinThreads) void join_kernel(AttentionKernelArgs k) {
-    constexpr int N = D / 64, kWaves = kJoinThreads / 64, kMost = kMaxSpans / kWaves;
-    __shared__ float sums[kWaves][D];
-    const unsigned at = blockIdx.x;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const unsigned token = at / (unsigned)k.a.H_q;
+// A row's spans joined, in four sums of every fourth span: a workgroup for each query head of a token, a sum to each wave, or
+// (W = 1, up to 16 spans) a wave for it.  Two ways, the same bits: 64 spans took one wave 11 us of dependent
+// loads, of a workgroup 3 us; 16384 heads of up to 9 spans 10 us more in a workgroup each.
+template <typename T, int D, int W>
+__global__ __launch_bounds__(kThreads) void join_kernel(AttentionKernelArgs k) {
+    constexpr int N = D / 64, kHeads = kWaves / W, kSums = 4 / W, kEach = 4 * W;        // heads of a workgroup; sums of a wave, spans of a sum
+    static_assert(kWaves == 4 && kMaxSpans == 64, "");
+    __shared__ float sums[W == 1 ? 1 : 4][D];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, first = wave % W * kSums;
+    const int64_t at = (int64_t)blockIdx.x * kHeads + wave / W;
+    if (at >= k.a.total_tokens * k.a.H_q) return;
+    const unsigned token = (unsigned)at / (unsigned)k.a.H_q;
     const int keys = row_keys(k.a, k.a.past[dev::divide(token, k.rows)]);
     if (keys <= 0 || keys > k.a.max_keys) return;
     const int span = span_keys(k.a.tokens_per_row * (int)k.group.d, keys), spans = (keys + span - 1) / span;
     if (spans == 1) return;
-    const float2 mine = lane < spans ? k.stats[(int64_t)at * k.spans + lane] : float2{-INFINITY, 0.f};
-    float x[N] = {}, v[kMost][N];
-    const float* p = k.part + (int64_t)at * k.spans * D + lane * N;
+    const float2 mine = lane < spans ? k.stats[at * k.spans + lane] : float2{-INFINITY, 0.f};
+    float x[kSums][N] = {}, v[kEach][kSums][N];
+    const float* p = k.part + at * k.spans * D + lane * N;
 #pragma unroll
-    for (int i = 0; i < kMost; ++i)
+    for (int i = 0; i < kEach; ++i)
 #pragma unroll
-        for (int j = 0; j < N; ++j) v[i][j] = i * kWaves + wave < spans ? p[(i * kWaves + wave) * D + j] : 0.f;
+        for (int w = 0; w < kSums; ++w)
+#pragma unroll
+            for (int j = 0; j < N; ++j) v[i][w][j] = 4 * i + first + w < spans ? p[(4 * i + first + w) * D + j] : 0.f;
     float top = mine.x;
 #pragma unroll
     for (int i = 1; i < 64; i *= 2) top = fmaxf(top, __shfl_xor(top, i));
     const float by = top == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mine.x - top);
-    const float sum = dev::group_sum(by * mine.y, 64);
+    const float sum = dev::group_sum(by * mine.y, 64), inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
-    for (int i = 0; i < kMost; ++i) {
-        const float f = __shfl(by, i * kWaves + wave);
+    for (int i = 0; i < kEach; ++i)
 #pragma unroll
-        for (int j = 0; j < N; ++j) x[j] += f * v[i][j];
-    }
+        for (int w = 0; w < kSums; ++w) {
+            const float f = __shfl(by, 4 * i + first + w);
 #pragma unroll
-    for (int j = 0; j < N; ++j) sums[wave][lane * N + j] = x[j];
-    __syncthreads();
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    if ((int)threadIdx.x < D) {
-        float o = 0.f;
+            for (int j = 0; j < N; ++j) x[w][j] = fmaf(f, v[i][w][j], x[w][j]);
+        }
+    T* const o = static_cast<T*>(k.a.o) + at * D;
+    if constexpr (W == 1) {
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) o += sums[w][threadIdx.x];
-        static_cast<T*>(k.a.o)[(int64_t)at * D + threadIdx.x] = (T)(o * inv);
+        for (int j = 0; j < N; ++j) o[lane * N + j] = (T)((((x[0][j] + x[1][j]) + x[2][j]) + x[3][j]) * inv);
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) sums[wave][lane * N + j] = x[0][j];
+        __syncthreads();
+        const int dim = threadIdx.x;
+        if (dim < D) o[dim] = (T)((((sums[0][dim] + sums[1][dim]) + sums[2][dim]) + sums[3][dim]) * inv);
     }
 }
 
@@ -435,9 +460,9 @@ template <typename T, int FORMAT, int D, int NT>
 hipError_t launch_rows(AttentionKernelArgs k, hipStream_t stream) {
     const int rows = k.a.tokens_per_row * (int)k.group.d;
     k.row_tiles = (rows + 16 * NT - 1) / (16 * NT);
-    const int64_t blocks = ((int64_t)k.a.num_seqs * k.spans + 7) / 8 * 8 * k.a.cache.num_heads * k.row_tiles;
-    if (!grid_fits(blocks, Lds<T, D>::kThreads)) return hipErrorInvalidConfiguration;
-    decode_kernel<T, FORMAT, D, NT><<<(unsigned)blocks, Lds<T, D>::kThreads, Lds<T, D>::kTotal, stream>>>(k);
+    const int64_t blocks = ((int64_t)k.a.num_seqs * k.spans * k.a.cache.num_heads + 7) / 8 * 8 * k.row_tiles;
+    if (!grid_fits(blocks, kThreads)) return hipErrorInvalidConfiguration;
+    decode_kernel<T, FORMAT, D, NT><<<(unsigned)blocks, kThreads, Lds<T, D>::kTotal, stream>>>(k);
     return hipGetLastError();
 }
 
@@ -448,7 +473,7 @@ hipError_t launch_decode(const AttentionArgs& a, hipStream_t stream) {
     k.rows = Divisor((uint32_t)a.tokens_per_row);
     k.spans = most_spans(rows, k.a.max_keys);
     const int64_t heads = a.total_tokens * a.H_q;
-    if (!grid_fits(heads, kJoinThreads)) return hipErrorInvalidConfiguration;
+    if (!grid_fits(heads, kThreads)) return hipErrorInvalidConfiguration;
     k.part = static_cast<float*>(a.workspace);
     k.stats = reinterpret_cast<float2*>(k.part + (k.spans > 1 ? heads * k.spans * D : 0));
     // as many row tiles to a wave as the rows fill and the registers hold; more rows share the keys in gdn_attention_wide.hip (two
@@ -460,15 +485,16 @@ hipError_t launch_decode(const AttentionArgs& a, hipStream_t stream) {
     else if (rows <= 32 || most == 2) e = launch_rows<T, FORMAT, D, (most > 1 ? 2 : 1)>(k, stream);
     else e = launch_rows<T, FORMAT, D, (most > 2 ? 4 : 1)>(k, stream);
     if (e != hipSuccess || k.spans == 1) return e;
-    join_kernel<T, D><<<(unsigned)heads, kJoinThreads, 0, stream>>>(k);
+    if (k.spans <= 16) join_kernel<T, D, 1><<<(unsigned)((heads + kWaves - 1) / kWaves), kThreads, 0, stream>>>(k);
+    else join_kernel<T, D, 4><<<(unsigned)heads, kThreads, 0, stream>>>(k);
     return hipGetLastError();
 }
 
 template <int FORMAT, int D, int NT>
 hipError_t launch_prompt(const AttentionKernelArgs& k, hipStream_t stream) {
     const int64_t tiles = k.a.total_tokens * (int)k.group.d / (16 * NT) + k.a.num_seqs, blocks = tiles * k.a.cache.num_heads;
-    if (!grid_fits(blocks, Lds<float, D>::kThreads) || k.a.total_tokens * (int64_t)k.group.d > 0x7fffffffLL) return hipErrorInvalidConfiguration;
-    prompt_kernel<float, FORMAT, D, NT><<<(unsigned)blocks, Lds<float, D>::kThreads, Lds<float, D>::kTotal, stream>>>(k);
+    if (!grid_fits(blocks, kThreads) || k.a.total_tokens * (int64_t)k.group.d > 0x7fffffffLL) return hipErrorInvalidConfiguration;
+    prompt_kernel<float, FORMAT, D, NT><<<(unsigned)blocks, kThreads, Lds<float, D>::kTotal, stream>>>(k);
     return hipGetLastError();
 }
 

@@ -190,11 +190,12 @@ __device__ __forceinline__ void fill_rows(const AttentionKernelArgs& k, const Un
 // attend to: a padding row's outputs are zeros then, those of a row with more keys than max_keys NaN.
 template <typename T, int D>
 __device__ __forceinline__ bool decode_unit(const AttentionKernelArgs& k, int per, int threads, Unit& u) {
-    // The row tiles of one span of keys stand 8 apart: on the same XCD, whose L2 then holds its keys.  So do its heads, whose
-    // rows lie side by side: 58.4 -> 57.6 us for one request of 131072 keys in 8 bits, 240 -> 233 us for 64 in bf16.
+    // The row tiles of one span of keys stand 8 apart: on the same XCD, whose L2 then holds its keys.  Its heads stand on
+    // different ones, which keeps them evenly loaded: all on one was 1-3 % faster without row tiles, but 124 us for 107 with trees
+    // of 16 rows, whose longest spans then meet on one XCD.
     const unsigned id = blockIdx.x, tile = id / 8 % (unsigned)k.row_tiles, at = id / (8 * (unsigned)k.row_tiles) * 8 + id % 8;
-    const unsigned H = (unsigned)k.a.cache.num_heads, group8 = at / (8 * H), by_head = group8 * 8 + at % 8, spans = (unsigned)k.spans;
-    u.h = (int)((at - group8 * 8 * H) / 8);
+    const unsigned H = (unsigned)k.a.cache.num_heads, by_head = at / H, spans = (unsigned)k.spans;
+    u.h = (int)(at - by_head * H);
     u.seq = (int)(by_head / spans);
     u.span = (int)(by_head - (unsigned)u.seq * spans);
     if (u.seq >= k.a.num_seqs) return false;

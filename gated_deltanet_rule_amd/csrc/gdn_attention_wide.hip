@@ -443,7 +443,7 @@ hipError_t launch(AttentionKernelArgs k, hipStream_t stream) {
     const int H = k.a.cache.num_heads;
     const bool decode = k.a.tokens_per_row > 0;
     const int64_t tiles = decode ? (k.a.tokens_per_row * (int)k.group.d + kRowsOfTile - 1) / kRowsOfTile : k.a.total_tokens * (int)k.group.d / kRowsOfTile + k.a.num_seqs;
-    const int64_t units = decode ? ((int64_t)k.a.num_seqs * k.spans + 7) / 8 * 8 * H : H;
+    const int64_t units = decode ? ((int64_t)k.a.num_seqs * k.spans * H + 7) / 8 * 8 : H;
     if (!grid_fits(tiles * units, kThreads) || k.a.total_tokens * (int64_t)k.group.d > 0x7fffffffLL) return hipErrorInvalidConfiguration;
     k.row_tiles = (int)tiles;
     auto* const kernel = decode ? wide_decode_kernel<FORMAT, D> : wide_prompt_kernel<FORMAT, D>;
