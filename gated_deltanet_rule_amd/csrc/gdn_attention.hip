@@ -472,8 +472,8 @@ hipError_t launch_decode(const AttentionArgs& a, hipStream_t stream) {
     const int rows = a.tokens_per_row * (int)k.group.d;
     k.rows = Divisor((uint32_t)a.tokens_per_row);
     k.spans = most_spans(rows, k.a.max_keys);
-    const int64_t heads = a.total_tokens * a.H_q;
-    if (!grid_fits(heads, kThreads)) return hipErrorInvalidConfiguration;
+    const int64_t heads = a.total_tokens * a.H_q, joins = k.spans <= 16 ? (heads + kWaves - 1) / kWaves : heads;
+    if (k.spans > 1 && !grid_fits(joins, kThreads)) return hipErrorInvalidConfiguration;
     k.part = static_cast<float*>(a.workspace);
     k.stats = reinterpret_cast<float2*>(k.part + (k.spans > 1 ? heads * k.spans * D : 0));
     // as many row tiles to a wave as the rows fill and the registers hold; more rows share the keys in gdn_attention_wide.hip (two
@@ -485,8 +485,8 @@ hipError_t launch_decode(const AttentionArgs& a, hipStream_t stream) {
     else if (rows <= 32 || most == 2) e = launch_rows<T, FORMAT, D, (most > 1 ? 2 : 1)>(k, stream);
     else e = launch_rows<T, FORMAT, D, (most > 2 ? 4 : 1)>(k, stream);
     if (e != hipSuccess || k.spans == 1) return e;
-    if (k.spans <= 16) join_kernel<T, D, 1><<<(unsigned)((heads + kWaves - 1) / kWaves), kThreads, 0, stream>>>(k);
-    else join_kernel<T, D, 4><<<(unsigned)heads, kThreads, 0, stream>>>(k);
+    auto* const join = k.spans <= 16 ? join_kernel<T, D, 1> : join_kernel<T, D, 4>;
+    join<<<(unsigned)joins, kThreads, 0, stream>>>(k);
     return hipGetLastError();
 }
 
