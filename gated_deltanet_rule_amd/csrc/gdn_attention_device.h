@@ -125,7 +125,7 @@ __device__ __forceinline__ bool finite(float x) { return fabsf(x) < INFINITY; }
 // spans keep more of the chip busy for few requests, long ones start and join less often (16 rows of 128 dims in bf16 at
 // 256 / 512 / 1024 keys: one request of 1024 keys 9.5 / 12 / 17 us, 64 requests of up to 8192 keys 266 / 245 / 235 us).
 constexpr int kMaxSpans = 64;
-__host__ __device__ inline int least_span(int rows) { return rows <= 16 ? 512 : (rows <= 64 ? 512 : 1024); }
+__host__ __device__ inline int least_span(int rows) { return rows <= 64 ? 512 : 1024; }
 __host__ __device__ inline int span_keys(int rows, int keys) {
     int span = least_span(rows);
     while (keys > kMaxSpans * (int64_t)span) span *= 2;
