@@ -42,24 +42,38 @@ __device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
     }
 }
 
-// Largest of each aligned group of `lanes` lanes (a power of two); NaN counts as nothing here.
-__device__ __forceinline__ float group_max(float x, int lanes) {
-    if (lanes > 1) x = fmaxf(x, dev::dpp_move<0xB1>(x));
-    if (lanes > 2) x = fmaxf(x, dev::dpp_move<0x4E>(x));
-    if (lanes > 4) x = fmaxf(x, dev::dpp_move<0x141>(x));
-    if (lanes > 8) x = fmaxf(x, dev::dpp_move<0x140>(x));
-    if (lanes > 16) x = fmaxf(x, __shfl_xor(x, 16));
-    if (lanes > 32) x = fmaxf(x, __shfl_xor(x, 32));
+// Largest of each aligned group of `lanes` lanes (a power of two).
+__device__ __forceinline__ unsigned group_max(unsigned x, int lanes) {
+    const auto with = [&](unsigned y) { x = x > y ? x : y; };
+    const auto move = [&](auto f) { with(__builtin_bit_cast(unsigned, f(__builtin_bit_cast(float, x)))); };
+    if (lanes > 1) move([](float f) { return dev::dpp_move<0xB1>(f); });
+    if (lanes > 2) move([](float f) { return dev::dpp_move<0x4E>(f); });
+    if (lanes > 4) move([](float f) { return dev::dpp_move<0x141>(f); });
+    if (lanes > 8) move([](float f) { return dev::dpp_move<0x140>(f); });
+    if (lanes > 16) with((unsigned)__shfl_xor((int)x, 16));
+    if (lanes > 32) with((unsigned)__shfl_xor((int)x, 32));
     return x;
+}
+
+// x / by, correctly rounded, for finite x and by > 0, given the correctly rounded 1 / by: two steps on the remainder, of which
+// the first gives a neighbour of the quotient and the second the nearest (Markstein's theorem), in five instructions where a division
+// of its own takes eleven.  A remainder that underflows belongs to a quotient that is far below every code's half step.
+__device__ __forceinline__ float divide(float x, float by, float inverse) {
+    float q = x * inverse;
+    q = fmaf(fmaf(-q, by, x), inverse, q);
+    q = fmaf(fmaf(-q, by, x), inverse, q);
+    return copysignf(q, x);                // (a negative zero)
 }
 
 template <int FORMAT>
 __device__ __forceinline__ u32x2_t codes8(const float (&x)[8], float scale) {
+    constexpr float M = FORMAT == GDN_CACHE_E4M3 ? 448.f : 127.f;
+    const float inverse = 1.f / scale;
     u32x2_t w = {0u, 0u};
-    if constexpr (FORMAT == GDN_CACHE_E4M3) {
-        float v[8];
+    float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = fminf(fmaxf(x[i] / scale, -448.f), 448.f);
+    for (int i = 0; i < 8; ++i) v[i] = __builtin_amdgcn_fmed3f(divide(x[i], scale, inverse), -M, M);
+    if constexpr (FORMAT == GDN_CACHE_E4M3) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             int p = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i], v[4 * i + 1], 0, false);
@@ -67,10 +81,7 @@ __device__ __forceinline__ u32x2_t codes8(const float (&x)[8], float scale) {
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int c = (int)rintf(fminf(fmaxf(x[i] / scale, -127.f), 127.f));
-            w[i / 4] |= (unsigned)(c & 255) << (8 * (i & 3));
-        }
+        for (int i = 0; i < 8; ++i) w[i / 4] |= (unsigned)((int)rintf(v[i]) & 255) << (8 * (i & 3));
     }
     return w;
 }
@@ -102,7 +113,7 @@ __global__ __launch_bounds__(kThreads) void write_kernel(CacheCopyArgs a) {
     if (slot < 0 || slot >= a.cache.num_rows) return;
     void* const cache[2] = {a.cache.k, a.cache.v};
     float* const scales[2] = {a.cache.k_scale, a.cache.v_scale};
-    float x[2][8];
+    float x[2][8] = {};
 #pragma unroll
     for (int i = 0; i < 2; ++i)
         if (e < d) load8(static_cast<const T*>(a.in[i]) + token * a.in_stride[i] + (int64_t)h * d + e, x[i]);
@@ -112,16 +123,14 @@ __global__ __launch_bounds__(kThreads) void write_kernel(CacheCopyArgs a) {
         if constexpr (FORMAT == GDN_CACHE_PLAIN) {
             if (e < d) store8(static_cast<T*>(cache[i]) + head * d + e, x[i]);
         } else {
-            float most = 0.f;
-            int bad = 0;
+            // as bits, which order like the magnitudes and put infinities and NaN on top
+            unsigned top = 0u;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float v = e < d ? fabsf(x[i][j]) : 0.f;
-                most = fmaxf(most, v);
-                bad |= !(v < INFINITY);
+                const unsigned v = __builtin_bit_cast(unsigned, x[i][j]) & 0x7fffffffu;
+                top = top > v ? top : v;
             }
-            // an infinity or a NaN anywhere: an infinite maximum
-            most = group_max(bad ? INFINITY : most, LPH);
+            const float most = __builtin_bit_cast(float, group_max(top, LPH));
             const bool finite = most < INFINITY;
             const float scale = finite ? fmaxf(most, 0x1p-100f) / (FORMAT == GDN_CACHE_E4M3 ? 448.f : 127.f) : NAN;
             u32x2_t w = {0u, 0u};
