@@ -9,9 +9,13 @@
 // transposed, S^T = K Q^T and O^T = V^T P^T, 16 x 16 tiles with a query row to each lane of a
 // group of 16: a lane then holds four keys' weights of its row for each tile of 16 keys, which is
 // the operand that the second product takes if V's rows are taken in that order, so weights
-// never move between lanes and a row's factors are the lane's own.  K goes from memory into
-// operands directly (a lane's 16 bytes of a key are eight steps of the contraction; queries are
-// laid out alike); V goes through the wave's own LDS, which hands it out transposed.
+// never move between lanes and a row's factors are the lane's own.
+//
+// Memory bounds it: a decode row reads its whole context for a few products.  Loads take
+// whole cache rows, neighbouring lanes neighbouring bytes, one tile ahead of the sums in registers, and
+// go through the wave's own LDS, so that no wave waits for another.  (Loaded straight into the operands, 16 lanes in
+// 16 rows, K took the memory path up to four times as long: 298 us instead of 266 for 64 requests of up to 8192 keys, 136
+// instead of 66 for one of 131072 keys in 8 bits.)  Now 240 us, 5.1 TB/s of keys and values, and 58.6 us, 4.7 TB/s.
 //
 // A long context is cut into spans that workgroups take side by side, joined by a second
 // launch.  The spans follow from the row's own number of keys and the shape, so a row's bits do
@@ -193,7 +197,7 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
         for (int f = 0; f < kFrags; ++f) asm volatile("" : "+v"(q[n][f]));
         asm volatile("" : "+v"(sees[n].all), "+v"(sees[n].first), "+v"(sees[n].mask));
     }
-    const int some = k.a.tree_mask ? u.past : u.past + (int)dev::divide(u.row0, k.group) + 1;        // every row sees the keys below
+    const int some = k.a.tree_mask ? u.past : causal_keys(k, u, u.row0);        // every row sees the keys below
 
     f32x4_t o[NT][kDims] = {};
     float m[NT], l[NT];

@@ -257,10 +257,16 @@ __device__ __forceinline__ bool prompt_unit(const AttentionKernelArgs& k, int pe
     return true;
 }
 
-// Where row r of a unit (a query head of a token) stands in q and o, and the keys that it sees.
+// Keys that row r of a unit (a query head of a token) sees without a tree: a prompt may end past the last position.
+__device__ __forceinline__ int causal_keys(const AttentionKernelArgs& k, const Unit& u, int r) {
+    const int64_t n = (int64_t)u.past + (int)dev::divide(r, k.group) + 1;
+    return n < 0x7fffffff ? (int)n : 0x7fffffff;
+}
+
+// The keys that row r sees.
 __device__ __forceinline__ dev::Sees row_sees(const AttentionKernelArgs& k, const Unit& u, int r) {
+    if (!k.a.tree_mask) return {causal_keys(k, u, r), 0, 0};
     const int t = (int)dev::divide(r, k.group);
-    if (!k.a.tree_mask) return {u.past + t + 1, 0, 0};
     const uint64_t all = u.tokens >= 64 ? ~0ull : (1ull << u.tokens) - 1;
     return {u.past, u.past, (uint64_t)k.a.tree_mask[u.first + t] & all};
 }

@@ -1,11 +1,19 @@
 // gdn_attention_wide.hip -- attention of many query rows over a paged cache for gfx950: bf16
-// prompts, and decode rows with large trees.
+// prompts, and decode rows of many tokens.
 //
 // The same sums as gdn_attention.hip, for rows enough to share the keys: four waves of 32 rows take
 // the same tiles of 64 keys from LDS, where two of K and two of V stand in turn.  Plain values
 // go there past the registers, codes through them, widened.  The products are transposed here
 // too, 32 x 32 tiles with a query row to each pair of lanes, so that weights are the second
 // product's operand as they come out of the first.
+//
+// The matrix cores bound it, as far as they are fed: a wave's products take 1024 cycles of a tile at 128 dims, its softmax 700
+// of the vector ALU, which the other wave of the SIMD has to fill.  8 prompts of up to 4096 tokens, 128 dims: 461 us,
+// 860 TFLOP/s where a large library product reaches 1150.  8192 tokens behind 24576, 256 dims, 8-bit codes: 5.2 ms, 740
+// TFLOP/s with one wave to a SIMD.  Trees of 32 tokens (128 rows) of 16 requests: 108 us with the join, 410 TFLOP/s, held by the
+// start and end of each span.  Tried and not better: eight waves in two phases (466 and 463 us), four tiles of
+// 32 keys in turn (477), loads behind the scores (511), the next tile's scores beside this one's exponentials (458, but spilling at 256
+// dims), wave priorities, a workgroup's heads on one XCD.
 #include <hip/hip_runtime.h>
 
 #include "gdn_attention_device.h"
@@ -153,10 +161,10 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
     }
     // every row of the workgroup (of the wave) sees the keys below `some` (`mine`), no row of the wave one from `end` on
     const bool tree = k.a.tree_mask != nullptr;
-    const int some = tree ? u.past : u.past + (int)dev::divide(u.row0, k.group) + 1;
+    const int some = tree ? u.past : causal_keys(k, u, u.row0);
     const int last_row = (first_row + 32 < u.rows ? first_row + 32 : u.rows) - 1;
-    const int mine = tree ? u.past : u.past + (int)dev::divide(first_row, k.group) + 1;
-    const int end = first_row >= u.rows ? 0 : (tree ? u.hi : u.past + (int)dev::divide(last_row, k.group) + 1);
+    const int mine = tree ? u.past : causal_keys(k, u, first_row);
+    const int end = first_row >= u.rows ? 0 : (tree ? u.hi : causal_keys(k, u, last_row));
     const auto works = [&](int t) { return t < tiles && u.lo + t * kTile < end; };
     // Whether keys of a tile are absent, or some rows of the workgroup do not see some.
     const auto special = [&](int t, uint64_t there) { return there != ~0ull || u.lo + (t + 1) * kTile > some; };

@@ -28,6 +28,8 @@
  *               the softmax's weights, times the value's scale where there is one, are rounded
  *               to bf16 on their way into the matrix cores, by at most 2^-8 of each; 8-bit
  *               codes are exact there.  With fp32 activations nothing is rounded below fp32.
+ *               Values are summed before the sum is divided, with weights of up to 2^8: their
+ *               sum over the keys has to stay below 2^119.
  *               A row's results are bitwise the same whatever shares its call, and a prompt
  *               token's do not depend on how its prompt is cut into calls.
  *   Non-finite  A key or value that a token does not see leaves it untouched, whatever it
