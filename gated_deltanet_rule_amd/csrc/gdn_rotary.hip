@@ -2,9 +2,11 @@
 //
 //     (a, b) <- factor (a cos t - b sin t, b cos t + a sin t),   t = p f_i
 //
-// Memory-bound: every value crosses HBM once each way.  A workgroup takes TB tokens: its threads
-// first form the tokens' cosines and sines, one frequency each, into LDS, where all heads
+// Memory-bound: every value crosses HBM once each way.  A workgroup takes a token: its threads
+// first form the cosines and sines, one frequency each, into LDS, where all heads
 // share them; then they turn the heads' pairs, V pairs to a thread as two 16-byte vectors.
+// 131072 tokens of 32 + 8 heads of 128 dims in bf16: 468 us, 5.7 TB/s of 6.6 for a large copy; 64 tokens: 3.5 us, of
+// which the copy's share is 0.2 and the rest a launch.  Where rows or parts are not whole vectors V is 1.
 #include <hip/hip_runtime.h>
 
 #include "gdn_attention_internal.h"
@@ -19,7 +21,7 @@ constexpr int kThreads = 256;
 
 struct RotaryKernelArgs {
     RotaryArgs a;
-    Divisor units_of_head, units_of_token;
+    Divisor units_of_head;
     int turned;      // of a head's units, those that turn; the rest copy (none in place)
 };
 
@@ -45,26 +47,22 @@ __device__ __forceinline__ float2 turn(int p, float f, float factor) {
 }
 
 // A head's units: pairs V j .. V j + V - 1 for j < turned, then 2 V elements each that only copy.
-template <typename T, int V, bool INTERLEAVED, int TB>
+template <typename T, int V, bool INTERLEAVED>
 __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryKernelArgs k) {
     extern __shared__ float2 turns[];
     const gdn_rotary_shape& s = k.a.shape;
     const int half = s.rotary_dim / 2, heads = s.num_q_heads + s.num_k_heads;
-    const int64_t first = (int64_t)blockIdx.x * TB;
-    const int tokens = (int)(k.a.num_tokens - first < TB ? k.a.num_tokens - first : TB);
-    for (int i = threadIdx.x; i < tokens * half; i += kThreads) {
-        const int t = TB == 1 ? 0 : i / half, f = i - t * half;
-        turns[i] = turn(k.a.positions[first + t], k.a.inv_freq[f], s.factor);
-    }
+    const int64_t token = blockIdx.x;
+    const int position = k.a.positions[token];
+    for (int i = threadIdx.x; i < half; i += kThreads) turns[i] = turn(position, k.a.inv_freq[i], s.factor);
     __syncthreads();
+    if (position < 0) return;
     const int units = heads * (int)k.units_of_head.d;
-    for (int i = threadIdx.x; i < tokens * units; i += kThreads) {
-        const int t = TB == 1 ? 0 : (int)dev::divide(i, k.units_of_token), in_token = i - t * units;
-        if (k.a.positions[first + t] < 0) continue;
-        const int head = (int)dev::divide(in_token, k.units_of_head), unit = in_token - head * (int)k.units_of_head.d;
+    for (int i = threadIdx.x; i < units; i += kThreads) {
+        const int head = (int)dev::divide(i, k.units_of_head), unit = i - head * (int)k.units_of_head.d;
         const int which = head >= s.num_q_heads, h = which ? head - s.num_q_heads : head;
-        const T* in = static_cast<const T*>(k.a.in[which]) + (first + t) * k.a.in_stride[which] + (int64_t)h * s.head_dim;
-        T* out = static_cast<T*>(k.a.out[which]) + (first + t) * k.a.out_stride[which] + (int64_t)h * s.head_dim;
+        const T* in = static_cast<const T*>(k.a.in[which]) + token * k.a.in_stride[which] + (int64_t)h * s.head_dim;
+        T* out = static_cast<T*>(k.a.out[which]) + token * k.a.out_stride[which] + (int64_t)h * s.head_dim;
         float a[V], b[V];
         if (unit >= k.turned) {
             const int e = s.rotary_dim + (unit - k.turned) * 2 * V;
@@ -76,7 +74,7 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryKernelArgs k) {
             continue;
         }
         const int ea = INTERLEAVED ? 2 * V * unit : V * unit, eb = INTERLEAVED ? ea + V : ea + half;
-        const float2* cs = turns + t * half + V * unit;
+        const float2* cs = turns + V * unit;
         load<T, V>(in + ea, a);
         load<T, V>(in + eb, b);
         float x[V], y[V];
@@ -106,19 +104,17 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryKernelArgs k) {
     }
 }
 
-template <typename T, int V, int TB>
+template <typename T, int V>
 hipError_t launch(const RotaryArgs& a, hipStream_t stream) {
     const gdn_rotary_shape& s = a.shape;
     const bool in_place = (s.num_q_heads == 0 || a.in[0] == a.out[0]) && (s.num_k_heads == 0 || a.in[1] == a.out[1]);
-    RotaryKernelArgs k = {a, Divisor(), Divisor(), s.rotary_dim / (2 * V)};
+    RotaryKernelArgs k = {a, Divisor(), s.rotary_dim / (2 * V)};
     const int copied = in_place ? 0 : (s.head_dim - s.rotary_dim + 2 * V - 1) / (2 * V);
     k.units_of_head = Divisor(k.turned + copied);
-    k.units_of_token = Divisor((s.num_q_heads + s.num_k_heads) * (k.turned + copied));
-    const int64_t blocks = (a.num_tokens + TB - 1) / TB;
-    if (!grid_fits(blocks, kThreads)) return hipErrorInvalidConfiguration;
-    const size_t lds = (size_t)TB * (s.rotary_dim / 2) * sizeof(float2);
-    if (s.interleaved) rotary_kernel<T, V, true, TB><<<(unsigned)blocks, kThreads, lds, stream>>>(k);
-    else rotary_kernel<T, V, false, TB><<<(unsigned)blocks, kThreads, lds, stream>>>(k);
+    if (!grid_fits(a.num_tokens, kThreads)) return hipErrorInvalidConfiguration;
+    const size_t lds = (size_t)(s.rotary_dim / 2) * sizeof(float2);
+    if (s.interleaved) rotary_kernel<T, V, true><<<(unsigned)a.num_tokens, kThreads, lds, stream>>>(k);
+    else rotary_kernel<T, V, false><<<(unsigned)a.num_tokens, kThreads, lds, stream>>>(k);
     return hipGetLastError();
 }
 
@@ -131,8 +127,8 @@ hipError_t launch(const RotaryArgs& a, hipStream_t stream) {
         if ((i ? s.num_k_heads : s.num_q_heads) == 0) continue;
         wide = wide && a.in_stride[i] % V == 0 && a.out_stride[i] % V == 0 && (uintptr_t)a.in[i] % 16 == 0 && (uintptr_t)a.out[i] % 16 == 0;
     }
-    if (!wide) return launch<T, 1, 1>(a, stream);
-    return launch<T, V, 1>(a, stream);
+    if (!wide) return launch<T, 1>(a, stream);
+    return launch<T, V>(a, stream);
 }
 
 }  // namespace
