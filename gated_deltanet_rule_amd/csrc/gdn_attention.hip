@@ -395,6 +395,7 @@ __global__ __launch_bounds__(kThreads, (workgroups<T, D>())) void prompt_kernel(
 // loads, of a workgroup 3 us; 16384 heads of up to 9 spans 10 us more in a workgroup each.
 template <typename T, int D, int W>
 __global__ __launch_bounds__(kThreads) void join_kernel(AttentionKernelArgs k) {
+#pragma clang fp contract(off)             // a product that one of them fused into the sum of the statistics would round differently
     constexpr int N = D / 64, kHeads = kWaves / W, kSums = 4 / W, kEach = 4 * W;        // heads of a workgroup; sums of a wave, spans of a sum
     static_assert(kWaves == 4 && kMaxSpans == 64, "");
     __shared__ float sums[W == 1 ? 1 : 4][D];

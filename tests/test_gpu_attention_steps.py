@@ -107,7 +107,7 @@ def test_steps(d, dtype, fmt):
 
 
 @pytest.mark.parametrize("dtype,fmt", FORMATS)
-@pytest.mark.parametrize("d,tokens", [(64, 1100), (128, 150), (256, 300)])
+@pytest.mark.parametrize("d,tokens", [(64, 1100), (128, 150), (128, 1100), (256, 300)])
 def test_pieces_of_a_prompt_are_the_prompt(d, tokens, dtype, fmt):
     """Cut anywhere, shared with whatever: the same bits (1100 tokens: more and fewer rows of a workgroup)."""
     whole = Engine(1, tokens, d, dtype, fmt)
@@ -215,6 +215,29 @@ def test_a_captured_step(dtype, fmt):
         step(side)
         torch.cuda.current_stream().wait_stream(side)
         assert torch.equal(o, want), i
+
+
+@pytest.mark.parametrize("dtype,fmt", FORMATS)
+@pytest.mark.parametrize("per,hq,hkv,d", [(1, 8, 2, 128), (2, 6, 2, 64), (9, 16, 1, 256), (40, 4, 1, 128)])
+def test_bits_do_not_depend_on_max_keys(per, hq, hkv, d, dtype, fmt):
+    """A launch and a workspace sized for more spans (beyond 16 and up to the most there are) give the same bits."""
+    past, block = [3000, 700, 11], 16
+    keys = [p + per for p in past]
+    table, rows = C.pages(keys, block, DEV, 3)
+    cache = C.filled_cache(rows, hkv, d, dtype, fmt, C.owned_rows(table, block, keys), DEV, 3)
+    wide = torch.cat([table, torch.full((3, 6000), -1, dtype=torch.int32, device=DEV)], 1)
+    q = C.queries(3 * per, hq, d, dtype, DEV, 8)
+    out = []
+    for most in (max(keys), 9000, 30000, 90000):
+        ws = A.alloc_attention_workspace(q, cache["k_cache"], tokens_per_row=per, max_keys=most)
+        if ws is not None:
+            ws.fill_(0xff)
+        o = torch.full_like(q, 5.0)
+        A.gdn_attention_decode(q, o=o, computed=C.i32(past, DEV), kv_table=wide, kv_block=block, scale=d ** -0.5, tokens_per_row=per, max_keys=most,
+                               workspace=ws, **cache)
+        out.append(o)
+    R.check("decode", out[0], *R.attention(q, cache, table, block, past, [per] * 3, d ** -0.5))
+    assert all(torch.equal(o, out[0]) for o in out[1:])
 
 
 def test_refused_tensors():
