@@ -367,7 +367,7 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
     }
 }
 
-// Most tiles of 16 rows to a wave: more spill.
+// Most tiles of 16 rows to a wave: more spill hundreds of bytes.
 template <typename T, int D>
 constexpr int row_tiles() { return D == 256 ? 1 : (D == 128 || sizeof(T) == 4 ? 2 : 4); }
 
@@ -503,7 +503,8 @@ hipError_t launch_prompt(const AttentionKernelArgs& k, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// One row tile to a wave where two would leave compute units without work.
+// One row tile to a wave where two would leave compute units without work (one / two of 128 dims, 8 heads over 2: 512 tokens
+// 22.6 / 31.6 us, 1024 59 / 56, 4096 612 / 506; of 64 dims 12.9 / 18.1, 27.5 / 30.6, 237 / 223).
 template <int FORMAT, int D>
 hipError_t launch_prompt(const AttentionArgs& a, hipStream_t stream) {
     constexpr int most = row_tiles<float, D>();
