@@ -17,6 +17,10 @@
 // 16 rows, K took the memory path up to four times as long: 298 us instead of 266 for 64 requests of up to 8192 keys, 136
 // instead of 66 for one of 131072 keys in 8 bits.)  Now 240 us, 5.1 TB/s of keys and values, and 58.6 us, 4.7 TB/s.
 //
+// With bf16 the weights are rounded to bf16 for the second product.  As two bf16 parts each, in two products, they left only the
+// output's rounding: 240.5 us for 240.0, but 17.1 for 16.3 and 41.4 for 38.2 (16 requests of 4096 keys in 8 bits, two heads of
+// 128 and 256 dims), where 8-bit values are further off already.
+//
 // A long context is cut into spans that workgroups take side by side, joined by a second
 // launch.  The spans follow from the row's own number of keys and the shape, so a row's bits do
 // not depend on what shares its call.
@@ -306,10 +310,12 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float x = __builtin_amdgcn_exp2f(s[n][b][i] - base);
-                    l[n] += x;
+                    if constexpr (kCodes || sizeof(T) == 4) l[n] += x;
                     w[n][4 * b + i] = (T)(x * by[i]);
                 }
             }
+            // the rounded weights' sum (see gdn_attention_wide.hip)
+            if constexpr (!kCodes && sizeof(T) == 2) l[n] += dev::sum8(w[n], 0.f);
         }
 #pragma unroll
         for (int t = 0; t < kDims; ++t) {

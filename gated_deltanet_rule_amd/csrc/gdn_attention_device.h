@@ -44,6 +44,15 @@ __device__ __forceinline__ f32x4_t mma16(f32x8_t a, f32x8_t b, f32x4_t acc) {
     return acc;
 }
 
+// The sum of eight weights that were rounded to bf16.  The instruction rounds to nearest but cuts its smallest terms off (0.1 of
+// a half step too little in the mean, beside terms 2^20 apart), so sums over many keys add such sums in fp32.
+__device__ __forceinline__ float sum8(bf16x8_t w, float sum) {
+    const bf16x2_t one = {(__bf16)1.f, (__bf16)1.f};
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) sum = __builtin_amdgcn_fdot2_f32_bf16(bf16x2_t{w[i], w[i + 1]}, one, sum, false);
+    return sum;
+}
+
 // Four 8-bit codes as values of T (exact in bf16: at most 8 significant bits).
 template <typename T, int FORMAT>
 __device__ __forceinline__ void codes4(unsigned w, T (&v)[4]) {

@@ -298,10 +298,21 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float e = __builtin_amdgcn_exp2f(kCodes ? s[b][4 * i + j] - base : fmaf(s[b][4 * i + j], c, -base));
-                    l += e;
+                    if constexpr (kCodes) l += e;
                     w[2 * b + i / 2][4 * (i & 1) + j] = (__bf16)(e * by[j]);
                 }
             }
+        // The rounded weights' sum: a row's largest weight may be up to 2^8, not 1, and where it has nearly all of the sum its rounding
+        // then cancels.  (With codes the weights carry the values' scales, and what they are rounded by is not the sum's.)
+        if constexpr (!kCodes) {
+            float x = 0.f, y = 0.f;
+#pragma unroll
+            for (int g = 0; g < 4; g += 2) {
+                x = dev::sum8(w[g], x);
+                y = dev::sum8(w[g + 1], y);
+            }
+            l += x + y;
+        }
     };
     const auto sums = [&](int t) {
         // chunk 4 d + piece of four keys: fixed distances too, from one first for the even d and one for the odd

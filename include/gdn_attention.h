@@ -27,7 +27,8 @@
  *   Arithmetic  Scores, softmax statistics, sums and scales are fp32.  With bf16 activations
  *               the softmax's weights, times the value's scale where there is one, are rounded
  *               to bf16 on their way into the matrix cores, by at most 2^-8 of each; 8-bit
- *               codes are exact there.  With fp32 activations nothing is rounded below fp32.
+ *               codes are exact there.  Over a plain cache the rounded weights are summed, so that
+ *               the rounding of a key that has nearly all of the weight cancels.  With fp32 activations nothing is rounded below fp32.
  *               Values are summed before the sum is divided, with weights of up to 2^8: their
  *               sum over the keys has to stay below 2^119.
  *               A row's results are bitwise the same whatever shares its call, and a prompt

@@ -1,0 +1,61 @@
+"""What attention makes of values on the GPU: rows that a few keys dominate."""
+import math
+
+import pytest
+import torch
+
+from gated_deltanet_rule_amd import attention as A
+from tests import attention_cases as C
+from tests import attention_reference as R
+
+pytestmark = pytest.mark.gpu
+BF16 = torch.bfloat16
+DEV = "cuda"
+
+
+def prefill(q, cache, table, past, scale):
+    o = torch.full_like(q, 5.0)
+    A.gdn_attention_prefill(q, o=o, cu_seqlens=C.packed([q.shape[0]], DEV), start_pos=C.i32([past], DEV), kv_table=table, kv_block=16, scale=scale, **cache)
+    return o
+
+
+def decode(q, cache, table, past, scale):
+    o = torch.full_like(q, 5.0)
+    ws = A.alloc_attention_workspace(q, cache["k_cache"], tokens_per_row=q.shape[0], max_keys=past + q.shape[0])
+    A.gdn_attention_decode(q, o=o, computed=C.i32([past], DEV), kv_table=table, kv_block=16, scale=scale, tokens_per_row=q.shape[0],
+                           max_keys=past + q.shape[0], workspace=ws, **cache)
+    return o
+
+
+@pytest.mark.parametrize("hq,d,past,new,how", [(1, 64, 300, 1, decode), (16, 128, 700, 1, decode), (8, 256, 200, 2, decode), (16, 128, 300, 33, decode),
+                                               (4, 64, 100, 40, prefill), (8, 128, 0, 200, prefill), (4, 256, 300, 50, prefill)])
+def test_rounded_weights_cancel(hq, d, past, new, how):
+    """The weights of a plain bf16 cache are rounded to bf16, and their sum is the sum of the rounded ones: with w_j (1 + e_j),
+    |e_j| <= 2^-8, the output is off by sum_j p_j e_j (v_j - o) / (1 + sum_j p_j e_j), which vanishes where one key has
+    nearly all of the weight, however far above the running maximum of its time it came."""
+    table, rows = C.pages([past + new], 16, DEV, 3)
+    at = C.owned_rows(table, 16, [past + new])
+    cache = C.filled_cache(rows, 1, d, BF16, None, at, DEV, 3)
+    # queries and keys of -1, 0 and 1: a score is a whole number, exact in fp32, of some 5 either way
+    g = torch.Generator(device=DEV).manual_seed(8)
+    q = torch.randint(-1, 2, (new, hq, d), generator=g, device=DEV).to(BF16)
+    cache["k_cache"][at] = torch.randint(-1, 2, (past + new, 1, d), generator=g, device=DEV).to(BF16)
+    scale = 1.0 if d <= 128 else 0.5
+    o = how(q, cache, table, past, scale).double()
+    k, v = cache["k_cache"][at, 0].double(), cache["v_cache"][at, 0].double()
+    seen = torch.ones(new, past + new, dtype=torch.bool, device=DEV).tril(past)
+    score = (torch.matmul(q.double().view(-1, d), k.t().contiguous()).view(new, hq, -1) * scale).masked_fill(~seen[:, None], -math.inf)
+    p = torch.softmax(score, -1)
+    exact = torch.matmul(p.view(new * hq, -1), v).view(new, hq, d)
+    away, spread = torch.zeros_like(exact), torch.matmul(p.view(new * hq, -1), v.abs()).view(new, hq, d)
+    for t in range(new):
+        away[t] = (p[t][..., None] * (v - exact[t][:, None]).abs()).sum(1)
+    # in the exponent: log2 e, the score's product, the largest score's and their difference rounded, each 2^-24 of at most
+    # twice the largest; 16 roundings of the exponential and the inverse; sums over the keys
+    largest = score.masked_fill(~seen[:, None], 0.0).abs().amax(-1, keepdim=True)
+    eps = 2.0 ** -24 * (6 * 1.4427 * largest + 16)
+    before = 2.0 ** -8 / (1 - 2.0 ** -8) * away + (2 * eps + 2 * (past + new + 64) * 2.0 ** -24) * spread
+    # the output's rounding: half a step of the binade that the value before it may lie in
+    half = torch.ldexp(torch.ones_like(exact), torch.frexp(exact.abs() + before).exponent - 9)
+    off = (o - exact).abs()
+    assert (off <= before + half).all(), "off by up to %.3g of what is allowed" % float((off / (before + half)).max())
