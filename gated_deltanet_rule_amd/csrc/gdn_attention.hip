@@ -167,6 +167,21 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
             }
         }
     };
+    // Whether the lane's share of V in LDS is finite; all of V, what is not as zeros.
+    const auto all_finite = [lane](char* lds) {
+        constexpr int kOfChunk = 16 / (int)sizeof(T);
+        bool fine = true;
+        for (int i = lane; i < kTile * Tl::kChunks; i += 64) {
+            const T* const v = &Tl::v_at(lds, i / Tl::kChunks, i % Tl::kChunks * kOfChunk);
+#pragma unroll
+            for (int j = 0; j < kOfChunk; ++j) fine &= dev::finite((float)v[j]);
+        }
+        return fine;
+    };
+    const auto zero_others = [lane](char* lds) {
+        for (int i = lane; i < kTile * D; i += 64)
+            if (!dev::finite((float)Tl::v_at(lds, i / D, i % D))) Tl::v_at(lds, i / D, i % D) = (T)0.f;
+    };
     const auto place_k = [](int n, int c) { return Tl::k(n, c); };
     const auto place_v = [](int n, int c) { return Tl::v(n, c); };
     int p0 = u.lo + wave * kTile;
@@ -212,7 +227,7 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
         const uint32_t there = present;
         const bool partial = there != 0xffffffffu || p0 + kTile > some, more = p0 + kWaves * kTile < u.hi;
         stage(kp, place_k, 0xffffffffu);
-        if constexpr (kCodes) scales[lane] = lane < 32 ? scale * c : scale;
+        if constexpr (kCodes) scales[lane] = lane < 32 ? scale * c : (dev::finite(scale) ? scale : NAN);        // (an infinite scale is a NaN one)
         if (Tl::kBeside) stage(vp, place_v, there);
         if (more) {
             row = row_of();
@@ -271,20 +286,13 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
             stage(vp, place_v, there);
             if (more) load(k.a.cache.v, vp);
         }
-        // Where some rows do not see some keys, no value that is not finite may meet a weight of zero: it is added to the
-        // rows that see it, and stands as zero in the product.
-        if (partial) {
-            constexpr int kOfChunk = 16 / (int)sizeof(T);
-            bool fine = !kCodes || dev::finite(scales[kTile + (lane & 31)]);
-            for (int i = lane; i < kTile * Tl::kChunks; i += 64) {
-                const T* const v = &Tl::v_at(tile, i / Tl::kChunks, i % Tl::kChunks * kOfChunk);
-#pragma unroll
-                for (int j = 0; j < kOfChunk; ++j) fine &= dev::finite((float)v[j]);
-            }
-            if (__any(!fine)) {
+        // Where some rows do not see some keys, no value that is not finite may meet a weight of zero that stands for that: it is added to
+        // the rows that see it, and is a zero in the product.  Codes and scales can only be NaN.
+        if (kCodes && partial) {
+            if (__any(!(all_finite(tile) && dev::finite(scales[kTile + (lane & 31)])))) {
                 for (int n = 0; n < kTile; ++n) {
                     if (!(there >> n & 1)) continue;
-                    const bool no = kCodes && !dev::finite(scales[kTile + n]);
+                    const bool no = !dev::finite(scales[kTile + n]);
 #pragma unroll
                     for (int t = 0; t < kDims; ++t)
 #pragma unroll
@@ -295,9 +303,8 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
                                 if (!dev::finite(v) && (seen[x] >> n & 1)) o[x][t][i] += v;
                         }
                 }
-                for (int i = lane; i < kTile * D; i += 64)
-                    if (!dev::finite((float)Tl::v_at(tile, i / D, i % D))) Tl::v_at(tile, i / D, i % D) = (T)0.f;
-                if (kCodes && lane >= 32 && !dev::finite(scales[lane])) scales[lane] = 0.f;
+                zero_others(tile);
+                if (lane >= 32 && !dev::finite(scales[lane])) scales[lane] = 0.f;
             }
         }
 #pragma unroll
@@ -316,6 +323,33 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
             }
             // the rounded weights' sum (see gdn_attention_wide.hip)
             if constexpr (!kCodes && sizeof(T) == 2) l[n] += dev::sum8(w[n], 0.f);
+        }
+        // The same of plain values, infinities among them: they are added times their weights, as the product would take them.
+        if (!kCodes && partial) {
+            if (__any(!all_finite(tile))) {
+                for (int j = 0; j < kTile; ++j) {
+                    if (!(there >> j & 1)) continue;
+                    float by[NT];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {        // the weight of the lane's row, from the lane that holds the key
+                        by[n] = 0.f;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (j == 16 * (i / 4) + 4 * quad + i % 4) by[n] = (float)w[n][i];
+                        by[n] = __shfl(by[n], j % 16 / 4 * 16 + col);
+                    }
+#pragma unroll
+                    for (int t = 0; t < kDims; ++t)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float v = (float)Tl::v_at(tile, j, 16 * t + 4 * quad + i);
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+                                if (!dev::finite(v) && (seen[n] >> j & 1)) o[n][t][i] += by[n] * v;
+                        }
+                }
+                zero_others(tile);
+            }
         }
 #pragma unroll
         for (int t = 0; t < kDims; ++t) {

@@ -182,7 +182,7 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
                             dev::codes8<__bf16, FORMAT>(kp[g][i][2 * x], kp[g][i][2 * x + 1]);
             if (wave == 0) {
                 kfactor(t)[lane] = ks * c;
-                vfactor(t)[lane] = special(t, there) && !dev::finite(vs) ? 0.f : vs;
+                vfactor(t)[lane] = dev::finite(vs) ? vs : (special(t, there) ? 0.f : NAN);       // (an infinite scale is a NaN one)
                 vstored(t)[lane] = vs;
             }
         }
@@ -328,16 +328,14 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
                 o[d] = mma32(__builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7), w[g], o[d]);
             }
     };
-    // Where keys are absent, or some rows do not see some, no value that is not finite may meet a weight of zero: absent
-    // keys' values are zeroed; others are added to the rows that see them, and are zeros in the product.  All waves
-    // come here together, between the landing of the tile's V and its sums.
-    const auto mend = [&](int t, uint64_t now) {
-        if (!special(t, now)) return;
-        constexpr int kCount = kTile * D / 8;
-        const int p0 = u.lo + t * kTile;
+    // Where keys are absent, or some rows do not see some, no value that is not finite may meet a weight of zero that stands for
+    // that: absent keys' values are zeroed here, between the landing of the tile's V and its sums, where all waves come
+    // together; whether others are left, for part().
+    const auto inspect = [&](int t, uint64_t now) {
+        if (!special(t, now)) return false;
         const lds_t vt = vtile(t);
         bool fine = true;
-        for (int i = threadIdx.x; i < kCount; i += kThreads) {
+        for (int i = threadIdx.x; i < kTile * D / 8; i += kThreads) {
             const int n = i / D * 8 + i % 64 / 8;                 // chunks as they lie: D to eight keys
             const lds_ptr<bf16x8_t> at = (lds_ptr<bf16x8_t>)vt + i;
             if (now >> n & 1) {
@@ -355,33 +353,53 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
         int bad = 0;
 #pragma unroll
         for (int i = 0; i < kWaves; ++i) bad |= flags[i];
-        if (bad) {
-            if (p0 < end) {
-                const uint64_t seen = sees.from(p0) & now;
-                for (int n = 0; n < kTile; ++n) {
-                    if (!(now >> n & 1)) continue;
-                    float by = 1.f;
-                    if constexpr (kCodes) by = vstored(t)[n];
+        dev::lds_barrier();
+        return __builtin_amdgcn_readfirstlane(bad) != 0;
+    };
+    // Values that are not finite, added to the rows that see them, and zeros in the product.  Plain ones (infinities among them) are
+    // added times their weights, as the product would take them, which are formed here for themselves: the tile's own, in the
+    // loop, then find the maximum where it has to be.  Codes and scales can only be NaN.
+    const auto part = [&](int t, uint64_t now) {
+        const lds_t vt = vtile(t);
+        if (works(t)) {
+            if constexpr (!kCodes) {
+                scores(t);
+                maximum(t, now);
+                const float sum = l;
+                weights(t);
+                l = sum;
+            }
+            const uint64_t seen = sees.from(u.lo + t * kTile) & now;
+            for (int n = 0; n < kTile; ++n) {
+                if (!(now >> n & 1)) continue;
+                float scale = 1.f, by = 1.f;                  // by: the row's weight, from the lane of its pair that holds the key
+                if constexpr (kCodes) {
+                    scale = vstored(t)[n];
+                } else {
 #pragma unroll
-                    for (int d = 0; d < kDims; ++d)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const int dim = 32 * d + 8 * (i / 4) + 4 * half + i % 4;
-                            float v = (float)*(lds_ptr<__bf16>)(vt + Tile<D>::v(n, dim / 8) + dim % 8 * 2);
-                            if (!dev::finite(by)) v = NAN;
-                            if (!dev::finite(v) && (seen >> n & 1)) o[d][i] += v;
-                        }
+                    for (int i = 0; i < 32; ++i)
+                        if (n == 16 * (i / 8) + 8 * (i / 4 & 1) + 4 * half + i % 4) by = (float)w[i / 8][i % 8];
+                    by = __shfl(by, 32 * (n >> 2 & 1) + col);
                 }
-            }
-            dev::lds_barrier();
-            for (int i = threadIdx.x; i < kCount; i += kThreads) {
-                const lds_ptr<bf16x8_t> at = (lds_ptr<bf16x8_t>)vt + i;
-                bf16x8_t v = *at;
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (!dev::finite((float)v[j])) v[j] = (__bf16)0.f;
-                *at = v;
+                for (int d = 0; d < kDims; ++d)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int dim = 32 * d + 8 * (i / 4) + 4 * half + i % 4;
+                        float v = (float)*(lds_ptr<__bf16>)(vt + Tile<D>::v(n, dim / 8) + dim % 8 * 2);
+                        if (!dev::finite(scale)) v = NAN;
+                        if (!dev::finite(v) && (seen >> n & 1)) o[d][i] += kCodes ? v : by * v;
+                    }
             }
+        }
+        dev::lds_barrier();
+        for (int i = threadIdx.x; i < kTile * D / 8; i += kThreads) {
+            const lds_ptr<bf16x8_t> at = (lds_ptr<bf16x8_t>)vt + i;
+            bf16x8_t v = *at;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (!dev::finite((float)v[j])) v[j] = (__bf16)0.f;
+            *at = v;
         }
         dev::lds_barrier();
     };
@@ -399,8 +417,9 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
     asm volatile("" : "+v"(sees.all), "+v"(sees.first), "+v"(sees.mask));
     land(-1);
     dev::lds_barrier();
-    mend(0, there[1]);
+    bool bad = inspect(0, there[1]);
     for (int t = 0; t < tiles; ++t) {
+        if (__builtin_expect(bad, 0)) part(t, there[1]);        // (before the next tile's loads take registers)
         issue(t);
         if (works(t)) {
             scores(t);
@@ -410,7 +429,7 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
         }
         land(t);
         dev::lds_barrier();
-        if (t + 1 < tiles) mend(t + 1, there[1]);
+        bad = t + 1 < tiles && inspect(t + 1, there[1]);
     }
 
     float x, y;

@@ -34,7 +34,8 @@
  *               A row's results are bitwise the same whatever shares its call, and a prompt
  *               token's do not depend on how its prompt is cut into calls.
  *   Non-finite  A key or value that a token does not see leaves it untouched, whatever it
- *               holds: stale cache rows may hold infinities and NaN.
+ *               holds: stale cache rows may hold infinities and NaN.  One that it sees counts
+ *               as in the formula, an infinite value whose weight underflowed to zero as NaN.
  */
 #ifndef GDN_ATTENTION_H
 #define GDN_ATTENTION_H

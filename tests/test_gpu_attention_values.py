@@ -1,4 +1,4 @@
-"""What attention makes of values on the GPU: rows that a few keys dominate."""
+"""What attention makes of values on the GPU: rows that a few keys dominate, and infinities that a token sees."""
 import math
 
 import pytest
@@ -9,8 +9,9 @@ from tests import attention_cases as C
 from tests import attention_reference as R
 
 pytestmark = pytest.mark.gpu
-BF16 = torch.bfloat16
+BF16, F32 = torch.bfloat16, torch.float32
 DEV = "cuda"
+FORMATS = [(BF16, None), (BF16, "e4m3"), (BF16, "int8"), (F32, None), (F32, "e4m3"), (F32, "int8")]
 
 
 def prefill(q, cache, table, past, scale):
@@ -59,3 +60,47 @@ def test_rounded_weights_cancel(hq, d, past, new, how):
     half = torch.ldexp(torch.ones_like(exact), torch.frexp(exact.abs() + before).exponent - 9)
     off = (o - exact).abs()
     assert (off <= before + half).all(), "off by up to %.3g of what is allowed" % float((off / (before + half)).max())
+
+
+@pytest.mark.parametrize("dtype,fmt", FORMATS)
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_infinities_that_are_seen(d, dtype, fmt):
+    """An infinite value counts by its weight: an infinity where that is positive, NaN where it underflows to zero, wherever the
+    token stands in its call.  (In 8 bits such a head is NaN.)"""
+    n, first, second, block, hq = 260, 20, 140, 16, 2
+    table, rows = C.pages([n], block, DEV, 5)
+    own = C.owned_rows(table, block, [n])
+    cache = C.filled_cache(rows, 1, d, dtype, fmt, own, DEV, 5)
+    # query head 0's score is higher with key 10 than with any other by 288 powers of two; query head 1 sees all alike
+    q = torch.ones(n, hq, d, dtype=dtype, device=DEV)
+    q[:, 1] = 0
+    k = torch.zeros(rows, 1, d, dtype=dtype, device=DEV)
+    k[own[10]] = 1
+    v = torch.ones(rows, 1, d, dtype=dtype, device=DEV)
+    v[own[first], :, 3] = math.inf
+    v[own[first], :, 4] = -math.inf
+    v[own[second], :, 5] = math.inf
+    A.gdn_kv_cache_write(k, v, torch.arange(rows, device=DEV), **cache)
+    scale = 200.0 / d
+    whole = prefill(q, cache, table, 0, scale)
+    finite = torch.isfinite(whole.float())
+    assert finite[:first].all()
+    if fmt is None:
+        assert whole[first:, 0, 3: 5].isnan().all() and whole[second:, 0, 5].isnan().all()
+        assert (whole[first:, 1, 3] == math.inf).all() and (whole[first:, 1, 4] == -math.inf).all() and (whole[second:, 1, 5] == math.inf).all()
+        assert finite[first: second, :, 5].all() and finite[:, :, 6:].all() and finite[:, :, :3].all()
+    else:
+        assert whole[first:].isnan().all()
+
+    def same(a, b):
+        return torch.equal(a.float().nan_to_num(7.0, 8.0, 9.0), b.float().nan_to_num(7.0, 8.0, 9.0))
+
+    for cuts in ([0, 1, 20, 21, 64, 139, n], [0, 30, 31, 128, 141, n], [0, 70, 140, 200, n]):
+        for a, b in zip(cuts, cuts[1:]):
+            assert same(prefill(q[a:b], cache, table, a, scale), whole[a:b]), (a, b)
+    # and in decode rows: a chain, where some tokens do not see the infinity or all do
+    for start in (5, 15, 30, 100, 135, 150, 200):
+        for per in (1, 7, 50):
+            want = whole[start: start + per].float()
+            got = decode(q[start: start + per].contiguous(), cache, table, start, scale).float()
+            assert torch.equal(torch.isfinite(got), torch.isfinite(want)) and torch.equal(got.isnan(), want.isnan()), (start, per)
