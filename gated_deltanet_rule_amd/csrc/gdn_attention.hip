@@ -445,7 +445,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttentionKernelArgs k) {
     const unsigned token = (unsigned)at / (unsigned)k.a.H_q;
     const int keys = row_keys(k.a, k.a.past[dev::divide(token, k.rows)]);
     if (keys <= 0 || keys > k.a.max_keys) return;
-    const int span = span_keys(k.a.tokens_per_row * (int)k.group.d, keys), spans = (keys + span - 1) / span;
+    const int span = span_keys(k.a.tokens_per_row * (int)k.group.d, keys), spans = span_count(keys, span);
     if (spans == 1) return;
     const float2 mine = lane < spans ? k.stats[at * k.spans + lane] : float2{-INFINITY, 0.f};
     float x[kSums][N] = {}, v[kEach][kSums][N];
@@ -494,11 +494,6 @@ AttentionKernelArgs kernel_args(const AttentionArgs& a) {
     k.block = Divisor((uint32_t)a.kv_block);
     k.group = Divisor((uint32_t)(a.H_q / a.cache.num_heads));
     return k;
-}
-
-int most_spans(int rows, int64_t keys) {
-    const int64_t n = (keys + least_span(rows) - 1) / least_span(rows);
-    return (int)(n < kMaxSpans ? (n > 0 ? n : 1) : kMaxSpans);
 }
 
 template <typename T, int FORMAT, int D, int NT>

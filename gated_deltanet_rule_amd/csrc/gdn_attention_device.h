@@ -130,17 +130,6 @@ __device__ __forceinline__ bool finite(float x) { return fabsf(x) < INFINITY; }
 
 }  // namespace dev
 
-// Keys of a span of a long context: at least this many for so many rows of a head, doubled until kMaxSpans suffice.  Short
-// spans keep more of the chip busy for few requests, long ones start and join less often (16 rows of 128 dims in bf16 at
-// 256 / 512 / 1024 keys: one request of 1024 keys 9.5 / 12 / 17 us, 64 requests of up to 8192 keys 266 / 245 / 235 us).
-constexpr int kMaxSpans = 64;
-__host__ __device__ inline int least_span(int rows) { return rows <= 64 ? 512 : 1024; }
-__host__ __device__ inline int span_keys(int rows, int keys) {
-    int span = least_span(rows);
-    while (keys > kMaxSpans * (int64_t)span) span *= 2;
-    return span;
-}
-
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct AttentionKernelArgs {
@@ -219,7 +208,7 @@ __device__ __forceinline__ bool decode_unit(const AttentionKernelArgs& k, int pe
         return false;
     }
     const int span = span_keys(u.rows, keys);
-    u.spans = (keys + span - 1) / span;
+    u.spans = span_count(keys, span);
     if (u.span >= u.spans) return false;
     u.past = u.past < k.a.capacity ? u.past : k.a.capacity;
     u.lo = u.span * span;
