@@ -1,4 +1,5 @@
-"""Decode rows of long contexts on the GPU: row lengths up to the most that a table can hold."""
+"""Decode rows of long contexts on the GPU: more spans than one sum of the join takes, spans that have to double, and
+row lengths up to the most that a table can hold."""
 import pytest
 import torch
 
@@ -19,6 +20,60 @@ def decode(q, cache, table, kv_block, past, per, scale, max_keys=0):
     A.gdn_attention_decode(q, o=o, computed=C.i32(past, DEV), kv_table=table, kv_block=kv_block, scale=scale, tokens_per_row=per, max_keys=max_keys,
                            workspace=ws, **cache)
     return o
+
+
+# Spans of 512 keys up to 64 rows of a head, of 1024 beyond; doubled from 32768 (65536) keys on.  20000 keys: 40 (20) spans.
+# 40 tokens of a group of 2 are 80 rows, in bf16 for the kernel of many rows.
+@pytest.mark.parametrize("dtype,fmt", [(BF16, None), (BF16, "e4m3"), (F32, "int8")])
+@pytest.mark.parametrize("keys", [20000, 32768, 32769, 65536, 65537, 70001])
+@pytest.mark.parametrize("per,hq,hkv,d", [(1, 4, 1, 128), (1, 2, 2, 64), (40, 2, 1, 128), (3, 1, 1, 256)])
+def test_long_rows(per, hq, hkv, d, keys, dtype, fmt):
+    past = [keys - per]
+    table, rows = C.pages([keys], 64, DEV, keys)
+    cache = C.filled_cache(rows, hkv, d, dtype, fmt, C.owned_rows(table, 64, [keys]), DEV, 2)
+    q = C.queries(per, hq, d, dtype, DEV, 4) * 3          # some keys count far more than others, wherever they lie
+    o = decode(q, cache, table, 64, past, per, d ** -0.5)
+    R.check("long", o, *R.attention(q, cache, table, 64, past, [per], d ** -0.5))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("keys", [513, 8192, 8193, 32768, 32769, 65537, 131072, 131073])
+@pytest.mark.parametrize("per,hq,d", [(1, 2, 64), (40, 2, 128), (2, 1, 256)])
+def test_every_key_counts_once(per, hq, d, keys, dtype):
+    """With a scale of zero all weights are 1, and dim i of the values marks the i-th part of the keys: the sums are whole
+    numbers below 2^24, exact in any order, and each output is its part's share of the keys."""
+    table, rows = C.pages([keys], 64, DEV, keys)
+    own = C.owned_rows(table, 64, [keys])
+    cache = C.filled_cache(rows, 1, d, dtype, None, own, DEV, 2)
+    part = torch.arange(keys, device=DEV) * d // keys
+    cache["v_cache"][own, 0] = torch.nn.functional.one_hot(part, d).to(dtype)
+    q = C.queries(per, hq, d, dtype, DEV, 4)
+    mask = torch.full((per,), -1, dtype=torch.int64, device=DEV)          # every token sees all of them
+    o = torch.full(q.shape, 5.0, dtype=dtype, device=DEV)
+    ws = A.alloc_attention_workspace(q, cache["k_cache"], tokens_per_row=per, max_keys=keys)
+    if ws is not None:
+        ws.fill_(0xff)
+    A.gdn_attention_decode(q, o=o, computed=C.i32([keys - per], DEV), kv_table=table, kv_block=64, scale=0.0, tokens_per_row=per, tree_mask=mask,
+                           max_keys=keys, workspace=ws, **cache)
+    share = (torch.bincount(part, minlength=d).double() / keys).expand(per, hq, d)
+    # the sum's inverse and the product with it, then the output's rounding
+    R.check("share", o, share, share * (2 * 2.0 ** -24 + R.HALF_STEP[dtype] * (1 + 2.0 ** -22)))
+
+
+@pytest.mark.parametrize("dtype,fmt", [(BF16, "int8"), (F32, None)])
+@pytest.mark.parametrize("per,hq,hkv,d", [(1, 8, 2, 128), (40, 2, 1, 64)])
+def test_a_long_row_beside_short_ones(per, hq, hkv, d, dtype, fmt):
+    """Alone with a tight launch and beside rows of 1 to 33000 keys: the same bits."""
+    keys = [per, 70001, 513 + per, 33000]
+    past, block = [n - per for n in keys], 24
+    table, rows = C.pages(keys, block, DEV, 6)
+    cache = C.filled_cache(rows, hkv, d, dtype, fmt, C.owned_rows(table, block, keys), DEV, 6)
+    q = C.queries(4 * per, hq, d, dtype, DEV, 6)
+    together = decode(q, cache, table, block, past, per, d ** -0.5)
+    R.check("together", together, *R.attention(q, cache, table, block, past, [per] * 4, d ** -0.5))
+    for b in range(4):
+        mine = slice(b * per, (b + 1) * per)
+        assert torch.equal(decode(q[mine], cache, table[b: b + 1].contiguous(), block, past[b: b + 1], per, d ** -0.5, max_keys=keys[b]), together[mine]), b
 
 
 @pytest.mark.parametrize("dtype,per", [(BF16, 1), (F32, 1), (BF16, 33)])
