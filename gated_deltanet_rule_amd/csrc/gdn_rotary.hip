@@ -37,13 +37,24 @@ __device__ __forceinline__ void store(T* p, const float (&v)[V]) {
     else dev::store_vec(p, v);
 }
 
-// cos and sin of p f, the product exact to 2^-53 and reduced to half a turn either way while it
-// is in 64 bits; sincospif is good to about one unit in the last place.
+// cos and sin of p f, times factor.  p f has up to 55 bits and 1 / (2 pi) more: products are taken as a double and the rest that
+// it leaves off, so that the part of a turn is exact to 2^-52 however many turns there are.  fp32 values take cosine and sine of it in
+// 64 bits, rounded once; for bf16 ones fp32 does, 2^-15 of a half step off.
+template <typename T>
 __device__ __forceinline__ float2 turn(int p, float f, float factor) {
-    const double turns = (double)p * (double)f * 0.15915494309189533577;
-    float s, c;
-    sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
-    return {c * factor, s * factor};
+#pragma clang fp contract(off)             // (a product taken into a sum would be another number than the one whose rest is taken)
+    constexpr double kTurn = 0x1.45f306dc9c883p-3, kRest = -0x1.6b01ec5417056p-57;        // 1 / (2 pi) and what is left of it
+    const double x = (double)p * (double)f, rest = fma((double)p, (double)f, -x), turns = x * kTurn;
+    const double part = (turns - rint(turns)) + (fma(x, kTurn, -turns) + fma(rest, kTurn, x * kRest));
+    if constexpr (sizeof(T) == 4) {
+        double s, c;
+        sincospi(2. * part, &s, &c);
+        return {(float)(c * factor), (float)(s * factor)};
+    } else {
+        float s, c;
+        sincospif(2.f * (float)part, &s, &c);
+        return {c * factor, s * factor};
+    }
 }
 
 // A head's units: pairs V j .. V j + V - 1 for j < turned, then 2 V elements each that only copy.
@@ -54,7 +65,7 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryKernelArgs k) {
     const int half = s.rotary_dim / 2, heads = s.num_q_heads + s.num_k_heads;
     const int64_t token = blockIdx.x;
     const int position = k.a.positions[token];
-    for (int i = threadIdx.x; i < half; i += kThreads) turns[i] = turn(position, k.a.inv_freq[i], s.factor);
+    for (int i = threadIdx.x; i < half; i += kThreads) turns[i] = turn<T>(position, k.a.inv_freq[i], s.factor);
     __syncthreads();
     if (position < 0) return;
     const int units = heads * (int)k.units_of_head.d;
