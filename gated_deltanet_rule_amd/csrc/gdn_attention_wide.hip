@@ -54,11 +54,14 @@ struct Tile {
 
 // 16 bytes a lane from memory into LDS, past the registers: lane l's to dst + 16 l.  In assembly, since the
 // compiler has every transposing load wait for such a load in flight, whatever tile it fills; landed() waits
-// for a wave's own, and a barrier behind that for all.  (m0 holds nothing between instructions: whatever needs it
-// sets it.)
+// for a wave's own, and a barrier behind that for all.  (The compiler sets m0 right before what needs it and
+// takes none of it over an assembly that says it writes it; that it warns of any such register is silenced here.)
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void load_to_lds(const void* src, lds_t dst) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"((unsigned)(uintptr_t)dst), "v"(src) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"((unsigned)(uintptr_t)dst), "v"(src) : "memory", "m0");
 }
+#pragma clang diagnostic pop
 __device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" : : : "memory"); }
 
 // LDS of a workgroup: two tiles of K, two of V, and their keys' factors (scores, values, values as they are
