@@ -122,13 +122,7 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
     int entry = -1, key = 0, row = -1;
     const auto lookup = [&](int p0) {
         key = p0 + (lane & 31);
-        const unsigned page = dev::divide((unsigned)key, k.block);
-        entry = pages.table[page < (unsigned)pages.width ? page : (unsigned)pages.width - 1];
-    };
-    const auto row_of = [&]() {
-        const unsigned page = dev::divide((unsigned)key, k.block);
-        const int64_t at = (int64_t)entry * k.block.d + ((unsigned)key - page * k.block.d);
-        return key < u.hi && page < (unsigned)pages.width && entry >= 0 && at < pages.num_rows ? (int)at : -1;
+        entry = pages.entry(key);
     };
     u32x4_t kp[kLoads], vp[kLoads];
     float scale = 0.f;                                  // of the lane's key: K's in the lower half of the wave, V's in the upper
@@ -188,7 +182,7 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
     const bool any = p0 < u.hi;
     if (any) {
         lookup(p0);
-        row = row_of();
+        row = pages.row(key, entry, u.hi);
         load_scales();
         load(k.a.cache.k, kp);
         lookup(p0 + kWaves * kTile);
@@ -230,7 +224,7 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
         if constexpr (kCodes) scales[lane] = lane < 32 ? scale * c : (dev::finite(scale) ? scale : NAN);        // (an infinite scale is a NaN one)
         if (Tl::kBeside) stage(vp, place_v, there);
         if (more) {
-            row = row_of();
+            row = pages.row(key, entry, u.hi);
             present = (uint32_t)__ballot(row >= 0);
             load_scales();
             load(k.a.cache.k, kp);

@@ -100,13 +100,7 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
     int entry = -1, key = 0;
     const auto lookup = [&](int t) {
         key = u.lo + t * kTile + lane;
-        const unsigned page = dev::divide((unsigned)key, k.block);
-        entry = pages.table[page < (unsigned)pages.width ? page : (unsigned)pages.width - 1];
-    };
-    const auto row_of = [&]() {
-        const unsigned page = dev::divide((unsigned)key, k.block);
-        const int64_t at = (int64_t)entry * k.block.d + ((unsigned)key - page * k.block.d);
-        return key < u.hi && page < (unsigned)pages.width && entry >= 0 && at < pages.num_rows ? (int)at : -1;
+        entry = pages.entry(key);
     };
     u32x4_t kp[kGroups][kPieces], vp[kGroups][kPieces];
     float ks = 0.f, vs = 0.f;
@@ -204,7 +198,7 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
     };
     uint64_t there[2] = {0, 0};                    // which keys of tiles t and t + 1 are there, after issue(t)
     const auto issue = [&](int t) {                // the next tile, into the buffers of the one before
-        const int next = t + 1 < tiles ? row_of() : -1;
+        const int next = t + 1 < tiles ? pages.row(key, entry, u.hi) : -1;
         there[0] = there[1];
         there[1] = __ballot(next >= 0);
         if (t + 1 < tiles) {
@@ -407,7 +401,7 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
         dev::lds_barrier();
     };
     {
-        const int row = row_of();
+        const int row = pages.row(key, entry, u.hi);
         there[1] = __ballot(row >= 0);
         load_k(0, row);
         load_v(0, row);
