@@ -220,7 +220,7 @@ gdn_status gdn_attention_prefill(const gdn_kv_cache* cache, int32_t num_q_heads,
 size_t gdn_attention_decode_workspace_size(const gdn_kv_cache* cache, int32_t num_q_heads, int32_t num_rows, int32_t tokens_per_row,
                                            int64_t max_keys) {
     if (check_cache_shape(cache) != GDN_OK || check_heads(cache, num_q_heads, 1.f) != GDN_OK || num_rows < 0 || tokens_per_row < 1 ||
-        tokens_per_row > kMaxRowTokens || max_keys < 0)
+        tokens_per_row > kMaxRowTokens || (int64_t)num_rows * tokens_per_row > kMaxTokens || max_keys < 0)
         return 0;
     return gdn::attention_workspace_bytes(num_q_heads, cache->num_heads, cache->head_dim, num_rows, tokens_per_row,
                                           max_keys < kMaxTokens ? max_keys : kMaxTokens);

@@ -142,7 +142,7 @@ gdn_status gdn_attention_prefill(const gdn_kv_cache* cache, int32_t num_q_heads,
                                  void* o, hipStream_t stream);
 
 /* Bytes of device workspace that gdn_attention_decode needs for at most num_rows rows,
- * tokens_per_row tokens of each and max_keys keys (0 for an unsupported shape): a workspace of
+ * tokens_per_row tokens of each and max_keys keys (0 for an unsupported shape or size): a workspace of
  * this size serves every smaller call too. */
 size_t gdn_attention_decode_workspace_size(const gdn_kv_cache* cache, int32_t num_q_heads,
                                            int32_t num_rows, int32_t tokens_per_row,
