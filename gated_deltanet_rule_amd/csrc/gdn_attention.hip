@@ -283,7 +283,7 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
         // Where some rows do not see some keys, no value that is not finite may meet a weight of zero that stands for that: it is added to
         // the rows that see it, and is a zero in the product.  Codes and scales can only be NaN.
         if (kCodes && partial) {
-            if (__any(!(all_finite(tile) && dev::finite(scales[kTile + (lane & 31)])))) {
+            if (__builtin_expect(__any(!(all_finite(tile) && dev::finite(scales[kTile + (lane & 31)]))), 0)) {
                 for (int n = 0; n < kTile; ++n) {
                     if (!(there >> n & 1)) continue;
                     const bool no = !dev::finite(scales[kTile + n]);
@@ -320,7 +320,7 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
         }
         // The same of plain values, infinities among them: they are added times their weights, as the product would take them.
         if (!kCodes && partial) {
-            if (__any(!all_finite(tile))) {
+            if (__builtin_expect(__any(!all_finite(tile)), 0)) {
                 for (int j = 0; j < kTile; ++j) {
                     if (!(there >> j & 1)) continue;
                     float by[NT];
