@@ -15,7 +15,9 @@
 // whole cache rows, neighbouring lanes neighbouring bytes, one tile ahead of the sums in registers, and
 // go through the wave's own LDS, so that no wave waits for another.  (Loaded straight into the operands, 16 lanes in
 // 16 rows, K took the memory path up to four times as long: 298 us instead of 266 for 64 requests of up to 8192 keys, 136
-// instead of 66 for one of 131072 keys in 8 bits.)  Now 240 us, 5.1 TB/s of keys and values, and 58.6 us, 4.7 TB/s.
+// instead of 66 for one of 131072 keys in 8 bits.)  Now 240 us, 5.1 TB/s of keys and values, and 58.7 us, 4.7 TB/s.
+// fp32 prompts share a staged tile among 16 or 32 rows of one wave only: 4096 tokens of 8 heads over 2, 128 dims, 505 us, 68 TFLOP/s
+// of 153 for a large library product; 256 dims 1.26 ms, 55 TFLOP/s, one wave to a SIMD.
 //
 // With bf16 the weights are rounded to bf16 for the second product.  As two bf16 parts each, in two products, they left only the
 // output's rounding: 240.5 us for 240.0, but 17.1 for 16.3 and 41.4 for 38.2 (16 requests of 4096 keys in 8 bits, two heads of
@@ -47,7 +49,7 @@ struct Tile {
     static constexpr int kSum = 16 * (D + 4) * 4;                                           // 16 rows of a wave's sums
     // Where two tiles fit twice into LDS, V has a place of its own and is loaded and staged beside K, else it takes K's after
     // the scores: 57.6 us beside and 65 after (131072 keys of 128 dims in 8 bits); but 44.5 and 42.1 (16 x 4096 keys of 256
-    // dims in bf16), 608 and 352 (a prompt of 2048 tokens, 256 dims in fp32, whose two tiles leave room for two waves).
+    // dims in bf16), 608 and 362 (a prompt of 2048 tokens, 256 dims in fp32, whose two tiles leave room for two waves).
     static constexpr bool kBeside = kRow <= 256;
     static constexpr int kV = kBeside ? kTile * kRow : 0, kUsed = kV + kTile * kVRow, kBytes = kUsed > kSum ? kUsed : kSum;
     __device__ static __forceinline__ int k(int key, int c) { return key * kRow + (c ^ (kChunks >= 16 ? key & 15 : key >> 1 & 7)) * 16; }
@@ -511,7 +513,8 @@ hipError_t launch_decode(const AttentionArgs& a, hipStream_t stream) {
     k.part = static_cast<float*>(a.workspace);
     k.stats = reinterpret_cast<float2*>(k.part + (k.spans > 1 ? heads * k.spans * D : 0));
     // as many row tiles to a wave as the rows fill and the registers hold; more rows share the keys in gdn_attention_wide.hip (two
-    // heads of 16 requests with 4096 keys, 48 / 64 rows here and 96 there: 61 / 64 and 36 us at 128 dims, where four tiles spill)
+    // heads of 16 requests with 4096 keys, here / there: 64 dims, 32 rows 15.8 / 16.2 us, 64 rows 22.7 / 19.6, 96 rows 31.7 / 26.0; 128
+    // dims, 32 rows 25.6 / 20.8, 48 rows 35.6 / 25.7, 64 rows 36.8 / 26.4; 256 dims, 32 rows 57.3 / 52.9, 64 rows 90.7 / 58.4)
     constexpr int most = row_tiles<T, D>();
     hipError_t e;
     if (sizeof(T) == 2 && rows > 16 * most) e = launch_attention_wide(k, stream);
@@ -533,7 +536,7 @@ hipError_t launch_prompt(const AttentionKernelArgs& k, hipStream_t stream) {
 }
 
 // One row tile to a wave where two would leave compute units without work (one / two of 128 dims, 8 heads over 2: 512 tokens
-// 22.6 / 31.6 us, 1024 59 / 56, 4096 612 / 506; of 64 dims 12.9 / 18.1, 27.5 / 30.6, 237 / 223).
+// 22.3 / 31.2 us, 1024 59 / 56, 4096 602 / 505; of 64 dims 12.7 / 17.9, 27.6 / 31.3, 235 / 221).
 template <int FORMAT, int D>
 hipError_t launch_prompt(const AttentionArgs& a, hipStream_t stream) {
     constexpr int most = row_tiles<float, D>();

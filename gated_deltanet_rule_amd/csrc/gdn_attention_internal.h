@@ -25,7 +25,10 @@ struct Divisor {
 
 // Keys of a span of a long context: at least this many for so many rows of a head, doubled until kMaxSpans suffice.  Short
 // spans keep more of the chip busy for few requests, long ones start and join less often (16 rows of 128 dims in bf16 at
-// 256 / 512 / 1024 keys: one request of 1024 keys 9.5 / 12 / 17 us, 64 requests of up to 8192 keys 266 / 245 / 235 us).
+// 256 / 512 / 1024 keys: one request of 1024 keys 9.5 / 12 / 17 us, 64 requests of up to 8192 keys 266 / 245 / 235 us).  With more
+// rows a span's partial sums weigh more: 512 / 1024 / 2048 keys, 16 requests with eight heads and up to 8192 keys, 60 rows 104 / 97 / 93
+// us, 68 rows 109 / 99 / 94, 128 rows 136 / 113 / 104, 256 rows 221 / 166 / 166; with two heads and 4096 keys 64 rows 29 / 34 / 54, 68 rows
+// 31 / 35 / 55, 128 rows 35 / 37 / 57.  fp32, eight heads, 68 rows 542 / 497 / 506.
 constexpr int kMaxSpans = 64;
 __host__ __device__ inline int least_span(int rows) { return rows <= 64 ? 512 : 1024; }
 __host__ __device__ inline int span_keys(int rows, int keys) {

@@ -8,12 +8,17 @@
 // product's operand as they come out of the first.
 //
 // The matrix cores bound it, as far as they are fed: a wave's products take 1024 cycles of a tile at 128 dims, its softmax 700
-// of the vector ALU, which the other wave of the SIMD has to fill.  8 prompts of up to 4096 tokens, 128 dims: 461 us,
-// 860 TFLOP/s where a large library product reaches 1150.  8192 tokens behind 24576, 256 dims, 8-bit codes: 5.2 ms, 740
-// TFLOP/s with one wave to a SIMD.  Trees of 32 tokens (128 rows) of 16 requests: 108 us with the join, 410 TFLOP/s, held by the
-// start and end of each span.  Tried and not better: eight waves in two phases (466 and 463 us), four tiles of
+// of the vector ALU, which the other wave of the SIMD has to fill.  8 prompts of up to 4096 tokens, 128 dims: 466 us,
+// 854 TFLOP/s where a large library product reaches 1150.  (Its clock is what the card's power leaves: 2.06 to 1.83 GHz by the cycles
+// counted in 30 calls in a row, 482 to 553 us.)  8192 tokens behind 24576, 256 dims, 8-bit codes: 5.1 ms, 750
+// TFLOP/s with one wave to a SIMD.  Trees of 32 tokens (128 rows) of 16 requests: 108 us with the join, 420 TFLOP/s, held by the
+// start and end of each span.  A prompt's keys are not split over workgroups: 16 tokens behind 32768, 8 heads, are 8 workgroups, 714
+// us (a chain of decoded tokens: 41).  Tried and not better: eight waves in two phases (466 and 463 us), four tiles of
 // 32 keys in turn (477), loads behind the scores (511), the next tile's scores beside this one's exponentials (458, but spilling at 256
 // dims), wave priorities, a workgroup's heads on one XCD.
+//
+// Weights are rounded to bf16 for the second product, the one rounding below fp32: as two bf16 parts they would take half as many
+// products again, of what bounds the kernel.
 #include <hip/hip_runtime.h>
 
 #include "gdn_attention_device.h"

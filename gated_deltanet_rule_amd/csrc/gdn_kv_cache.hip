@@ -5,9 +5,10 @@
 // Memory-bound: every value crosses HBM once each way.  LPH lanes share a head, 8 values to a
 // lane (bf16: one 16-byte vector), so a head's largest value takes log2(LPH) steps across lanes
 // and K and V of a head are in flight together.
-// 131072 tokens of 8 heads of 128 dims, bf16 to 8 bits and back: 185 us written (4.3 TB/s, from rows of 6 KB and into scattered
-// pages) and 140 read (5.8 TB/s).  Four heads to a thread instead of one, for more loads in flight: 342 us
-// both instead of 328.
+// 131072 tokens of 8 heads of 128 dims, bf16 to 8 bits, into rows at random / pages of 16 rows / in order: written in 173 / 169 /
+// 162 us (4.7 to 5.0 TB/s; an even copy reaches 6.57), read in 159 / 157 / 138 (5.1 to 5.9); plain 215 / 214 / 201 and 208 / 208 / 183.
+// Where the rows lie costs little; what else keeps the write from the copy's rate is not isolated.  Four heads to a thread instead of
+// one, for more loads in flight: 342 us both ways instead of 328.
 #include <hip/hip_runtime.h>
 
 #include "gdn_attention_internal.h"

@@ -5,8 +5,11 @@
 // Memory-bound: every value crosses HBM once each way.  A workgroup takes a token: its threads
 // first form the cosines and sines, one frequency each, into LDS, where all heads
 // share them; then they turn the heads' pairs, V pairs to a thread as two 16-byte vectors.
-// 131072 tokens of 32 + 8 heads of 128 dims in bf16: 468 us, 5.7 TB/s of 6.6 for a large copy; 64 tokens: 3.5 us, of
-// which the copy's share is 0.2 and the rest a launch.  Where rows or parts are not whole vectors V is 1.
+// 131072 tokens of 32 + 8 heads of 128 dims in bf16: 467 us, 5.7 TB/s of 6.6 for a large copy; 64 tokens: 3.4 us, of
+// which the copy's share is 0.2 and the rest a launch.  4099 tokens of 16 + 2 heads of 256 dims in fp32: 35 us, where an even copy of as
+// much takes 25; 65536 tokens 462 us, 5.2 TB/s.
+// Where rows or parts are not whole vectors V is 1, and a token of few heads leaves most of its workgroup idle: 65536 tokens of 8 + 2 heads
+// of 80 dims, all of the head 65 us (3.2 TB/s), a quarter of it 125 (1.7); of 1 + 1 heads of 64 dims 44 us (0.8).
 #include <hip/hip_runtime.h>
 
 #include "gdn_attention_internal.h"
