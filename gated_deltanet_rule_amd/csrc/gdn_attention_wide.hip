@@ -8,11 +8,11 @@
 // product's operand as they come out of the first.
 //
 // The matrix cores bound it, as far as they are fed: a wave's products take 1024 cycles of a tile at 128 dims, its softmax 700
-// of the vector ALU, which the other wave of the SIMD has to fill.  8 prompts of up to 4096 tokens, 128 dims: 466 us,
-// 854 TFLOP/s where a large library product reaches 1150.  (Its clock is what the card's power leaves: 2.06 to 1.83 GHz by the cycles
-// counted in 30 calls in a row, 482 to 553 us.)  8192 tokens behind 24576, 256 dims, 8-bit codes: 5.1 ms, 750
+// of the vector ALU, which the other wave of the SIMD has to fill.  8 prompts of up to 4096 tokens, 128 dims: 452 to 470
+// us, 870 TFLOP/s where a large library product reaches 1150.  (Its clock is what the card's power leaves: 2.06 to 1.83 GHz by the cycles
+// counted in 30 calls in a row, 482 to 553 us.)  8192 tokens behind 24576, 256 dims, 8-bit codes: 4.87 ms, 790
 // TFLOP/s with one wave to a SIMD.  Trees of 32 tokens (128 rows) of 16 requests: 108 us with the join, 420 TFLOP/s, held by the
-// start and end of each span.  A prompt's keys are not split over workgroups: 16 tokens behind 32768, 8 heads, are 8 workgroups, 714
+// start and end of each span.  A prompt's keys are not split over workgroups: 16 tokens behind 32768, 8 heads, are 8 workgroups, 704
 // us (a chain of decoded tokens: 41).  Tried and not better: eight waves in two phases (466 and 463 us), four tiles of
 // 32 keys in turn (477), loads behind the scores (511), the next tile's scores beside this one's exponentials (458, but spilling at 256
 // dims), wave priorities, a workgroup's heads on one XCD.
@@ -419,9 +419,10 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
     asm volatile("" : "+v"(sees.all), "+v"(sees.first), "+v"(sees.mask));
     land(-1);
     dev::lds_barrier();
-    bool bad = inspect(0, there[1]);
+    // (right behind the barrier, where no other tile's loads or scores are live, and marked as seldom: 4.87 ms for 8192 tokens of 256 dims in 8
+    // bits, 5.1 to 9.1 in other places)
+    if (__builtin_expect(inspect(0, there[1]), 0)) part(0, there[1]);
     for (int t = 0; t < tiles; ++t) {
-        if (__builtin_expect(bad, 0)) part(t, there[1]);        // (before the next tile's loads take registers)
         issue(t);
         if (works(t)) {
             scores(t);
@@ -431,7 +432,7 @@ __device__ __forceinline__ void attend(const AttentionKernelArgs& k, const Unit&
         }
         land(t);
         dev::lds_barrier();
-        bad = t + 1 < tiles && inspect(t + 1, there[1]);
+        if (t + 1 < tiles && __builtin_expect(inspect(t + 1, there[1]), 0)) part(t + 1, there[1]);
     }
 
     float x, y;

@@ -135,7 +135,7 @@ gdn_status gdn_kv_cache_read(const gdn_kv_cache* cache, int64_t num_tokens, cons
  *   o           device [total_tokens, num_q_heads, head_dim] (dtype), dense, written; a token
  *               that sees no key (all absent) gets zeros
  * The keys of a row are not split over workgroups here: a few tokens behind a long context are far faster as a
- * chain of gdn_attention_decode (16 tokens behind 32768, 8 heads: 41 us for 714).
+ * chain of gdn_attention_decode (16 tokens behind 32768, 8 heads: 41 us for 704).
  */
 gdn_status gdn_attention_prefill(const gdn_kv_cache* cache, int32_t num_q_heads, float scale,
                                  int32_t num_seqs, int64_t total_tokens, const int32_t* cu_seqlens,
