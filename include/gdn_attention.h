@@ -27,15 +27,17 @@
  *   Arithmetic  Scores, softmax statistics, sums and scales are fp32.  With bf16 activations
  *               the softmax's weights, times the value's scale where there is one, are rounded
  *               to bf16 on their way into the matrix cores, by at most 2^-8 of each; 8-bit
- *               codes are exact there.  Over a plain cache the rounded weights are summed, so that
- *               the rounding of a key that has nearly all of the weight cancels.  With fp32 activations nothing is rounded below fp32.
+ *               codes are exact there.  Over a plain cache the rounded weights are summed, so
+ *               that the rounding of a key that has nearly all of the weight cancels.  With fp32
+ *               activations nothing is rounded below fp32.
  *               Values are summed before the sum is divided, with weights of up to 2^8: their
  *               sum over the keys has to stay below 2^119.
  *               A row's results are bitwise the same whatever shares its call, and a prompt
  *               token's do not depend on how its prompt is cut into calls.
  *   Non-finite  A key or value that a token does not see leaves it untouched, whatever it
  *               holds: stale cache rows may hold infinities and NaN.  One that it sees counts
- *               as in the formula, an infinite value whose weight underflowed to zero as NaN.
+ *               as in the formula, an infinite value whose weight underflowed to zero as NaN,
+ *               a head of values with an infinite scale (the write makes none) as NaN too.
  */
 #ifndef GDN_ATTENTION_H
 #define GDN_ATTENTION_H

@@ -104,3 +104,25 @@ def test_infinities_that_are_seen(d, dtype, fmt):
             want = whole[start: start + per].float()
             got = decode(q[start: start + per].contiguous(), cache, table, start, scale).float()
             assert torch.equal(torch.isfinite(got), torch.isfinite(want)) and torch.equal(got.isnan(), want.isnan()), (start, per)
+
+
+@pytest.mark.parametrize("dtype,fmt", [(BF16, "e4m3"), (BF16, "int8"), (F32, "e4m3"), (F32, "int8")])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_infinite_scales(d, dtype, fmt):
+    """A head of values whose scale is infinite is NaN to the tokens that see it, in whatever call, and nothing to others."""
+    n, at = 200, 20
+    table, rows = C.pages([n], 16, DEV, 5)
+    own = C.owned_rows(table, 16, [n])
+    cache = C.filled_cache(rows, 2, d, dtype, fmt, own, DEV, 5)
+    q = C.queries(n, 4, d, dtype, DEV, 5)
+    clean = prefill(q, cache, table, 0, 0.1)
+    cache["v_scale"][own[at], 1] = math.inf
+    cache["v_cache"].view(torch.uint8)[own[at], 1, :5] = 0          # codes of zero among them
+    whole = prefill(q, cache, table, 0, 0.1)
+    assert torch.equal(whole[:at], clean[:at]) and torch.equal(whole[:, :2], clean[:, :2]) and whole[at:, 2:].isnan().all()
+    for a, b in ((0, 21), (19, 22), (21, 64), (64, 200), (70, 71), (130, 190)):
+        part = prefill(q[a:b], cache, table, a, 0.1)
+        assert torch.equal(part.nan_to_num(7.0), whole[a:b].nan_to_num(7.0)), (a, b)
+    for start, per in ((5, 1), (5, 40), (15, 10), (21, 1), (30, 50), (150, 33)):
+        got = decode(q[start: start + per].contiguous(), cache, table, start, 0.1)
+        assert torch.equal(got.isnan(), whole[start: start + per].isnan()), (start, per)
